@@ -19,6 +19,7 @@ There is no CPU fallback: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -33,6 +34,13 @@ __all__ = [
     "materialize_grouped",
     "chol_inverse_upper",
     "gptq_quantize",
+    "gated_ffn",
+    "gated_ffn_forward",
+    "gated_ffn_backward",
+    "distill_topk",
+    "distill_topk_forward",
+    "distill_topk_backward",
+    "distill_topk_step",
     "set_tile_override",
     "set_staging",
     "library_path",
@@ -114,6 +122,17 @@ def _load():
         "hess_gptq_quantize": (c_int, [vp, i64, i64, i64, vp, i64, vp, c_int, vp, i64, vp, i64, vp, vp, i64, vp,
                                        i64, vp]),
         "hess_chol_inverse_upper": (c_int, [vp, i64, i64, vp, i64, vp, i64, vp, vp]),
+        "hess_gated_ffn_workspace": (i64, [i64, i64, i64, c_int, c_int]),
+        "hess_gated_ffn_preact_cols": (i64, [i64]),
+        "hess_gated_ffn_forward": (c_int, [vp, i64, vp, i64, vp, i64, c_int, c_int, i64, i64, i64, vp, i64, vp, vp,
+                                           i64, vp]),
+        "hess_gated_ffn_backward": (c_int, [vp, i64, vp, i64, vp, i64, vp, i64, vp, c_int, c_int, i64, i64, i64, vp,
+                                            i64, vp, i64, vp, i64, vp, i64, vp]),
+        "hess_distill_topk_workspace": (i64, [i64, i64, c_int]),
+        "hess_distill_topk": (c_int, [vp, i64, c_int, i64, i64, vp, c_int, i64, vp, c_int, i64, c_int, vp,
+                                      ctypes.c_float, vp, vp, vp, i64, vp, i64, vp]),
+        "hess_distill_topk_backward": (c_int, [vp, vp, i64, c_int, i64, i64, vp, c_int, i64, vp, c_int, i64, c_int,
+                                               vp, ctypes.c_float, vp, vp, i64, vp]),
         "hess_imatrix_create": (vp, [i64, c_int]),
         "hess_imatrix_destroy": (c_int, [vp]),
         "hess_imatrix_add_batch": (c_int, [vp, vp, i64, i64, vp]),
@@ -527,3 +546,291 @@ def materialize_grouped(hessians, damp_percent: float = 0.01, outs=None, neutral
     _check(_load().hess_materialize_grouped(hs_arr, n, float(damp_percent), flags, h_arr, d_arr, p_arr,
                                             _stream(stream)))
     return [(outs[e], dead[e].view(torch.bool), damp[e]) for e in range(n)]
+
+
+# -- the gated feed-forward block -----------------------------------------------------------------
+
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+_CODES = {torch.bfloat16: HESS_BF16, torch.float32: HESS_F32, torch.float16: HESS_F16}
+
+
+def _on_stream(fn):
+    """Adds ``stream``: the call, its temporaries and its outputs belong to that stream instead of the current one."""
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    return call
+
+
+def _float_code(name: str, t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}; use torch.bfloat16, torch.float16 or torch.float32")
+    return code
+
+
+def _rows(t: torch.Tensor):
+    """(tensor, row stride) of a 2-D tensor whose rows are contiguous and do not overlap (copied if need be)."""
+    n, c = t.shape
+    s0, s1 = t.stride()
+    if (s1 != 1 and c > 1) or (n > 1 and s0 < c):
+        t = t.contiguous()
+        s0 = t.stride(0)
+    return t, (s0 if n > 1 else max(c, 1))
+
+
+def _out(name: str, out, shape, like: torch.Tensor) -> torch.Tensor:
+    """``out`` checked, or a new tensor: ``shape`` on like's device and of its dtype, rows contiguous."""
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if out.dtype != like.dtype or out.device != like.device or tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a {like.dtype} {tuple(shape)} tensor on {like.device}")
+    if out.dim() != 2 and not out.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if out.dim() == 2 and ((out.stride(1) != 1 and shape[1] > 1) or (shape[0] > 1 and out.stride(0) < shape[1])):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return out
+
+
+def _workspace(work, need: int, device):
+    """(pointer, bytes, tensor) of ``work`` if it is large enough, else of a new workspace."""
+    if need == 0:
+        return None, 0, None
+    if need < 0:
+        raise HessError(-1, _load().hess_last_error().decode(errors="replace"))
+    if work is None or work.numel() * work.element_size() < need:
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+    elif work.device != device or not work.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return work.data_ptr(), work.numel() * work.element_size(), work
+
+
+def _act_mode(act: str) -> int:
+    mode = _ACTS.get(act)
+    if mode is None:
+        raise ValueError(f"unknown activation {act!r}; use one of {sorted(_ACTS)}")
+    return mode
+
+
+def _ffn_args(x, w_gate, w_up):
+    code = _float_code("x", x)
+    if w_gate.dim() != 2 or w_gate.shape != w_up.shape:
+        raise ValueError("w_gate and w_up must be (f, d) matrices of one shape")
+    f, d = w_gate.shape
+    if x.dim() < 1 or x.shape[-1] != d:
+        raise ValueError(f"last dimension of x {tuple(x.shape)} != d = {d}")
+    for name, t in (("w_gate", w_gate), ("w_up", w_up)):
+        if t.dtype != x.dtype or t.device != x.device:
+            raise ValueError(f"{name} must have x's dtype and device")
+    x2, ldx = _rows(x.reshape(-1, d) if x.dim() != 2 else x)
+    wg, ldg = _rows(w_gate)
+    wu, ldu = _rows(w_up)
+    return code, x2, ldx, wg, ldg, wu, ldu, x2.shape[0], d, f
+
+
+@_on_stream
+def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu",
+                      save: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """``h = act(x w_gate^T) * (x w_up^T)`` for x (..., d) and weights (f, d); not recorded by autograd.
+
+    bfloat16, float16 or float32 throughout; ``act`` is ``"silu"``, ``"gelu"`` or ``"gelu_tanh"``.
+    With ``save`` returns ``(h, preact)``, preact being what gated_ffn_backward needs: the
+    (tokens, 2 f') pair of pre-activations, f' = f rounded up to a multiple of 8.
+    """
+    lib = _load()
+    mode = _act_mode(act)
+    code, x2, ldx, wg, ldg, wu, ldu, n, d, f = _ffn_args(x, w_gate, w_up)
+    h = _out("out", out, (*x.shape[:-1], f), x)
+    pre = None
+    if save:
+        pre = torch.empty((n, 2 * (-(-f // 8) * 8)), dtype=x.dtype, device=x.device)
+    if n > 0:
+        ldh = h.stride(0) if h.dim() == 2 and n > 1 else f
+        wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 0), x.device)
+        _check(lib.hess_gated_ffn_forward(x2.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu, code, mode, n,
+                                          d, f, h.data_ptr(), ldh, pre.data_ptr() if save else None, wp, wb,
+                                          _stream(None, x.device.index)))
+    return (h, pre) if save else h
+
+
+@_on_stream
+def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                       preact: torch.Tensor, act: str = "silu", need_x: bool = True, need_w: bool = True,
+                       workspace: torch.Tensor | None = None):
+    """``(dx, dw_gate, dw_up)`` for the gradient dh of gated_ffn_forward's h (entries not needed are None)."""
+    lib = _load()
+    mode = _act_mode(act)
+    code, x2, ldx, wg, ldg, wu, ldu, n, d, f = _ffn_args(x, w_gate, w_up)
+    if tuple(dh.shape) != (*x.shape[:-1], f) or dh.dtype != x.dtype or dh.device != x.device:
+        raise ValueError(f"dh must be a {x.dtype} {(*x.shape[:-1], f)} tensor on {x.device}")
+    cols = 2 * (-(-f // 8) * 8)
+    if tuple(preact.shape) != (n, cols) or preact.dtype != x.dtype or preact.device != x.device \
+            or not preact.is_contiguous():
+        raise ValueError(f"preact must be the contiguous {x.dtype} ({n}, {cols}) tensor gated_ffn_forward saved")
+    dh2, lddh = _rows(dh.reshape(-1, f) if dh.dim() != 2 else dh)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_x else None
+    dwg = torch.empty((f, d), dtype=x.dtype, device=x.device) if need_w else None
+    dwu = torch.empty((f, d), dtype=x.dtype, device=x.device) if need_w else None
+    wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 1), x.device)
+    _check(lib.hess_gated_ffn_backward(dh2.data_ptr() if n > 0 else None, lddh, x2.data_ptr() if n > 0 else None, ldx,
+                                       wg.data_ptr(), ldg, wu.data_ptr(), ldu, preact.data_ptr() if n > 0 else None,
+                                       code, mode, n, d, f, dx.data_ptr() if need_x and n > 0 else None, d,
+                                       dwg.data_ptr() if need_w else None, d, dwu.data_ptr() if need_w else None, d,
+                                       wp, wb, _stream(None, x.device.index)))
+    return dx, dwg, dwu
+
+
+class _GatedFfn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, act):
+        h, preact = gated_ffn_forward(x, w_gate, w_up, act=act, save=True)
+        ctx.save_for_backward(x, w_gate, w_up, preact)
+        ctx.act = act
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        x, w_gate, w_up, preact = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dwg, dwu = gated_ffn_backward(dh, x, w_gate, w_up, preact, act=ctx.act, need_x=need[0],
+                                          need_w=need[1] or need[2])
+        return dx, (dwg if need[1] else None), (dwu if need[2] else None), None
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu") -> torch.Tensor:
+    """gated_ffn_forward under autograd: the backward pass is gated_ffn_backward (once differentiable)."""
+    if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
+        return _GatedFfn.apply(x, w_gate, w_up, act)
+    return gated_ffn_forward(x, w_gate, w_up, act=act)
+
+
+# -- distillation from a teacher's top logits -----------------------------------------------------
+
+def _distill_args(logits, ids, values, weight, temperature):
+    code = _float_code("logits", logits)
+    if logits.dim() < 1:
+        raise ValueError("logits must be (..., vocab)")
+    lead, vocab = logits.shape[:-1], logits.shape[-1]
+    if ids.shape != values.shape or ids.shape[:-1] != lead or ids.dim() < 1:
+        raise ValueError("ids and values must be (..., k) with the leading dimensions of logits")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64")
+    vcode = _float_code("values", values)
+    for name, t in (("ids", ids), ("values", values)):
+        if t.device != logits.device:
+            raise ValueError(f"{name} must be on the device of logits")
+    k = ids.shape[-1]
+    z2, ldz = _rows(logits.reshape(-1, vocab) if logits.dim() != 2 else logits)
+    i2, ldi = _rows(ids.reshape(-1, k) if ids.dim() != 2 else ids)
+    v2, ldv = _rows(values.reshape(-1, k) if values.dim() != 2 else values)
+    n = z2.shape[0]
+    w = _row_floats("weight", weight, lead, logits.device)
+    return (z2, i2, v2, w), lead, n, vocab, (
+        z2.data_ptr(), ldz, code, n, vocab, i2.data_ptr(), 1 if ids.dtype == torch.int64 else 0, ldi, v2.data_ptr(),
+        vcode, ldv, k, w.data_ptr() if w is not None else None, float(temperature))
+
+
+def _row_floats(name, t, lead, device):
+    """A float32 value for each row, contiguous (a broadcast one is written out)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(lead) or t.dtype != torch.float32 or t.device != device:
+        raise ValueError(f"{name} must be a float32 {tuple(lead)} tensor on {device}")
+    return t.contiguous()
+
+
+def _grad_out(out, logits):
+    grad = _out("out", out, logits.shape, logits)
+    return grad, (grad.stride(0) if grad.dim() == 2 and grad.shape[0] > 1 else logits.shape[-1])
+
+
+def _distill_call(logits, ids, values, weight, temperature, want_stats, want_grad, out, workspace):
+    lib = _load()
+    keep, lead, n, vocab, args = _distill_args(logits, ids, values, weight, temperature)
+    dev = logits.device
+    loss = torch.empty(lead, dtype=torch.float32, device=dev)
+    stats = torch.empty((*lead, 2), dtype=torch.float32, device=dev) if want_stats else None
+    grad, ldg = _grad_out(out, logits) if want_grad else (None, 0)
+    wp, wb, work = _workspace(workspace, lib.hess_distill_topk_workspace(n, vocab, args[2]), dev)
+    _check(lib.hess_distill_topk(*args, loss.data_ptr(), stats.data_ptr() if want_stats else None,
+                                 grad.data_ptr() if want_grad else None, ldg, wp, wb, _stream(None, dev.index)))
+    return loss, stats, grad
+
+
+@_on_stream
+def distill_topk_forward(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
+                         weight: torch.Tensor | None = None, temperature: float = 1.0,
+                         workspace: torch.Tensor | None = None):
+    """``(loss, stats)``: each row's divergence from the teacher's top entries, and what the backward pass needs.
+
+    logits (..., vocab) bfloat16, float16 or float32; ids (..., k) int32 or int64 (negative: absent);
+    values (..., k) the teacher's logits there; weight (...) float32, 0 for rows to leave out.  loss (...)
+    and stats (..., 2), the maximum of logits / temperature and the sum of exponentials above it, are float32.
+    """
+    return _distill_call(logits, ids, values, weight, temperature, True, False, None, workspace)[:2]
+
+
+@_on_stream
+def distill_topk_step(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
+                      weight: torch.Tensor | None = None, temperature: float = 1.0, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None):
+    """``(loss, dlogits)`` in one call: each row's loss and the gradient of their sum (``out`` may be logits)."""
+    loss, _, grad = _distill_call(logits, ids, values, weight, temperature, False, True, out, workspace)
+    return loss, grad
+
+
+@_on_stream
+def distill_topk_backward(dloss: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
+                          stats: torch.Tensor, weight: torch.Tensor | None = None, temperature: float = 1.0,
+                          out: torch.Tensor | None = None) -> torch.Tensor:
+    """dlogits for the gradient dloss of distill_topk_forward's loss (``out`` may be logits)."""
+    lib = _load()
+    keep, lead, n, vocab, args = _distill_args(logits, ids, values, weight, temperature)
+    dl = _row_floats("dloss", dloss, lead, logits.device)
+    if tuple(stats.shape) != (*lead, 2) or stats.dtype != torch.float32 or stats.device != logits.device \
+            or not stats.is_contiguous():
+        raise ValueError(f"stats must be the contiguous float32 {(*lead, 2)} tensor distill_topk_forward returned")
+    grad, ldg = _grad_out(out, logits)
+    _check(lib.hess_distill_topk_backward(dl.data_ptr(), *args, stats.data_ptr(), grad.data_ptr(), ldg,
+                                          _stream(None, logits.device.index)))
+    return grad
+
+
+class _DistillTopk(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, values, weight, temperature):
+        loss, stats = distill_topk_forward(logits, ids, values, weight=weight, temperature=temperature)
+        ctx.save_for_backward(logits, ids, values, weight, stats)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        logits, ids, values, weight, stats = ctx.saved_tensors
+        return distill_topk_backward(dloss, logits, ids, values, stats, weight=weight,
+                                     temperature=ctx.temperature), None, None, None, None
+
+
+def distill_topk(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, weight: torch.Tensor | None = None,
+                 temperature: float = 1.0) -> torch.Tensor:
+    """Each row's loss under autograd (gradient for logits only, once differentiable).
+
+    ``values`` and ``weight`` are constants of the loss: an error is raised if they require a gradient.
+    """
+    if torch.is_grad_enabled():
+        if values.requires_grad or (weight is not None and weight.requires_grad):
+            raise ValueError("values and weight are constants of the loss: detach them")
+        if logits.requires_grad:
+            return _DistillTopk.apply(logits, ids, values, weight, float(temperature))
+    return distill_topk_forward(logits, ids, values, weight=weight, temperature=temperature)[0]

@@ -1,0 +1,57 @@
+// Internal interface of the gated feed-forward block: the three products it
+// consists of, their tile schedule, and the launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hess {
+
+enum FfnMode {
+  kFfnFwd = 0,  // h = act(x Wg^T) * (x Wu^T)          M = n, N = f (half a tile's columns each), K = d
+  kFfnDx = 1,   // dx = dg Wg + du Wu                   M = n, N = d, K = f, two segments
+  kFfnDw = 2,   // [dWg; dWu] = [dg du]^T x             M = 2 fp, N = d, K = n
+};
+
+// One product.  The pre-activation pair g, u and its gradient dg, du are kept
+// as one n x 2 fp matrix (fp = f rounded up to 8, columns f .. fp - 1 zero):
+// g or dg in the first fp columns, u or du in the last.
+struct FfnGemm {
+  const void* a;   // fwd: x (n x d); dx and dw: the n x 2 fp gradient pair
+  int64_t lda;
+  const void* b0;  // fwd and dx: Wg (f x d); dw: x (n x d)
+  int64_t ldb0;
+  const void* b1;  // fwd and dx: Wu
+  int64_t ldb1;
+  void* o0;        // fwd: h; dx: dx; dw: dWg
+  int64_t ldo0;
+  void* o1;        // fwd: the pre-activation pair, row stride 2 fp, or null; dw: dWu
+  int64_t ldo1;
+  float* ws;       // partial tiles of the split items
+  int64_t M, N, K;
+  int64_t f, fp;
+  int act;
+  int vec_out;     // 4 consecutive outputs may be stored as one (fwd's o1 always may)
+  // schedule: tiles 0 .. full - 1 of the blocked order are done whole; each of
+  // the others is cut into `parts` ranges of part_len K-iterations, whose
+  // partial sums go to workspace slot part * (ntiles - full) + (tile - full)
+  int tm, tn, ntiles, full, parts, part_len, niter;
+};
+
+// Edges of the two tile kernels and their K step.
+constexpr int kFfnEdge = 128, kFfnStep = 16;
+
+// Fills the schedule for tiles of the given edge.  max_slots: workspace slots.
+void ffn_schedule(FfnGemm& g, int mode, int edge, int step, int max_slots);
+constexpr int kFfnMaxSlots = 256;
+
+hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int dtype, hipStream_t stream);
+
+// dg = dh u act'(g), du = dh act(g) into the n x 2 fp pair dgu (columns past f zero).
+hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f,
+                          int64_t fp, int act, int dtype, hipStream_t stream);
+
+// Zeros rows x cols elements of esize bytes at p (row stride ld elements).
+hipError_t launch_zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int esize, hipStream_t stream);
+
+}  // namespace hess

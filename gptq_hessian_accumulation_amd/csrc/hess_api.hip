@@ -22,6 +22,29 @@
 #include "../../include/hess.h"
 #include "hess_internal.hpp"
 
+namespace hess {
+namespace {
+thread_local char g_err[512] = "";
+}
+
+int fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int hip_fail(hipError_t e, const char* what) {
+  return fail(HESS_EHIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
+}
+}  // namespace hess
+
 using namespace hess;
 
 struct hess_s {
@@ -127,8 +150,6 @@ struct LocalScratch {
 };
 LocalScratch g_local[kMaxDevices];
 
-thread_local char g_err[512] = "";
-
 using HLock = std::lock_guard<std::recursive_mutex>;
 
 // The locks of several handles, taken in address order (so that two calls
@@ -149,18 +170,6 @@ int64_t g_group_chunk = 0; // test hook: cap on the gathered bytes per grouped l
 bool g_group_direct = true; // grouped 256-tile updates read the routed rows in place when X's size is known
 bool g_staging = true;    // thin-batch staging enabled (process-wide)
 bool g_async = true;      // asynchronous flushes for handles created from now on (process-wide)
-
-int fail(int code, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof(g_err), fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-int hip_fail(hipError_t e, const char* what) {
-  return fail(HESS_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
 
 // Order this call after the handle's previous call when the stream changes.
 int order_stream(hess_t h, hipStream_t s) {
@@ -1308,13 +1317,6 @@ int64_t hess_gptq_quantize_workspace(int64_t rows, int64_t cols) {
   if (rows < 1 || rows > kQuantMaxDim || cols < 1 || cols > kQuantMaxDim) return -1;
   return quant_workspace_doubles(rows, cols) * (int64_t)sizeof(double);
 }
-
-namespace {
-bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
-}
-}  // namespace
 
 int hess_gptq_quantize(const float* W, int64_t rows, int64_t cols, int64_t ldw, const float* U, int64_t ldu,
                        const uint8_t* dead, int group_size, float* Q, int64_t ldq, uint8_t* codes, int64_t ldc,

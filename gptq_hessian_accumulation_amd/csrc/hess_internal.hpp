@@ -8,6 +8,13 @@ namespace hess {
 
 constexpr int kInBF16 = 0;  // == HESS_BF16
 constexpr int kInF32 = 1;   // == HESS_F32
+constexpr int kInF16 = 2;   // == HESS_F16
+
+// Set the calling thread's error message (hess_last_error) and return code.
+int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int hip_fail(hipError_t e, const char* what);
+// Whether the byte ranges [a, a + abytes) and [b, b + bbytes) meet.
+bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes);
 
 constexpr int kMaxGroups = 64;  // Hessians per grouped launch
 

@@ -1,0 +1,360 @@
+// C ABI of the gated feed-forward block and the top-logit distillation loss
+// (declared in include/hess.h): argument checks, workspace layout, dispatch.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/hess.h"
+#include "distill_internal.hpp"
+#include "ffn_internal.hpp"
+#include "hess_internal.hpp"
+
+using namespace hess;
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t)1 << 24;
+constexpr int64_t kMaxWidth = (int64_t)1 << 17;
+constexpr int64_t kMaxStride = (int64_t)1 << 20;
+constexpr int64_t kMaxVocab = (int64_t)1 << 28;
+constexpr int kMaxTop = 1024;
+
+bool dtype_ok(int t) { return t == HESS_BF16 || t == HESS_F32 || t == HESS_F16; }
+int64_t elem_bytes(int t) { return t == HESS_F32 ? 4 : 2; }
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)a == 0; }
+
+// A matrix argument: rows x cols at p with row stride ld elements.
+struct Mat {
+  const char* name;
+  const void* p;
+  int64_t ld, rows, cols;
+  int64_t bytes(int64_t es) const { return rows > 0 ? ((rows - 1) * ld + cols) * es : 0; }
+};
+
+int check_mat(const Mat& m, int64_t es) {
+  if (!m.p) return fail(HESS_EINVAL, "null %s", m.name);
+  if (m.ld < m.cols || m.ld > kMaxStride)
+    return fail(HESS_EINVAL, "row stride %lld of %s outside [%lld, %lld]", (long long)m.ld, m.name, (long long)m.cols,
+                (long long)kMaxStride);
+  if (!aligned(m.p, es)) return fail(HESS_EALIGN, "%s not aligned to its element size", m.name);
+  return HESS_OK;
+}
+
+// No output may meet another output or an input.
+int check_outputs(const Mat* outs, int no, const Mat* ins, int ni, int64_t es, const void* work, int64_t wbytes) {
+  for (int a = 0; a < no; ++a) {
+    if (!outs[a].p) continue;
+    for (int b = 0; b < ni; ++b)
+      if (ins[b].p && overlaps(outs[a].p, outs[a].bytes(es), ins[b].p, ins[b].bytes(es)))
+        return fail(HESS_EINVAL, "%s overlaps %s", outs[a].name, ins[b].name);
+    for (int b = a + 1; b < no; ++b)
+      if (outs[b].p && overlaps(outs[a].p, outs[a].bytes(es), outs[b].p, outs[b].bytes(es)))
+        return fail(HESS_EINVAL, "%s overlaps %s", outs[a].name, outs[b].name);
+    if (wbytes > 0 && overlaps(outs[a].p, outs[a].bytes(es), work, wbytes))
+      return fail(HESS_EINVAL, "%s overlaps the workspace", outs[a].name);
+  }
+  for (int b = 0; b < ni; ++b)
+    if (wbytes > 0 && ins[b].p && overlaps(ins[b].p, ins[b].bytes(es), work, wbytes))
+      return fail(HESS_EINVAL, "%s overlaps the workspace", ins[b].name);
+  return HESS_OK;
+}
+
+int check_ffn_sizes(int64_t n, int64_t d, int64_t f, int dtype) {
+  if (!dtype_ok(dtype)) return fail(HESS_EINVAL, "unknown dtype %d", dtype);
+  if (n < 0 || n > kMaxRows) return fail(HESS_EINVAL, "n = %lld outside [0, 2^24]", (long long)n);
+  if (d < 1 || d > kMaxWidth || f < 1 || f > kMaxWidth)
+    return fail(HESS_EINVAL, "d = %lld, f = %lld outside [1, 2^17]", (long long)d, (long long)f);
+  return HESS_OK;
+}
+
+int check_work(const void* work, int64_t have, int64_t need) {
+  if (need == 0) return HESS_OK;
+  if (!work) return fail(HESS_EINVAL, "null workspace");
+  if (!aligned(work, 16)) return fail(HESS_EALIGN, "workspace not 16-byte aligned");
+  if (have < need)
+    return fail(HESS_EINVAL, "workspace of %lld bytes, %lld needed", (long long)have, (long long)need);
+  return HESS_OK;
+}
+
+// Bytes of partial tiles one product needs.
+int64_t slot_bytes(FfnGemm g, int mode) {
+  ffn_schedule(g, mode, kFfnEdge, kFfnStep, kFfnMaxSlots);
+  return (int64_t)(g.ntiles - g.full) * g.parts * kFfnEdge * kFfnEdge * 4;
+}
+
+FfnGemm shape(int64_t M, int64_t N, int64_t K) {
+  FfnGemm g{};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  return g;
+}
+
+int64_t forward_slots(int64_t n, int64_t d, int64_t f) { return slot_bytes(shape(n, f, d), kFfnFwd); }
+int64_t backward_slots(int64_t n, int64_t d, int64_t f) {
+  return std::max(slot_bytes(shape(n, d, f), kFfnDx), slot_bytes(shape(2 * up(f, 8), d, n), kFfnDw));
+}
+
+// Four consecutive outputs may be stored together.
+int vec_rows(const void* p, int64_t ld, int64_t es) { return aligned(p, 4 * es) && ld % 4 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t hess_gated_ffn_preact_cols(int64_t f) {
+  if (f < 1 || f > kMaxWidth) {
+    fail(HESS_EINVAL, "f = %lld outside [1, 2^17]", (long long)f);
+    return -1;
+  }
+  return 2 * up(f, 8);
+}
+
+int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int backward) {
+  if (check_ffn_sizes(n, d, f, dtype) != HESS_OK) return -1;
+  if (n == 0) return 0;
+  if (!backward) return forward_slots(n, d, f);
+  return up(n * 2 * up(f, 8) * elem_bytes(dtype), 256) + backward_slots(n, d, f);
+}
+
+int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64_t ldg, const void* w_up, int64_t ldu,
+                           int dtype, int act, int64_t n, int64_t d, int64_t f, void* h, int64_t ldh, void* preact,
+                           void* work, int64_t work_bytes, hess_stream_t stream) {
+  if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
+  if (act < HESS_SILU || act > HESS_GELU_TANH) return fail(HESS_EINVAL, "unknown activation %d", act);
+  if (n == 0) return HESS_OK;
+  const int64_t es = elem_bytes(dtype), fp = up(f, 8);
+  const Mat ins[3] = {{"x", x, ldx, n, d}, {"w_gate", w_gate, ldg, f, d}, {"w_up", w_up, ldu, f, d}};
+  const Mat outs[2] = {{"h", h, ldh, n, f}, {"preact", preact, 2 * fp, n, 2 * fp}};
+  for (const Mat& m : ins)
+    if (int rc = check_mat(m, es)) return rc;
+  if (int rc = check_mat(outs[0], es)) return rc;
+  if (!aligned(preact, 16)) return fail(HESS_EALIGN, "preact not 16-byte aligned");
+  const int64_t need = hess_gated_ffn_workspace(n, d, f, dtype, 0);
+  if (int rc = check_work(work, work_bytes, need)) return rc;
+  if (int rc = check_outputs(outs, 2, ins, 3, es, work, need)) return rc;
+
+  FfnGemm g = shape(n, f, d);
+  g.a = x;
+  g.lda = ldx;
+  g.b0 = w_gate;
+  g.ldb0 = ldg;
+  g.b1 = w_up;
+  g.ldb1 = ldu;
+  g.o0 = h;
+  g.ldo0 = ldh;
+  g.o1 = preact;
+  g.ldo1 = 2 * fp;
+  g.ws = static_cast<float*>(work);
+  g.f = f;
+  g.fp = fp;
+  g.act = act;
+  g.vec_out = vec_rows(h, ldh, es);
+  ffn_schedule(g, kFfnFwd, kFfnEdge, kFfnStep, kFfnMaxSlots);
+  const hipError_t e = launch_ffn_gemm(g, kFfnFwd, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HESS_OK : hip_fail(e, "gated feed-forward launch");
+}
+
+int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t ldx, const void* w_gate, int64_t ldg,
+                            const void* w_up, int64_t ldu, const void* preact, int dtype, int act, int64_t n,
+                            int64_t d, int64_t f, void* dx, int64_t lddx, void* dw_gate, int64_t lddg, void* dw_up,
+                            int64_t lddu, void* work, int64_t work_bytes, hess_stream_t stream) {
+  if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
+  if (act < HESS_SILU || act > HESS_GELU_TANH) return fail(HESS_EINVAL, "unknown activation %d", act);
+  if (!dw_gate != !dw_up) return fail(HESS_EINVAL, "dw_gate and dw_up: both or neither");
+  const int64_t es = elem_bytes(dtype), fp = up(f, 8);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Mat ins[5] = {{"dh", dh, lddh, n, f},
+                      {"x", x, ldx, n, d},
+                      {"w_gate", w_gate, ldg, f, d},
+                      {"w_up", w_up, ldu, f, d},
+                      {"preact", preact, 2 * fp, n, 2 * fp}};
+  const Mat outs[3] = {{"dx", dx, lddx, n, d}, {"dw_gate", dw_gate, lddg, f, d}, {"dw_up", dw_up, lddu, f, d}};
+  for (const Mat& m : ins) {
+    if (n == 0 && m.rows == 0) continue;
+    if (int rc = check_mat(m, es)) return rc;
+  }
+  for (const Mat& m : outs)
+    if (m.p && m.rows > 0)
+      if (int rc = check_mat(m, es)) return rc;
+  if (!aligned(preact, 16)) return fail(HESS_EALIGN, "preact not 16-byte aligned");
+  const int64_t need = hess_gated_ffn_workspace(n, d, f, dtype, 1);
+  if (int rc = check_work(work, work_bytes, need)) return rc;
+  if (int rc = check_outputs(outs, 3, ins, 5, es, work, need)) return rc;
+  hipError_t e = hipSuccess;
+  if (n == 0) {
+    if (dw_gate) {
+      e = launch_zero_rows(dw_gate, lddg, f, d, (int)es, s);
+      if (e == hipSuccess) e = launch_zero_rows(dw_up, lddu, f, d, (int)es, s);
+    }
+    return e == hipSuccess ? HESS_OK : hip_fail(e, "gradient clear launch");
+  }
+  if (!dx && !dw_gate) return HESS_OK;
+
+  char* dgu = static_cast<char*>(work);
+  float* slots = reinterpret_cast<float*>(dgu + up(n * 2 * fp * es, 256));
+  e = launch_ffn_dgu(dh, lddh, preact, dgu, n, f, fp, act, dtype, s);
+  if (e != hipSuccess) return hip_fail(e, "gate gradient launch");
+  if (dx) {
+    FfnGemm g = shape(n, d, f);
+    g.a = dgu;
+    g.lda = 2 * fp;
+    g.b0 = w_gate;
+    g.ldb0 = ldg;
+    g.b1 = w_up;
+    g.ldb1 = ldu;
+    g.o0 = dx;
+    g.ldo0 = lddx;
+    g.ws = slots;
+    g.f = f;
+    g.fp = fp;
+    g.vec_out = vec_rows(dx, lddx, es);
+    ffn_schedule(g, kFfnDx, kFfnEdge, kFfnStep, kFfnMaxSlots);
+    e = launch_ffn_gemm(g, kFfnDx, dtype, s);
+    if (e != hipSuccess) return hip_fail(e, "input gradient launch");
+  }
+  if (dw_gate) {
+    FfnGemm g = shape(2 * fp, d, n);
+    g.a = dgu;
+    g.lda = 2 * fp;
+    g.b0 = x;
+    g.ldb0 = ldx;
+    g.o0 = dw_gate;
+    g.ldo0 = lddg;
+    g.o1 = dw_up;
+    g.ldo1 = lddu;
+    g.ws = slots;
+    g.f = f;
+    g.fp = fp;
+    g.vec_out = vec_rows(dw_gate, lddg, es) && vec_rows(dw_up, lddu, es);
+    ffn_schedule(g, kFfnDw, kFfnEdge, kFfnStep, kFfnMaxSlots);
+    e = launch_ffn_gemm(g, kFfnDw, dtype, s);
+    if (e != hipSuccess) return hip_fail(e, "weight gradient launch");
+  }
+  return HESS_OK;
+}
+
+int64_t hess_distill_topk_workspace(int64_t n, int64_t vocab, int dtype) {
+  if (!dtype_ok(dtype) || n < 0 || n > kMaxRows || vocab < 1 || vocab > kMaxVocab) {
+    fail(HESS_EINVAL, "bad dtype, or n = %lld outside [0, 2^24], or vocab = %lld outside [1, 2^28]", (long long)n,
+         (long long)vocab);
+    return -1;
+  }
+  return distill_workspace(n, vocab, dtype);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_distill(const DistillParams& P, int dtype, int values_dtype) {
+  if (!dtype_ok(dtype) || !dtype_ok(values_dtype))
+    return fail(HESS_EINVAL, "unknown dtype %d or values_dtype %d", dtype, values_dtype);
+  if (P.n < 0 || P.n > kMaxRows) return fail(HESS_EINVAL, "n = %lld outside [0, 2^24]", (long long)P.n);
+  if (P.vocab < 1 || P.vocab > kMaxVocab)
+    return fail(HESS_EINVAL, "vocab = %lld outside [1, 2^28]", (long long)P.vocab);
+  if (P.k < 1 || P.k > kMaxTop) return fail(HESS_EINVAL, "k = %d outside [1, %d]", P.k, kMaxTop);
+  if (!(P.temperature > 0.0f) || !std::isfinite(P.temperature))
+    return fail(HESS_EINVAL, "temperature %g not positive and finite", (double)P.temperature);
+  if (P.n == 0) return HESS_OK;
+  if (!P.z || !P.ids || !P.values) return fail(HESS_EINVAL, "null logits, ids or values");
+  const int64_t es = elem_bytes(dtype);
+  const int64_t widest = (int64_t)1 << 30;
+  if (P.ldz < P.vocab || P.ldz > widest || P.ldi < P.k || P.ldi > widest || P.ldv < P.k || P.ldv > widest)
+    return fail(HESS_EINVAL, "a row stride is below its row length or above 2^30");
+  if (!aligned(P.z, es) || !aligned(P.ids, P.ids64 ? 8 : 4) || !aligned(P.values, elem_bytes(values_dtype)))
+    return fail(HESS_EALIGN, "logits, ids or values not aligned to the element size");
+  if (!aligned(P.weight, 4)) return fail(HESS_EALIGN, "weight not float-aligned");
+  if (P.dz) {
+    if (P.lddz < P.vocab || P.lddz > widest) return fail(HESS_EINVAL, "row stride of dlogits below vocab or above 2^30");
+    if (!aligned(P.dz, es)) return fail(HESS_EALIGN, "dlogits not aligned to its element size");
+  }
+  return HESS_OK;
+}
+
+struct Span {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+
+// The outputs must not meet the inputs or one another; dlogits may be logits.
+// extra: further outputs (and the workspace), or with extra_in further inputs.
+int check_distill_overlap(const DistillParams& P, int dtype, int values_dtype, const Span* extra, int nextra,
+                          bool extra_in) {
+  const int64_t es = elem_bytes(dtype);
+  auto rows = [&](int64_t ld, int64_t cols, int64_t e) { return ((P.n - 1) * ld + cols) * e; };
+  const Span ins[4] = {{"logits", P.z, rows(P.ldz, P.vocab, es)},
+                       {"ids", P.ids, rows(P.ldi, P.k, P.ids64 ? 8 : 4)},
+                       {"values", P.values, rows(P.ldv, P.k, elem_bytes(values_dtype))},
+                       {"weight", P.weight, P.weight ? P.n * 4 : 0}};
+  const Span dz{"dlogits", P.dz, P.dz ? rows(P.lddz, P.vocab, es) : 0};
+  auto meet = [](const Span& a, const Span& b) {
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && overlaps(a.p, a.bytes, b.p, b.bytes);
+  };
+  for (int i = 0; i < 4; ++i) {
+    if (meet(dz, ins[i]) && !(i == 0 && P.dz == P.z && P.lddz == P.ldz))
+      return fail(HESS_EINVAL, "dlogits overlaps %s", ins[i].name);
+    for (int j = 0; j < nextra && !extra_in; ++j)
+      if (meet(extra[j], ins[i])) return fail(HESS_EINVAL, "%s overlaps %s", extra[j].name, ins[i].name);
+  }
+  for (int j = 0; j < nextra; ++j) {
+    if (meet(dz, extra[j])) return fail(HESS_EINVAL, "dlogits overlaps %s", extra[j].name);
+    for (int i = j + 1; i < nextra && !extra_in; ++i)
+      if (meet(extra[i], extra[j])) return fail(HESS_EINVAL, "%s overlaps %s", extra[i].name, extra[j].name);
+  }
+  return HESS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hess_distill_topk(const void* logits, int64_t ldz, int dtype, int64_t n, int64_t vocab, const void* ids, int ids64,
+                      int64_t ldi, const void* values, int values_dtype, int64_t ldv, int k, const float* weight,
+                      float temperature, float* loss, float* stats, void* dlogits, int64_t lddz, void* work,
+                      int64_t work_bytes, hess_stream_t stream) {
+  DistillParams P{};
+  P.z = logits, P.ldz = ldz, P.n = n, P.vocab = vocab;
+  P.ids = ids, P.ids64 = ids64 != 0, P.ldi = ldi;
+  P.values = values, P.values_dtype = values_dtype, P.ldv = ldv, P.k = k;
+  P.weight = weight, P.temperature = temperature;
+  P.loss = loss, P.stats = stats, P.dz = dlogits, P.lddz = lddz;
+  if (int rc = check_distill(P, dtype, values_dtype)) return rc;
+  if (n == 0) return HESS_OK;
+  if (!loss) return fail(HESS_EINVAL, "null loss");
+  if (!aligned(loss, 4) || !aligned(stats, 4)) return fail(HESS_EALIGN, "loss or stats not aligned");
+  const int64_t need = distill_workspace(n, vocab, dtype);
+  if (int rc = check_work(work, work_bytes, need)) return rc;
+  const Span extra[3] = {{"loss", loss, n * 4}, {"stats", stats, stats ? n * 8 : 0}, {"the workspace", work, need}};
+  if (int rc = check_distill_overlap(P, dtype, values_dtype, extra, 3, false)) return rc;
+  P.work = work;
+  const hipError_t e = launch_distill(P, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HESS_OK : hip_fail(e, "distillation loss launch");
+}
+
+int hess_distill_topk_backward(const float* dloss, const void* logits, int64_t ldz, int dtype, int64_t n,
+                               int64_t vocab, const void* ids, int ids64, int64_t ldi, const void* values,
+                               int values_dtype, int64_t ldv, int k, const float* weight, float temperature,
+                               const float* stats, void* dlogits, int64_t lddz, hess_stream_t stream) {
+  DistillParams P{};
+  P.z = logits, P.ldz = ldz, P.n = n, P.vocab = vocab;
+  P.ids = ids, P.ids64 = ids64 != 0, P.ldi = ldi;
+  P.values = values, P.values_dtype = values_dtype, P.ldv = ldv, P.k = k;
+  P.weight = weight, P.temperature = temperature;
+  P.dloss = dloss, P.stats = const_cast<float*>(stats), P.dz = dlogits, P.lddz = lddz;
+  if (int rc = check_distill(P, dtype, values_dtype)) return rc;
+  if (n == 0) return HESS_OK;
+  if (!dloss || !stats || !dlogits) return fail(HESS_EINVAL, "null dloss, stats or dlogits");
+  if (!aligned(dloss, 4) || !aligned(stats, 4)) return fail(HESS_EALIGN, "dloss or stats not aligned");
+  const Span extra[2] = {{"dloss", dloss, n * 4}, {"stats", stats, n * 8}};
+  if (int rc = check_distill_overlap(P, dtype, values_dtype, extra, 2, true)) return rc;
+  const hipError_t e = launch_distill_backward(P, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HESS_OK : hip_fail(e, "distillation gradient launch");
+}
+
+}  // extern "C"

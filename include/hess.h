@@ -534,6 +534,127 @@ int hess_imatrix_read(hess_imx_t m, float* out, int64_t* n_out, hess_stream_t st
 int hess_imatrix_reset(hess_imx_t m, hess_stream_t stream);
 int hess_imatrix_destroy(hess_imx_t m);
 
+/*
+ * Gated feed-forward block -- the two input projections of a transformer
+ * layer's feed-forward part, their activation and product:
+ *
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u
+ *
+ * h is the input of the layer's down projection: during calibration it is
+ * what hess_add_batch accumulates for that projection; after quantization the
+ * backward pass tunes the block (or what lies below it).
+ *
+ * act: HESS_SILU g sigmoid(g); HESS_GELU g Phi(g) with the normal cumulative
+ * Phi; HESS_GELU_TANH its tanh form,
+ * 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).
+ *
+ * Shapes and types: x n x d, w_gate and w_up f x d (two row ranges of one
+ * packed 2f x d matrix serve as well), h and dh n x f, all row-major with row
+ * strides in elements, all of one dtype (HESS_BF16, HESS_F16 or HESS_F32).
+ * n >= 0 up to 2^24, 1 <= d, f <= 2^17, strides up to 2^20.  Products are
+ * exact in float32 and summed in float32 (float32 inputs: rounded to float32
+ * once per product); g and u stay in float32 up to h, which is rounded once,
+ * to nearest even.  Any element alignment and stride is accepted; 16-bit
+ * operands whose rows are not 16-byte aligned, or whose width is not a
+ * multiple of 8, are first copied to padded rows in the workspace.
+ *
+ * Workspace: hess_gated_ffn_workspace(n, d, f, dtype, backward) bytes of
+ * device memory, 16-byte aligned, for the forward (backward = 0) or the
+ * backward call; -1 for bad arguments.  No call allocates or synchronizes:
+ * they may be captured into a HIP graph.  The workspace must not be shared by
+ * calls that may overlap (two streams).
+ */
+enum hess_act { HESS_SILU = 0, HESS_GELU = 1, HESS_GELU_TANH = 2 };
+
+int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int backward);
+
+/* Elements per row of the pre-activation pair a backward pass needs: 2 fp
+ * with fp = f rounded up to a multiple of 8 (g in columns 0 .. f - 1, u in
+ * fp .. fp + f - 1); -1 for bad f. */
+int64_t hess_gated_ffn_preact_cols(int64_t f);
+
+/*
+ * hess_gated_ffn_forward -- h from x, w_gate and w_up.
+ *   preact    device, n x hess_gated_ffn_preact_cols(f) of dtype, contiguous,
+ *             16-byte aligned: receives g and u, each rounded once; NULL when
+ *             no backward pass follows (nothing is written then).
+ * h and preact must not overlap each other, an input or the workspace.
+ * Errors: EINVAL, EALIGN (element, preact or workspace alignment), EHIP.
+ * n = 0 is a no-op.
+ */
+int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64_t ldg, const void* w_up, int64_t ldu,
+                           int dtype, int act, int64_t n, int64_t d, int64_t f, void* h, int64_t ldh, void* preact,
+                           void* work, int64_t work_bytes, hess_stream_t stream);
+
+/*
+ * hess_gated_ffn_backward -- the gradients of sum(dh * h):
+ *   dg = dh u act'(g), du = dh act(g),
+ *   dx = dg Wg + du Wu (n x d), dw_gate = dg^T x, dw_up = du^T x (f x d).
+ *   preact    as the forward call wrote it (unchanged by this call).
+ *   dx        or NULL: not wanted.
+ *   dw_gate, dw_up  both, or both NULL: not wanted.
+ * Outputs are of dtype and are overwritten.  For 16-bit types dg and du are
+ * rounded to dtype before the products (the matrix instructions take 16-bit
+ * operands), the sums are float32.  n = 0: dw_gate and dw_up become zero.
+ * Errors as the forward call.
+ */
+int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t ldx, const void* w_gate, int64_t ldg,
+                            const void* w_up, int64_t ldu, const void* preact, int dtype, int act, int64_t n,
+                            int64_t d, int64_t f, void* dx, int64_t lddx, void* dw_gate, int64_t lddg, void* dw_up,
+                            int64_t lddu, void* work, int64_t work_bytes, hess_stream_t stream);
+
+/*
+ * Distillation from a teacher's top logits -- for each row (token) the
+ * divergence of the student from the teacher's k highest logits, the usual
+ * measure of what quantization cost a model and the loss to mend it with:
+ *
+ *   p = softmax(values / T) over the row's present entries
+ *   q = softmax(logits / T) over the whole vocabulary
+ *   loss = weight * sum_i p_i (log p_i - log q[ids_i])
+ *   dlogits_j = dloss * weight / T * (q_j - sum over present i with ids_i = j of p_i)
+ *
+ *   logits    n x vocab of dtype (HESS_BF16, HESS_F16, HESS_F32), row stride
+ *             ldz; any element alignment.
+ *   ids       n x k, row stride ldi; int32, or int64 with ids64 nonzero.  A
+ *             negative id marks an absent entry (lists shorter than k); an id
+ *             >= vocab makes the row's loss and gradient NaN.  Repeated ids
+ *             add their probabilities.
+ *   values    n x k teacher logits (or log-probabilities) of values_dtype,
+ *             row stride ldv; not read where the entry is absent.  A value
+ *             of -infinity makes the entry absent too.
+ *   weight    n floats, or NULL for ones.  A row of weight 0, or without a
+ *             present entry, has loss 0 and a zero gradient whatever its
+ *             logits hold (they are not read).
+ *   T         temperature, > 0 and finite.  The loss is not multiplied by T^2.
+ * Limits: 0 <= n <= 2^24, 1 <= vocab <= 2^28, 1 <= k <= 1024.  Exponentials
+ * and sums are float32, the k terms of the loss float64.
+ *
+ * hess_distill_topk -- loss, and optionally the row statistics for a later
+ * backward call and the gradient with dloss = 1, in one call.
+ *   loss      n floats.
+ *   stats     n x 2 floats, or NULL: the maximum of logits / T over the row and
+ *             the sum of exp(logits / T - maximum); zeros for rows not read.
+ *             (A pair, because their log-sum-exp alone would lose the sum
+ *             where every logit is the type's lowest value.)
+ *   dlogits   n x vocab of dtype, row stride lddz, or NULL.  May be logits
+ *             itself (same stride); must not overlap it otherwise.
+ *   work      hess_distill_topk_workspace(n, vocab, dtype) bytes, 16-byte
+ *             aligned, not shared by calls that may overlap.
+ * hess_distill_topk_backward -- dlogits from dloss (n floats) and stats.
+ * Errors: EINVAL, EALIGN, EHIP.  n = 0 is a no-op.  Neither call allocates or
+ * synchronizes: both may be captured into a HIP graph.  The same call gives
+ * the same bits every time.
+ */
+int64_t hess_distill_topk_workspace(int64_t n, int64_t vocab, int dtype);
+int hess_distill_topk(const void* logits, int64_t ldz, int dtype, int64_t n, int64_t vocab, const void* ids, int ids64,
+                      int64_t ldi, const void* values, int values_dtype, int64_t ldv, int k, const float* weight,
+                      float temperature, float* loss, float* stats, void* dlogits, int64_t lddz, void* work,
+                      int64_t work_bytes, hess_stream_t stream);
+int hess_distill_topk_backward(const float* dloss, const void* logits, int64_t ldz, int dtype, int64_t n,
+                               int64_t vocab, const void* ids, int ids64, int64_t ldi, const void* values,
+                               int values_dtype, int64_t ldv, int k, const float* weight, float temperature,
+                               const float* stats, void* dlogits, int64_t lddz, hess_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
