@@ -578,12 +578,14 @@ def _float_code(name: str, t: torch.Tensor) -> int:
     return code
 
 
-def _rows(t: torch.Tensor):
-    """(tensor, row stride) of a 2-D tensor whose rows are contiguous and do not overlap (copied if need be)."""
+def _rows(t: torch.Tensor, step: int = 1):
+    """(tensor, row stride) of a 2-D tensor whose rows are contiguous, do not overlap and start at multiples
+    of ``step`` elements (copied if need be)."""
     n, c = t.shape
     s0, s1 = t.stride()
-    if (s1 != 1 and c > 1) or (n > 1 and s0 < c):
-        t = t.contiguous()
+    if ((s1 != 1 and c > 1) or (n > 1 and (s0 < c or s0 % step != 0))
+            or t.data_ptr() % (step * t.element_size()) != 0):
+        t = t.clone(memory_format=torch.contiguous_format)
         s0 = t.stride(0)
     return t, (s0 if n > 1 else max(c, 1))
 
@@ -631,9 +633,11 @@ def _ffn_args(x, w_gate, w_up):
     for name, t in (("w_gate", w_gate), ("w_up", w_up)):
         if t.dtype != x.dtype or t.device != x.device:
             raise ValueError(f"{name} must have x's dtype and device")
-    x2, ldx = _rows(x.reshape(-1, d) if x.dim() != 2 else x)
-    wg, ldg = _rows(w_gate)
-    wu, ldu = _rows(w_up)
+    # the tiles read 16-bit rows of a multiple of 8 values where they are, if they start at 16 bytes
+    step = 8 if code != HESS_F32 and d % 8 == 0 else 1
+    x2, ldx = _rows(x.reshape(-1, d) if x.dim() != 2 else x, step)
+    wg, ldg = _rows(w_gate, step)
+    wu, ldu = _rows(w_up, step)
     return code, x2, ldx, wg, ldg, wu, ldu, x2.shape[0], d, f
 
 

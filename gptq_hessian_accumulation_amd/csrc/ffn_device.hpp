@@ -1,0 +1,122 @@
+// Device code shared by the products of the gated feed-forward block: the
+// activations, the outputs' stores, and the order of the tiles.
+#pragma once
+
+#include "elem.hpp"
+#include "ffn_internal.hpp"
+#include "../../include/hess.h"
+
+namespace hess {
+
+// act(g) and act'(g) in float32.  The cumulative normal goes through erfc and
+// tanh through the sigmoid (0.5 (1 + tanh s) = sigmoid(2 s)), so the left
+// tails keep their relative accuracy.  Exact: float32 outputs, where the
+// library exponential's last bits count; otherwise the hardware exponential.
+template <bool Exact> __device__ __forceinline__ float sigmoidf(float v) {
+  if constexpr (Exact) return 1.0f / (1.0f + expf(-v));
+  else return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+}
+
+template <bool Exact> __device__ __forceinline__ float act_value(float g, int act) {
+  if (act == HESS_SILU) return g * sigmoidf<Exact>(g);
+  if (act == HESS_GELU) return g * (0.5f * erfcf(-0.70710678118654752f * g));
+  return g * sigmoidf<Exact>(1.5957691216057308f * (g + 0.044715f * g * g * g));
+}
+
+template <bool Exact> __device__ __forceinline__ void act_both(float g, int act, float& a, float& da) {
+  if (act == HESS_SILU) {
+    const float s = sigmoidf<Exact>(g);
+    a = g * s;
+    da = s * (1.0f + g * (1.0f - s));
+  } else if (act == HESS_GELU) {
+    const float c = 0.5f * erfcf(-0.70710678118654752f * g);
+    a = g * c;
+    const float e = -0.5f * g * g;
+    da = c + g * 0.39894228040143268f * (Exact ? expf(e) : __expf(e));
+  } else {
+    const float s = sigmoidf<Exact>(1.5957691216057308f * (g + 0.044715f * g * g * g));
+    a = g * s;
+    da = s + g * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
+  }
+}
+
+// N consecutive outputs of one row (one store of any alignment); `left` of
+// them lie inside the matrix.
+template <class T, int N> __device__ __forceinline__ void store_n(T* p, const float (&v)[N], int left) {
+  typedef T TN __attribute__((ext_vector_type(N)));
+  typedef TN TU __attribute__((aligned(sizeof(T))));
+  if (left >= N) {
+    TN o;
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = from_f32<T>(v[j]);
+    *reinterpret_cast<TU*>(p) = o;
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < left) p[j] = from_f32<T>(v[j]);
+  }
+}
+
+// Outputs of row r, columns c .. c + N - 1 (dx, dw).
+template <int DT, int Mode, int N>
+__device__ __forceinline__ void put(const FfnGemm& P, int64_t r, int64_t c, const float (&v)[N]) {
+  typedef typename Elem<DT>::type T;
+  if (r >= P.M || c >= P.N) return;
+  const int left = (int)min((int64_t)N, P.N - c);
+  if constexpr (Mode == kFfnDx) {
+    store_n(static_cast<T*>(P.o0) + r * P.ldo0 + c, v, left);
+  } else {
+    if (r < P.fp) {
+      if (r < P.f) store_n(static_cast<T*>(P.o0) + r * P.ldo0 + c, v, left);
+    } else if (r - P.fp < P.f) {
+      store_n(static_cast<T*>(P.o1) + (r - P.fp) * P.ldo1 + c, v, left);
+    }
+  }
+}
+
+// Outputs of row r, features c .. c + N - 1 of the forward pass.
+template <int DT, int N>
+__device__ __forceinline__ void put_fwd(const FfnGemm& P, int64_t r, int64_t c, const float (&g)[N],
+                                        const float (&u)[N]) {
+  typedef typename Elem<DT>::type T;
+  if (r >= P.M || c >= P.fp) return;
+  float h[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) h[j] = act_value<DT == kInF32>(g[j], P.act) * u[j];
+  if (c < P.N) store_n(static_cast<T*>(P.o0) + r * P.ldo0 + c, h, (int)min((int64_t)N, P.N - c));
+  if (P.o1) {
+    // columns f .. fp - 1 are the zeros their absent weight rows gave
+    T* q = static_cast<T*>(P.o1) + r * 2 * P.fp + c;
+    store_n(q, g, N);
+    store_n(q + P.fp, u, N);
+  }
+}
+
+// Tile t of the blocked order: groups of kGroupM tile rows, column by column
+// inside a group, so that consecutive tiles (one XCD's, see item_of_block)
+// share few operand panels.
+constexpr int kGroupM = 8;
+__device__ __forceinline__ void tile_coords(const FfnGemm& P, int t, int& I, int& J) {
+  const int per = kGroupM * P.tn;
+  const int grp = t / per;
+  const int rows = min(kGroupM, P.tm - grp * kGroupM);
+  const int in = t - grp * per;
+  J = in / rows;
+  I = grp * kGroupM + in - J * rows;
+}
+
+// Workgroup b of n runs on XCD b % 8: give each XCD a consecutive run of items.
+__device__ __forceinline__ int item_of_block(int b, int n) {
+  const int q = n >> 3, r = n & 7, x = b & 7;
+  return x * q + min(x, r) + (b >> 3);
+}
+
+// Column b of a forward tile's B panel: which projection, and which of the
+// tile's features.  Each wave column (64 wide) holds 32 features' gate
+// columns, then their up columns.
+__device__ __forceinline__ void fwd_column(int b, int& up, int& col) {
+  up = (b >> 5) & 1;
+  col = (b >> 6) * 32 + (b & 31);
+}
+
+}  // namespace hess

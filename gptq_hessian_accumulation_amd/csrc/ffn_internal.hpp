@@ -31,21 +31,30 @@ struct FfnGemm {
   int64_t M, N, K;
   int64_t f, fp;
   int act;
-  int vec_out;     // 4 consecutive outputs may be stored as one (fwd's o1 always may)
   // schedule: tiles 0 .. full - 1 of the blocked order are done whole; each of
   // the others is cut into `parts` ranges of part_len K-iterations, whose
   // partial sums go to workspace slot part * (ntiles - full) + (tile - full)
   int tm, tn, ntiles, full, parts, part_len, niter;
 };
 
-// Edges of the two tile kernels and their K step.
-constexpr int kFfnEdge = 128, kFfnStep = 16;
+// Tiles: float32 operands 128 x 128 by steps of 16 in K, 16-bit operands 256 or
+// 128 by steps of 32.
+constexpr int kFfnStep32 = 16, kFfnStep16 = 32;
+constexpr int kFfnEdge32 = 128;
 
-// Fills the schedule for tiles of the given edge.  max_slots: workspace slots.
-void ffn_schedule(FfnGemm& g, int mode, int edge, int step, int max_slots);
-constexpr int kFfnMaxSlots = 256;
+// Chooses the tile's edge (returned) and fills the schedule.
+int ffn_schedule(FfnGemm& g, int mode, int dtype);
 
-hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int dtype, hipStream_t stream);
+hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream);
+// The tiles of 16-bit operands.  Every operand row 16-byte aligned; where an
+// operand's rows run along K, K is a multiple of 8 and the row's elements past
+// it up to that are zeros.
+hipError_t launch_ffn_tile16(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream);
+
+// Copies rows x cols 16-bit values (row stride ld) to rows of pad >= cols (a
+// multiple of 8) values, zeros past cols.
+hipError_t launch_pack_rows16(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t pad,
+                              hipStream_t stream);
 
 // dg = dh u act'(g), du = dh act(g) into the n x 2 fp pair dgu (columns past f zero).
 hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f,

@@ -1,0 +1,342 @@
+// The gated feed-forward block's products on 16-bit operands: tiles of edge
+// 256 or 128 on v_mfma_f32_16x16x32 (bf16 or fp16), float32 accumulators.
+//
+//  * 8 waves of 128 x 64 (edge 256) or 4 of 64 x 64 (edge 128), one matrix
+//    instruction per 16 x 16 accumulator and stage of 32 values of K.  Two
+//    waves share each SIMD (edge 128: two workgroups a CU), so that one's
+//    waits are covered by the other's matrix instructions.  The B
+//    operand goes first, so that a lane holds four consecutive columns; two
+//    neighbouring blocks are exchanged between lane rows before they are
+//    stored, which makes eight (one 16-byte store).
+//  * Operands go from memory straight into LDS, five stages deep: the loads
+//    of four iterations are in flight while one is multiplied, with one
+//    barrier an iteration and hand-placed loads and operand reads among the
+//    matrix instructions (the pipeline of the 256-tile Gram kernel).
+//  * An operand whose rows run along K (x and the weights forward, the
+//    gradient pair for dx) is kept row by row, 64 bytes a row, its 16-byte
+//    chunks XOR-swizzled by bits 1-2 of the row, and read with ds_read_b128.
+//    One whose rows run across K (the weights for dx, both operands of dW)
+//    is kept k by k and read transposed with ds_read_b64_tr_b16.
+//  * Loads need no masks: rows and columns past the matrix get an offset past
+//    every descriptor's range, k past the matrix or past the part of K a
+//    workgroup was given lies outside the descriptor (or its chunk's offset
+//    does), and all of these read as zeros.
+
+#include "ffn_device.hpp"
+#include "hess_device.hpp"
+
+namespace hess {
+
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+template <int DT> __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
+  if constexpr (DT == kInBF16)
+    return mfma16x16x32(a, b, c);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+constexpr uint32_t kOOB = 0x80000000u;  // an offset past any descriptor's range
+constexpr int64_t kAll = 0x7fffffff;
+constexpr int kStages = 5, kAhead = 4;
+
+template <int DT, int Mode, int Edge>
+__global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
+  constexpr bool kRowsA = Mode != kFfnDw;  // A's rows run along K
+  constexpr bool kRowsB = Mode == kFfnFwd;
+  constexpr int kColWaves = Edge / 64;     // the tile's waves are 2 x kColWaves
+  constexpr int kBm = Edge / 32, kBn = 4;  // 16-wide blocks of a wave
+  constexpr int kPanel = Edge * kFfnStep16 * 2;
+  constexpr int kStage = 2 * kPanel;
+  constexpr int kLoads = 2;                // 1-KB loads per wave, panel and stage
+  constexpr int kRow = Edge * 2;           // bytes of one k of a panel kept k by k
+  constexpr int kPerK = 1024 / kRow;       // k's in one load of such a panel
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / kColWaves, wc = wave % kColWaves;
+  const uint32_t lds0 = (uint32_t) reinterpret_cast<uintptr_t>((HESS_LDS char*)lds);
+
+  const int item = item_of_block(blockIdx.x, gridDim.x);
+  const int tail = P.ntiles - P.full;
+  int t = item, part = 0;
+  const bool whole = item < P.full;
+  if (!whole) {
+    part = (item - P.full) / tail;
+    t = P.full + (item - P.full) % tail;
+  }
+  const int it0 = __builtin_amdgcn_readfirstlane(whole ? 0 : part * P.part_len);
+  const int it1 = __builtin_amdgcn_readfirstlane(whole ? P.niter : min(P.niter, it0 + P.part_len));
+  int I, J;
+  tile_coords(P, t, I, J);
+  const int64_t i0 = (int64_t)I * Edge;
+  const int64_t j0 = (int64_t)J * (Mode == kFfnFwd ? Edge / 2 : Edge);
+  const int per_seg = Mode == kFfnDx ? P.niter / 2 : P.niter;
+  const int64_t rowA = P.lda * 2, rowB = P.ldb0 * 2;
+
+  // Offsets of this wave's loads.  Along K: load i holds 16 rows, lane l row
+  // l / 4 of them and position l % 4, where chunk (l % 4) ^ (row / 2 % 4)
+  // lives.  Across K: load i holds kPerK values of k, the lane a chunk of 8
+  // columns of one of them.
+  const int chunk = (lane & 3) ^ ((lane >> 3) & 3);
+  uint32_t voffA[kLoads], voffB[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = 16 * (kLoads * wave + i) + (lane >> 2);
+    const int k = kPerK * (kLoads * wave + i) + lane / (64 / kPerK);
+    const int col = 8 * chunk_pos(k, lane % (64 / kPerK));
+    if constexpr (kRowsA) voffA[i] = i0 + row < P.M ? (uint32_t)(row * rowA + chunk * 16) : kOOB;
+    else voffA[i] = i0 + col < P.M ? (uint32_t)(k * rowA + col * 2) : kOOB;
+    if constexpr (kRowsB) {
+      // the wave's B rows are of one projection (see fwd_column)
+      const int feat = (wave >> 1) * 32 + 16 * i + (lane >> 2);
+      voffB[i] = j0 + feat < P.N ? (uint32_t)(feat * (int64_t)((wave & 1) ? P.ldb1 : P.ldb0) * 2 + chunk * 16) : kOOB;
+    } else {
+      const int64_t ld = Mode == kFfnDx ? 0 : rowB;  // dx: the segment's stride, added per iteration
+      voffB[i] = j0 + col < P.N ? (uint32_t)(k * ld + col * 2) : kOOB;
+    }
+  }
+  // dx reads two weights, whose strides may differ; the wave's k rows are
+  // few, so the offset is rebuilt when the segment changes
+  uint32_t voffB1[kLoads];
+  if constexpr (Mode == kFfnDx) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int k = kPerK * (kLoads * wave + i) + lane / (64 / kPerK);
+      voffB1[i] = voffB[i] == kOOB ? kOOB : voffB[i] + (uint32_t)(k * P.ldb1 * 2);
+      if (voffB[i] != kOOB) voffB[i] += (uint32_t)(k * P.ldb0 * 2);
+    }
+  }
+
+  struct Next {
+    u32x4 ra, rb;
+    int lim;  // chunks of K left for the operands whose rows run along K
+    int seg;
+  };
+  auto describe = [&](int j) {
+    Next d;
+    d.seg = Mode == kFfnDx && j >= per_seg;
+    const int64_t k0 = (int64_t)(j - d.seg * per_seg) * kFfnStep16;
+    const int64_t kend = Mode == kFfnDx ? P.fp : P.K;
+    const bool live = j < it1;
+    d.lim = (int)((kend - k0 + 7) >> 3);
+    const int64_t valid = live ? max((int64_t)0, min((int64_t)kFfnStep16, P.K - k0)) : 0;
+    const uint64_t a = reinterpret_cast<uint64_t>(P.a);
+    if constexpr (kRowsA)
+      d.ra = rsrc_words(a + (uint64_t)(i0 * rowA + (d.seg * P.fp + k0) * 2), live ? kAll : 0);
+    else
+      d.ra = rsrc_words(a + (uint64_t)(k0 * rowA + i0 * 2), valid * rowA);
+    if constexpr (kRowsB) {
+      const uint64_t b = reinterpret_cast<uint64_t>((wave & 1) ? P.b1 : P.b0);
+      const int64_t ld = (wave & 1) ? P.ldb1 : P.ldb0;
+      d.rb = rsrc_words(b + (uint64_t)((j0 * ld + k0) * 2), live ? kAll : 0);
+    } else {
+      const uint64_t b = reinterpret_cast<uint64_t>(d.seg ? P.b1 : P.b0);
+      const int64_t ld = d.seg ? P.ldb1 : P.ldb0;
+      d.rb = rsrc_words(b + (uint64_t)((k0 * ld + j0) * 2), valid * ld * 2);
+    }
+    return d;
+  };
+  // load i of the wave's 2 kLoads of one stage
+  auto load1 = [&](uint32_t stage, const Next& d, int i) {
+    const bool isA = i < kLoads;
+    const int q = isA ? i : i - kLoads;
+    uint32_t off = isA ? voffA[q] : voffB[q];
+    if (Mode == kFfnDx && !isA) off = d.seg ? voffB1[q] : off;
+    if (isA ? kRowsA : kRowsB) off = chunk < d.lim ? off : kOOB;
+    lds_dma16(isA ? d.ra : d.rb, off, stage + (isA ? 0 : kPanel) + (uint32_t)((kLoads * wave + q) * 1024));
+  };
+  auto load_stage = [&](uint32_t stage, int j) {
+    const Next d = describe(j);
+#pragma unroll
+    for (int i = 0; i < 2 * kLoads; ++i) load1(stage, d, i);
+  };
+
+  // Operand block m of a panel half: lane l holds row (or column) l % 16 of
+  // the block, k = 8 (l / 16) .. + 7.
+  const int rowpos = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
+  const int tl = 8 * (lane >> 4) + ((lane & 15) >> 2);
+  // The block enters as 1024 m (rows) or, by the XOR of the chunks, as a flip
+  // of the bits 5-7 of the address (16 m columns are 2 m chunks).
+  auto lane_pos = [&](bool rows, int col0) {
+    if (rows) return col0 * 64 + rowpos;
+    const int c = (col0 + 4 * (lane & 3)) >> 3;
+    return tl * kRow + (chunk_pos(tl, c) << 4) + 8 * (lane & 1);
+  };
+  const int posA = lane_pos(kRowsA, wr * (Edge / 2)), posB = lane_pos(kRowsB, wc * 64);
+  auto read1 = [&](const char* stage, int pos, int m, bool rows) {
+    if (rows) return *reinterpret_cast<const u32x4*>(stage + pos + m * 1024);
+    const char* p = stage + (pos ^ (m << 5));
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HESS_LDS s16x4*)(p));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HESS_LDS s16x4*)(p + 4 * kRow));
+    const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+    return u32x4{a.x, a.y, b.x, b.y};
+  };
+  auto read_a = [&](uint32_t stage, int m) { return read1(lds + stage, posA, m, kRowsA); };
+  auto read_b = [&](uint32_t stage, int n) { return read1(lds + stage + kPanel, posB, n, kRowsB); };
+
+  f32x4 acc[kBm][kBn];
+#pragma unroll
+  for (int m = 0; m < kBm; ++m)
+#pragma unroll
+    for (int n = 0; n < kBn; ++n) acc[m][n] = f32x4{};
+
+  // Iteration j on the stage at cur (its first four A blocks are in a, its B
+  // blocks in b): wait for my loads of the next iteration, meet the other
+  // waves (the next stage is then complete, and nobody reads the one before
+  // cur), then group by group the matrix instructions of one A block, the
+  // read of the A block four groups later (of the next stage at the end), a
+  // read of the next stage's B (into c) and a load of iteration j + 4.
+  u32x4 a[4];
+  auto step = [&](uint32_t cur, uint32_t nxt, uint32_t target, int j, const u32x4 (&b)[kBn], u32x4 (&c)[kBn]) {
+    const Next d = describe(j + kAhead);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 2)));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < kBm; ++m) {
+#pragma unroll
+      for (int n = 0; n < kBn; ++n) acc[m][n] = mfma16<DT>(b[n], a[m & 3], acc[m][n]);
+      a[m & 3] = m + 4 < kBm ? read_a(cur, m + 4) : read_a(nxt, m + 4 - kBm);
+      if (m >= kBm - kBn) c[m - (kBm - kBn)] = read_b(nxt, m - (kBm - kBn));
+      if (kBm == 4 || (m & 1)) load1(lds0 + target, d, kBm == 4 ? m : m >> 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  static_assert(2 * kLoads == 4, "a load for every one (edge 128) or two groups");
+
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) load_stage(lds0 + q * kStage, it0 + q);
+  __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 1)));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  u32x4 b[kBn], c[kBn];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) a[q] = read_a(0, q);
+#pragma unroll
+  for (int q = 0; q < kBn; ++q) b[q] = read_b(0, q);
+  // two iterations a trip (two sets of B registers); an extra iteration
+  // multiplies zeros.  The stages go round in scalar registers.
+  uint32_t cur = 0, nxt = kStage, ld = kAhead * kStage;
+  auto rotate = [&] {
+    cur = nxt;
+    nxt = nxt + kStage == kStages * kStage ? 0u : nxt + kStage;
+    ld = ld + kStage == kStages * kStage ? 0u : ld + kStage;
+  };
+  for (int j = it0; j < it1; j += 2) {
+    step(cur, nxt, ld, j, b, c);
+    rotate();
+    step(cur, nxt, ld, j + 1, c, b);
+    rotate();
+  }
+  // the trailing loads write LDS: they end before the workgroup does
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_sched_barrier(0);
+
+  int lv = lane;
+  asm volatile("" : "+v"(lv));  // the output's offsets are computed here, not kept through the loop
+  const int rr = wr * (Edge / 2) + (lv & 15);
+  if (!whole) {
+    float* W = P.ws + ((int64_t)part * tail + (t - P.full)) * (Edge * Edge);
+    const int cc = wc * 64 + 4 * (lv >> 4);
+#pragma unroll
+    for (int m = 0; m < kBm; ++m)
+#pragma unroll
+      for (int n = 0; n < kBn; ++n) {
+        const f32x4 a = acc[m][n];
+        *reinterpret_cast<float4*>(W + (rr + 16 * m) * Edge + cc + 16 * n) = float4{a[0], a[1], a[2], a[3]};
+      }
+    return;
+  }
+  // Blocks n, n + 1: after exchanging the odd 16-lane rows of the first with
+  // the even ones of the second, lane row g holds columns 8 (g / 2) .. + 7 of
+  // block n + g % 2.
+  const int cc = 16 * ((lv >> 4) & 1) + 8 * (lv >> 5);
+  auto eight = [&](const f32x4& p, const f32x4& q, float (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[j]), __float_as_uint(q[j]), false, false);
+      o[j] = __uint_as_float(s[0]);
+      o[4 + j] = __uint_as_float(s[1]);
+    }
+  };
+#pragma unroll
+  for (int m = 0; m < kBm; ++m) {
+    const int64_t r = i0 + rr + 16 * m;
+    if constexpr (Mode == kFfnFwd) {
+#pragma unroll
+      for (int n = 0; n < kBn / 2; n += 2) {
+        float g[8], u[8];
+        eight(acc[m][n], acc[m][n + 1], g);
+        eight(acc[m][n + kBn / 2], acc[m][n + 1 + kBn / 2], u);
+        put_fwd<DT>(P, r, j0 + wc * 32 + 16 * n + cc, g, u);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < kBn; n += 2) {
+        float v[8];
+        eight(acc[m][n], acc[m][n + 1], v);
+        put<DT, Mode>(P, r, j0 + wc * 64 + 16 * n + cc, v);
+      }
+    }
+  }
+}
+
+template <int DT, int Mode> void launch_mode(const FfnGemm& g, int edge, hipStream_t stream) {
+  const int tail = g.ntiles - g.full;
+  if (edge == 256) ffn_tile16<DT, Mode, 256><<<g.full + tail * g.parts, 512, 0, stream>>>(g);
+  else ffn_tile16<DT, Mode, 128><<<g.full + tail * g.parts, 256, 0, stream>>>(g);
+}
+
+template <int DT> void launch_type(const FfnGemm& g, int mode, int edge, hipStream_t stream) {
+  if (mode == kFfnFwd) launch_mode<DT, kFfnFwd>(g, edge, stream);
+  else if (mode == kFfnDx) launch_mode<DT, kFfnDx>(g, edge, stream);
+  else launch_mode<DT, kFfnDw>(g, edge, stream);
+}
+
+// Row r of a matrix of `cols` 16-bit values to a row of `pad` (a multiple of
+// 8), the rest zeros; 8 values a thread.
+__global__ void __launch_bounds__(256) pack_rows16(const uint16_t* src, int64_t ld, int cols, uint16_t* dst, int pad,
+                                                   int64_t total) {
+  typedef uint16_t V __attribute__((ext_vector_type(8)));
+  typedef V VU __attribute__((aligned(2)));
+  const int per = pad / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    const uint16_t* p = src + r * ld + c;
+    V v;
+    if (c + 8 <= cols) {
+      v = *reinterpret_cast<const VU*>(p);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? p[j] : (uint16_t)0;
+    }
+    *reinterpret_cast<V*>(dst + r * pad + c) = v;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_ffn_tile16(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream) {
+  if (dtype == kInBF16) launch_type<kInBF16>(g, mode, edge, stream);
+  else launch_type<kInF16>(g, mode, edge, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_pack_rows16(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t pad,
+                              hipStream_t stream) {
+  const int64_t total = rows * (pad / 8);
+  if (total == 0) return hipSuccess;
+  const int grid = (int)(total < 256 * 4096 ? (total + 255) / 256 : 4096);
+  pack_rows16<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(src), ld, (int)cols, static_cast<uint16_t*>(dst),
+                                        (int)pad, total);
+  return hipGetLastError();
+}
+
+}  // namespace hess

@@ -82,4 +82,32 @@ __device__ __forceinline__ void transpose8x8_b16(const u32x4 (&row)[8], u32x4 (&
   }
 }
 
+// s_waitcnt immediate: vmcnt(n), no wait on the other counters
+constexpr int vm_wait(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+
+// Physical 16-byte chunk of logical chunk c (8 features) in token row t of a
+// row-major stage (rows of at least 16 chunks): c ^ 2 (t % 4) ^ 8 ((t / 8) % 2), an involution.  In a
+// transposed read the 16 lanes of a group read 4 consecutive rows t and two
+// adjacent chunks, which land in 8 distinct chunks of one 128-byte half of
+// the bank space; the group 8 tokens further on lands in the other half.
+__device__ __forceinline__ int chunk_pos(int t, int c) { return c ^ (2 * (t & 3)) ^ (8 * ((t >> 3) & 1)); }
+
+// A buffer descriptor over [base, base + bytes) as four scalar words, for the load
+// instruction written out below.
+__device__ __forceinline__ u32x4 rsrc_words(uint64_t base, int64_t bytes) {
+  u32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane((uint32_t)base);
+  r[1] = __builtin_amdgcn_readfirstlane((uint32_t)(base >> 32)) & 0xffffu;
+  r[2] = __builtin_amdgcn_readfirstlane((uint32_t)bytes);
+  r[3] = 0x00020000u;
+  return r;
+}
+
+// One 64-lane 16-byte load from memory into LDS at m0 + 16 * lane (zeros
+// for offsets past the descriptor's range).  m0 is set by the compiler as
+// an input operand; the s_nop covers the m0-write to LDS-DMA hazard.
+__device__ __forceinline__ void lds_dma16(const u32x4& r, uint32_t voff, uint32_t m0) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(r), "{m0}"(m0) : "memory");
+}
+
 }  // namespace hess

@@ -80,12 +80,6 @@ int check_work(const void* work, int64_t have, int64_t need) {
   return HESS_OK;
 }
 
-// Bytes of partial tiles one product needs.
-int64_t slot_bytes(FfnGemm g, int mode) {
-  ffn_schedule(g, mode, kFfnEdge, kFfnStep, kFfnMaxSlots);
-  return (int64_t)(g.ntiles - g.full) * g.parts * kFfnEdge * kFfnEdge * 4;
-}
-
 FfnGemm shape(int64_t M, int64_t N, int64_t K) {
   FfnGemm g{};
   g.M = M;
@@ -94,13 +88,57 @@ FfnGemm shape(int64_t M, int64_t N, int64_t K) {
   return g;
 }
 
-int64_t forward_slots(int64_t n, int64_t d, int64_t f) { return slot_bytes(shape(n, f, d), kFfnFwd); }
-int64_t backward_slots(int64_t n, int64_t d, int64_t f) {
-  return std::max(slot_bytes(shape(n, d, f), kFfnDx), slot_bytes(shape(2 * up(f, 8), d, n), kFfnDw));
+// Bytes of partial tiles a product needs.
+int64_t slot_bytes(FfnGemm g, int mode, int dtype) {
+  const int edge = ffn_schedule(g, mode, dtype);
+  return (int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4;
 }
 
-// Four consecutive outputs may be stored together.
-int vec_rows(const void* p, int64_t ld, int64_t es) { return aligned(p, 4 * es) && ld % 4 == 0; }
+// The 16-bit tiles take 16-byte rows of x and the weights: widths that are no
+// multiple of 8 are copied to padded rows in the workspace.
+bool packed(int64_t d, int dtype) { return dtype != HESS_F32 && d % 8 != 0; }
+int64_t pack_bytes(int64_t rows, int64_t d) { return up(rows * up(d, 8) * 2, 256); }
+
+// Workspace: forward: packed x, gate, up | partial tiles; backward: the
+// gradient pair | packed x, gate, up | partial tiles.
+struct FfnWork {
+  int64_t pack, slots, total;
+};
+FfnWork ffn_work(int64_t n, int64_t d, int64_t f, int dtype, bool backward) {
+  FfnWork w{};
+  w.pack = backward ? up(n * 2 * up(f, 8) * elem_bytes(dtype), 256) : 0;
+  w.slots = w.pack + (packed(d, dtype) ? pack_bytes(n, d) + 2 * pack_bytes(f, d) : 0);
+  w.total = w.slots + (backward ? std::max(slot_bytes(shape(n, d, f), kFfnDx, dtype),
+                                           slot_bytes(shape(2 * up(f, 8), d, n), kFfnDw, dtype))
+                                : slot_bytes(shape(n, f, d), kFfnFwd, dtype));
+  return w;
+}
+
+// x, gate and up as the tiles take them: where they are, or (widths that are
+// no multiple of 8) copied to padded rows.
+struct FfnOperands {
+  const void *x, *wg, *wu;
+  int64_t ldx, ldg, ldu, d;
+};
+int place_operands(FfnOperands& o, char* pack, int64_t n, int64_t f, int dtype, bool want_x, bool want_w,
+                   hipStream_t s) {
+  if (!packed(o.d, dtype)) {
+    if (dtype != HESS_F32 && (!aligned(o.x, 16) || !aligned(o.wg, 16) || !aligned(o.wu, 16) ||
+                              (n > 1 && o.ldx % 8 != 0) || (f > 1 && (o.ldg % 8 != 0 || o.ldu % 8 != 0))))
+      return fail(HESS_EALIGN, "rows of x, w_gate and w_up must be 16-byte aligned where d is a multiple of 8");
+    return HESS_OK;
+  }
+  const int64_t pad = up(o.d, 8);
+  char* pg = pack + pack_bytes(n, o.d);
+  char* pu = pg + pack_bytes(f, o.d);
+  hipError_t e = hipSuccess;
+  if (want_x) e = launch_pack_rows16(o.x, o.ldx, n, o.d, pack, pad, s);
+  if (want_w && e == hipSuccess) e = launch_pack_rows16(o.wg, o.ldg, f, o.d, pg, pad, s);
+  if (want_w && e == hipSuccess) e = launch_pack_rows16(o.wu, o.ldu, f, o.d, pu, pad, s);
+  if (e != hipSuccess) return hip_fail(e, "operand copy launch");
+  o = FfnOperands{pack, pg, pu, pad, pad, pad, pad};
+  return HESS_OK;
+}
 
 }  // namespace
 
@@ -117,8 +155,7 @@ int64_t hess_gated_ffn_preact_cols(int64_t f) {
 int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int backward) {
   if (check_ffn_sizes(n, d, f, dtype) != HESS_OK) return -1;
   if (n == 0) return 0;
-  if (!backward) return forward_slots(n, d, f);
-  return up(n * 2 * up(f, 8) * elem_bytes(dtype), 256) + backward_slots(n, d, f);
+  return ffn_work(n, d, f, dtype, backward != 0).total;
 }
 
 int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64_t ldg, const void* w_up, int64_t ldu,
@@ -134,28 +171,31 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
     if (int rc = check_mat(m, es)) return rc;
   if (int rc = check_mat(outs[0], es)) return rc;
   if (!aligned(preact, 16)) return fail(HESS_EALIGN, "preact not 16-byte aligned");
-  const int64_t need = hess_gated_ffn_workspace(n, d, f, dtype, 0);
-  if (int rc = check_work(work, work_bytes, need)) return rc;
-  if (int rc = check_outputs(outs, 2, ins, 3, es, work, need)) return rc;
+  const FfnWork room = ffn_work(n, d, f, dtype, false);
+  if (int rc = check_work(work, work_bytes, room.total)) return rc;
+  if (int rc = check_outputs(outs, 2, ins, 3, es, work, room.total)) return rc;
 
-  FfnGemm g = shape(n, f, d);
-  g.a = x;
-  g.lda = ldx;
-  g.b0 = w_gate;
-  g.ldb0 = ldg;
-  g.b1 = w_up;
-  g.ldb1 = ldu;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* base = static_cast<char*>(work);
+  FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
+  if (int rc = place_operands(o, base, n, f, dtype, true, true, s)) return rc;
+  FfnGemm g = shape(n, f, o.d);
+  g.a = o.x;
+  g.lda = o.ldx;
+  g.b0 = o.wg;
+  g.ldb0 = o.ldg;
+  g.b1 = o.wu;
+  g.ldb1 = o.ldu;
   g.o0 = h;
   g.ldo0 = ldh;
   g.o1 = preact;
   g.ldo1 = 2 * fp;
-  g.ws = static_cast<float*>(work);
+  g.ws = reinterpret_cast<float*>(base + room.slots);
   g.f = f;
   g.fp = fp;
   g.act = act;
-  g.vec_out = vec_rows(h, ldh, es);
-  ffn_schedule(g, kFfnFwd, kFfnEdge, kFfnStep, kFfnMaxSlots);
-  const hipError_t e = launch_ffn_gemm(g, kFfnFwd, dtype, static_cast<hipStream_t>(stream));
+  const int edge = ffn_schedule(g, kFfnFwd, dtype);
+  const hipError_t e = launch_ffn_gemm(g, kFfnFwd, edge, dtype, s);
   return e == hipSuccess ? HESS_OK : hip_fail(e, "gated feed-forward launch");
 }
 
@@ -182,9 +222,9 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
     if (m.p && m.rows > 0)
       if (int rc = check_mat(m, es)) return rc;
   if (!aligned(preact, 16)) return fail(HESS_EALIGN, "preact not 16-byte aligned");
-  const int64_t need = hess_gated_ffn_workspace(n, d, f, dtype, 1);
-  if (int rc = check_work(work, work_bytes, need)) return rc;
-  if (int rc = check_outputs(outs, 3, ins, 5, es, work, need)) return rc;
+  const FfnWork room = n > 0 ? ffn_work(n, d, f, dtype, true) : FfnWork{};
+  if (int rc = check_work(work, work_bytes, room.total)) return rc;
+  if (int rc = check_outputs(outs, 3, ins, 5, es, work, room.total)) return rc;
   hipError_t e = hipSuccess;
   if (n == 0) {
     if (dw_gate) {
@@ -196,33 +236,34 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
   if (!dx && !dw_gate) return HESS_OK;
 
   char* dgu = static_cast<char*>(work);
-  float* slots = reinterpret_cast<float*>(dgu + up(n * 2 * fp * es, 256));
+  float* slots = reinterpret_cast<float*>(dgu + room.slots);
+  FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
+  if (int rc = place_operands(o, dgu + room.pack, n, f, dtype, dw_gate != nullptr, dx != nullptr, s)) return rc;
   e = launch_ffn_dgu(dh, lddh, preact, dgu, n, f, fp, act, dtype, s);
   if (e != hipSuccess) return hip_fail(e, "gate gradient launch");
   if (dx) {
     FfnGemm g = shape(n, d, f);
     g.a = dgu;
     g.lda = 2 * fp;
-    g.b0 = w_gate;
-    g.ldb0 = ldg;
-    g.b1 = w_up;
-    g.ldb1 = ldu;
+    g.b0 = o.wg;
+    g.ldb0 = o.ldg;
+    g.b1 = o.wu;
+    g.ldb1 = o.ldu;
     g.o0 = dx;
     g.ldo0 = lddx;
     g.ws = slots;
     g.f = f;
     g.fp = fp;
-    g.vec_out = vec_rows(dx, lddx, es);
-    ffn_schedule(g, kFfnDx, kFfnEdge, kFfnStep, kFfnMaxSlots);
-    e = launch_ffn_gemm(g, kFfnDx, dtype, s);
+    const int edge = ffn_schedule(g, kFfnDx, dtype);
+    e = launch_ffn_gemm(g, kFfnDx, edge, dtype, s);
     if (e != hipSuccess) return hip_fail(e, "input gradient launch");
   }
   if (dw_gate) {
     FfnGemm g = shape(2 * fp, d, n);
     g.a = dgu;
     g.lda = 2 * fp;
-    g.b0 = x;
-    g.ldb0 = ldx;
+    g.b0 = o.x;
+    g.ldb0 = o.ldx;
     g.o0 = dw_gate;
     g.ldo0 = lddg;
     g.o1 = dw_up;
@@ -230,9 +271,8 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
     g.ws = slots;
     g.f = f;
     g.fp = fp;
-    g.vec_out = vec_rows(dw_gate, lddg, es) && vec_rows(dw_up, lddu, es);
-    ffn_schedule(g, kFfnDw, kFfnEdge, kFfnStep, kFfnMaxSlots);
-    e = launch_ffn_gemm(g, kFfnDw, dtype, s);
+    const int edge = ffn_schedule(g, kFfnDw, dtype);
+    e = launch_ffn_gemm(g, kFfnDw, edge, dtype, s);
     if (e != hipSuccess) return hip_fail(e, "weight gradient launch");
   }
   return HESS_OK;

@@ -88,15 +88,6 @@ constexpr int kStageB = 2 * kPanelB;         // 32 KB
 constexpr int kDma = kStageB / 1024 / 4;     // 1-KB loads per wave per stage (8)
 constexpr uint32_t kOOB = 0x80000000u;       // an offset past any descriptor's range
 constexpr int kDist = 4;                     // iterations between a stage's load and its use
-// s_waitcnt immediate: vmcnt(n), no wait on the other counters
-constexpr int vm_wait(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
-
-// Physical 16-byte chunk of logical chunk c (8 features) in token row t of a
-// row-major stage: c ^ 2 (t % 4) ^ 8 ((t / 8) % 2), an involution.  In a
-// transposed read the 16 lanes of a group read 4 consecutive rows t and two
-// adjacent chunks, which land in 8 distinct chunks of one 128-byte half of
-// the bank space; the group 8 tokens further on lands in the other half.
-__device__ __forceinline__ int chunk_pos(int t, int c) { return c ^ (2 * (t & 3)) ^ (8 * ((t >> 3) & 1)); }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(uint64_t base, int64_t bytes) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)base);
@@ -104,23 +95,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(uint64_t base, int64
   const int nrec = __builtin_amdgcn_readfirstlane((int)bytes);
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo), (short)0, nrec,
                                            0x00020000);
-}
-
-// The same descriptor as four scalar words, for the load instruction written out.
-__device__ __forceinline__ u32x4 rsrc_words(uint64_t base, int64_t bytes) {
-  u32x4 r;
-  r[0] = __builtin_amdgcn_readfirstlane((uint32_t)base);
-  r[1] = __builtin_amdgcn_readfirstlane((uint32_t)(base >> 32)) & 0xffffu;
-  r[2] = __builtin_amdgcn_readfirstlane((uint32_t)bytes);
-  r[3] = 0x00020000u;
-  return r;
-}
-
-// One 64-lane 16-byte load from memory into LDS at m0 + 16 * lane (zeros
-// for offsets past the descriptor's range).  m0 is set by the compiler as
-// an input operand; the s_nop covers the m0-write to LDS-DMA hazard.
-__device__ __forceinline__ void lds_dma16(const u32x4& r, uint32_t voff, uint32_t m0) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(r), "{m0}"(m0) : "memory");
 }
 
 __device__ __forceinline__ u32x4 tr_pair(const char* p) {
