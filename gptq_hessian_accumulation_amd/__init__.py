@@ -779,7 +779,7 @@ def distill_topk_forward(logits: torch.Tensor, ids: torch.Tensor, values: torch.
 
     logits (..., vocab) bfloat16, float16 or float32; ids (..., k) int32 or int64 (negative: absent);
     values (..., k) the teacher's logits there; weight (...) float32, 0 for rows to leave out.  loss (...)
-    and stats (..., 2), the maximum of logits / temperature and the sum of exponentials above it, are float32.
+    and stats (..., 2), the largest logit and the sum of exp((logits - largest) / temperature), are float32.
     """
     return _distill_call(logits, ids, values, weight, temperature, True, False, None, workspace)[:2]
 

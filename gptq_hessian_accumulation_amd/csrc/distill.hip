@@ -1,18 +1,30 @@
 // Distillation from a teacher's top logits on gfx950.  For each row, with
 // p = softmax(values / T) over the present entries and q = softmax(z / T):
 //
-//   loss = w sum_i p_i (log p_i - log q[id_i]),   q_j = exp(z_j / T - m) / s
+//   loss = w sum_i p_i (log p_i - log q[id_i]),   q_j = exp((z_j - m) / T) / s
 //   dz_j = c w / T (q_j - sum over i with id_i = j of p_i)
 //
-// with m = max(z / T) and s = sum exp(z / T - m).
+// with m = max z and s = sum exp((z - m) / T).
 //
-// One workgroup a row.  Exponentials are float32, joined across the workgroup
-// in float64; the k teacher terms are float64, because the loss is a difference of logarithms that cancel where
-// student and teacher agree.  1 / T is rounded once to float32 and used for
-// both softmaxes, so that the rounding acts as a temperature off by 2^-25 and
-// not as an offset between the two.
+// Three kernels, all bound by the bytes of z and dz:
+//  * loss and gradient in one pass over rows that fit the register file: a
+//    workgroup holds a whole row (up to 16 vectors of 16 bytes a thread) and
+//    reads it once;
+//  * the loss alone: one workgroup a row, a running maximum and sum;
+//  * the gradient from the row's statistics: chunks of rows, one pass.
+// Longer rows take the second and the third for loss and gradient.
+//
+// Exponentials are 2^x of float32 arguments (z - m) log2(e) / T (the
+// difference first, so that values near the type's largest stay finite);
+// threads' sums are float32 and joined in float64; the k teacher terms are
+// float64, because the loss is a difference of logarithms that cancel where
+// student and teacher agree.  log2(e) / T is rounded once to float32 and used
+// for both softmaxes, so that the rounding acts as a temperature off by 2^-24
+// and not as an offset between the two.
 
+#include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "distill_internal.hpp"
 #include "elem.hpp"
@@ -21,164 +33,604 @@ namespace hess {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
 constexpr int kTop = 1024;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
 
-__device__ __forceinline__ double wave_sum(double v) {
+template <class T> __device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
-__device__ __forceinline__ double wave_max(double v) {
+__device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
   return v;
 }
-// Sum / maximum over the workgroup, the same value in every thread.
-__device__ __forceinline__ double block_sum(double v, double* red) {
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double t = red[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) t += red[w];
-  return t;
-}
-__device__ __forceinline__ double block_max(double v, double* red) {
-  v = wave_max(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double t = red[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) t = fmax(t, red[w]);
-  return t;
-}
 
-__device__ __forceinline__ int64_t load_id(const DistillParams& P, int64_t row, int i) {
-  return P.ids64 ? static_cast<const int64_t*>(P.ids)[row * P.ldi + i]
-                 : static_cast<const int32_t*>(P.ids)[row * P.ldi + i];
-}
-__device__ __forceinline__ float load_value(const DistillParams& P, int64_t row, int i) {
-  const int64_t o = row * P.ldv + i;
-  if (P.values_dtype == kInBF16) return to_f32(static_cast<const __bf16*>(P.values)[o]);
-  if (P.values_dtype == kInF16) return to_f32(static_cast<const _Float16*>(P.values)[o]);
-  return static_cast<const float*>(P.values)[o];
-}
-
-template <int DT, bool Backward> __global__ void __launch_bounds__(kThreads) distill_row(DistillParams P) {
+// 16 bytes of a row of T: its values, and loads and stores at any alignment.
+template <int DT> struct Vec {
   typedef typename Elem<DT>::type T;
-  __shared__ double red[kWaves];
-  __shared__ int s_id[kTop];
-  __shared__ float s_p[kTop], s_z[kTop];
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  const T* z = static_cast<const T*>(P.z) + row * P.ldz;
-  T* dz = static_cast<T*>(P.dz) + (P.dz ? row * P.lddz : 0);
-  const float w = P.weight ? P.weight[row] : 1.0f;
-  const float it = (float)(1.0 / (double)P.temperature);
-
-  // the teacher's entries; id -1: absent, as is one of value -infinity (p = 0)
-  double vmax = -INFINITY;
-  int any = 0, bad = 0;
-  for (int i = tid; i < P.k; i += kThreads) {
-    const int64_t id = load_id(P, row, i);
-    const float v = id >= 0 ? load_value(P, row, i) : -INFINITY;
-    const bool present = v != -INFINITY;
-    any |= present;
-    bad |= id >= P.vocab;
-    s_id[i] = (present && id < P.vocab) ? (int)id : -1;
-    if (s_id[i] >= 0) {
-      s_p[i] = v;
-      s_z[i] = to_f32(z[id]);
-      vmax = fmax(vmax, (double)v * it);
+  static constexpr int N = 16 / Elem<DT>::size;
+  typedef T TN __attribute__((ext_vector_type(16 / sizeof(T))));
+  typedef typename std::conditional<sizeof(T) == 2, u32x4_at2, u32x4_at4>::type U;
+  // elements j .. j + N - 1 of a row of n; past it -infinity
+  static __device__ __forceinline__ u32x4 load(const T* row, int64_t j, int64_t n) {
+    if (j + N <= n) return *reinterpret_cast<const U*>(row + j);
+    TN t;
+#pragma unroll
+    for (int e = 0; e < N; ++e) t[e] = (T)(-INFINITY);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (j + e < n) t[e] = row[j + e];
+    return __builtin_bit_cast(u32x4, t);
+  }
+  static __device__ __forceinline__ void store(T* row, int64_t j, int64_t n, const float (&v)[N]) {
+    TN t;
+#pragma unroll
+    for (int e = 0; e < N; ++e) t[e] = from_f32<T>(v[e]);
+    if (j + N <= n) {
+      *reinterpret_cast<U*>(row + j) = __builtin_bit_cast(u32x4, t);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (j + e < n) row[j + e] = t[e];
     }
   }
-  any = __syncthreads_or(any);
-  bad = __syncthreads_or(bad);
-  if (w == 0.0f || !any) {
-    if (!Backward && tid == 0) P.loss[row] = 0.0f;
-    if (!Backward && P.stats && tid < 2) P.stats[2 * row + tid] = 0.0f;
-    if (P.dz)
-      for (int64_t j = tid; j < P.vocab; j += kThreads) dz[j] = from_f32<T>(0.0f);
-    return;
+  static __device__ __forceinline__ void store_whole(T* p, const float (&v)[N]) {
+    TN t;
+#pragma unroll
+    for (int e = 0; e < N; ++e) t[e] = from_f32<T>(v[e]);
+    *reinterpret_cast<U*>(p) = __builtin_bit_cast(u32x4, t);
   }
-  vmax = block_max(vmax, red);
-  double psum = 0.0;
-  for (int i = tid; i < P.k; i += kThreads)
-    if (s_id[i] >= 0) psum += exp((double)s_p[i] * it - vmax);
-  psum = block_sum(psum, red);
-  const double lsep = vmax + log(psum);
+  static __device__ __forceinline__ void get(const u32x4& r, float (&v)[N]) {
+    const TN t = __builtin_bit_cast(TN, r);
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = to_f32(t[e]);
+  }
+};
 
-  float m, sum;
-  if constexpr (Backward) {
-    m = P.stats[2 * row];
-    sum = P.stats[2 * row + 1];
-  } else {
-    m = -INFINITY;
-    for (int64_t j = tid; j < P.vocab; j += kThreads) m = fmaxf(m, to_f32(z[j]) * it);
-    m = (float)block_max((double)m, red);
-    // nothing above -infinity: the differences below would be NaN for -infinity itself
-    if (m == -INFINITY) m = 0.0f;
-    sum = 0.0f;
-    for (int64_t j = tid; j < P.vocab; j += kThreads) sum += expf(fmaf(to_f32(z[j]), it, -m));
-    sum = (float)block_sum((double)sum, red);
-  }
-  const double logsum = log((double)sum);
+// A thread's teacher entries i = tid + q Threads of one row.  id -1: absent,
+// as is an entry of value -infinity (p = 0) or past the vocabulary (bad).
+template <int Threads> struct Entries {
+  static constexpr int kPer = kTop / Threads;
+  int id[kPer];
+  float v[kPer], z[kPer];
+  int bad;
+  uint32_t raw_lo[kPer], raw_hi[kPer], raw_v[kPer];
 
-  double term = 0.0;
-  for (int i = tid; i < P.k; i += kThreads) {
-    if (s_id[i] < 0) continue;
-    const double lp = (double)s_p[i] * it - lsep;
-    const double p = exp(lp);
-    if (p != 0.0) term += p * (lp - ((double)s_z[i] * it - m - logsum));
-    s_p[i] = (float)p;
-  }
-  if constexpr (!Backward) {
-    term = block_sum(term, red);
-    if (tid == 0) {
-      P.loss[row] = bad ? NAN : (float)(term * w);
-      if (P.stats) {
-        P.stats[2 * row] = m;
-        P.stats[2 * row + 1] = sum;
+  // Issues the loads (nothing waits for them here) ...
+  __device__ __forceinline__ void load(const DistillParams& P, int64_t row) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int i = threadIdx.x + q * Threads;
+      raw_lo[q] = raw_hi[q] = raw_v[q] = 0;
+      if (i < P.k) {
+        if (P.ids64) {
+          const uint2 t = static_cast<const uint2*>(P.ids)[row * P.ldi + i];
+          raw_lo[q] = t.x;
+          raw_hi[q] = t.y;
+        } else {
+          raw_lo[q] = static_cast<const uint32_t*>(P.ids)[row * P.ldi + i];
+        }
+        if (P.values_dtype == kInF32) raw_v[q] = static_cast<const uint32_t*>(P.values)[row * P.ldv + i];
+        else raw_v[q] = static_cast<const uint16_t*>(P.values)[row * P.ldv + i];
       }
     }
   }
-  if (!P.dz) return;
-  __syncthreads();
-  const float c = bad ? NAN : (Backward ? P.dloss[row] : 1.0f) * w / P.temperature;
-  const float inv = 1.0f / sum;
-  for (int64_t j = tid; j < P.vocab; j += kThreads)
-    dz[j] = from_f32<T>(c * (expf(fmaf(to_f32(z[j]), it, -m)) * inv));
-  __syncthreads();
-  for (int i = tid; i < P.k; i += kThreads) {
-    const int id = s_id[i];
-    if (id < 0) continue;
-    float p = 0.0f;
-    for (int j = 0; j < P.k; ++j) p += s_id[j] == id ? s_p[j] : 0.0f;
-    dz[id] = from_f32<T>(c * (expf(fmaf(s_z[i], it, -m)) * inv - p));
+  // ... and takes what they brought.
+  __device__ __forceinline__ void decode(const DistillParams& P) {
+    bad = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int64_t t = P.ids64 ? (int64_t)(((uint64_t)raw_hi[q] << 32) | raw_lo[q]) : (int64_t)(int32_t)raw_lo[q];
+      const float x = P.values_dtype == kInF32    ? __uint_as_float(raw_v[q])
+                      : P.values_dtype == kInBF16 ? __uint_as_float(raw_v[q] << 16)
+                                                  : (float)__builtin_bit_cast(_Float16, (uint16_t)raw_v[q]);
+      const bool here = (int)threadIdx.x + q * Threads < P.k;
+      bad |= here && t >= P.vocab;
+      const bool present = here && t >= 0 && t < P.vocab && x != -INFINITY;
+      id[q] = present ? (int)t : -1;
+      v[q] = present ? x : -INFINITY;
+    }
+  }
+  // the student's logits of the entries in [lo, hi)
+  template <class T> __device__ __forceinline__ void gather(const T* zr, int lo, int hi) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      z[q] = 0.0f;
+      if (id[q] >= lo && id[q] < hi) z[q] = to_f32(zr[id[q]]);
+    }
+  }
+};
+
+// What the waves of a workgroup exchange for one row.
+template <int Waves> struct Joined {
+  float m[Waves], s[Waves], vm[Waves];
+  double ps[Waves], term[Waves];
+  int flags[Waves], dup;
+};
+
+// A wave's share of the teacher's softmax: its largest value, and the sum of
+// exponentials above it.
+template <int Threads>
+__device__ __forceinline__ void teacher_share(const Entries<Threads>& E, double it, float& vm, double& ps) {
+  vm = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < E.kPer; ++q) vm = fmaxf(vm, E.v[q]);
+  vm = wave_max(vm);
+  ps = 0.0;
+  if (__any(E.id[0] >= 0) || (E.kPer > 1 && vm != -INFINITY)) {
+#pragma unroll
+    for (int q = 0; q < E.kPer; ++q)
+      if (E.id[q] >= 0) ps += exp(((double)E.v[q] - (double)vm) * it);
+    ps = wave_sum(ps);
+  }
+}
+// The waves' shares joined, in every thread: vm, and log of the whole sum.
+template <int Waves>
+__device__ __forceinline__ void teacher_join(const Joined<Waves>& J, double it, float& vm, double& logps) {
+  const int l = threadIdx.x & 63;
+  const float x = l < Waves ? J.vm[l] : -INFINITY;
+  vm = wave_max(x);
+  logps = log(wave_sum(x == -INFINITY ? 0.0 : J.ps[l] * exp(((double)x - (double)vm) * it)));
+}
+
+// Whether two entries of ids[0 .. k) name the same word: groups of threads
+// compare each entry with a part of those before it.
+template <int Threads> __device__ __forceinline__ bool any_twice(const int* ids, int k) {
+  const int lg = k <= 64 ? 6 : 32 - __clz(k - 1);
+  const int groups = max(1, Threads >> lg);
+  const int g = lg < 31 ? threadIdx.x >> lg : 0;
+  bool twice = false;
+  if (g < groups) {
+    for (int i = threadIdx.x & ((1 << lg) - 1); i < k; i += Threads) {
+      const int id = ids[i];
+      const int j0 = (int)((int64_t)i * g / groups), j1 = (int)((int64_t)i * (g + 1) / groups);
+      for (int j = j0; j < j1; ++j) twice |= id >= 0 && ids[j] == id;
+    }
+  }
+  return twice;
+}
+
+// The entries' own elements of the gradient: c (q - p), p summed over the
+// entries of one word where any is named twice.
+template <int DT, int Threads>
+__device__ __forceinline__ void scatter(const DistillParams& P, const Entries<Threads>& E, const int* ids,
+                                        const float* ps, bool twice, typename Elem<DT>::type* dz, float m, float cl,
+                                        float inv, float c, int lo, int hi) {
+  typedef typename Elem<DT>::type T;
+#pragma unroll
+  for (int q = 0; q < E.kPer; ++q) {
+    const int id = E.id[q];
+    if (id < lo || id >= hi) continue;
+    float p;
+    if (twice) {
+      p = 0.0f;
+      for (int j = 0; j < P.k; ++j) p += ids[j] == id ? ps[j] : 0.0f;
+    } else {
+      p = ps[threadIdx.x + q * Threads];
+    }
+    dz[id] = from_f32<T>(c * (__builtin_amdgcn_exp2f((E.z[q] - m) * cl) * inv - p));
   }
 }
 
-template <bool Backward> hipError_t launch(const DistillParams& P, int dtype, hipStream_t stream) {
-  const unsigned grid = (unsigned)P.n;
-  if (dtype == kInBF16) distill_row<kInBF16, Backward><<<grid, kThreads, 0, stream>>>(P);
-  else if (dtype == kInF16) distill_row<kInF16, Backward><<<grid, kThreads, 0, stream>>>(P);
-  else distill_row<kInF32, Backward><<<grid, kThreads, 0, stream>>>(P);
+// Adds N values to a running maximum and sum of exponentials (float32).
+template <int N> __device__ __forceinline__ void online(const float (&v)[N], float cl, float& m, float& s) {
+  float a = m;
+#pragma unroll
+  for (int e = 0; e < N; ++e) a = fmaxf(a, v[e]);
+  float t = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) t += __builtin_amdgcn_exp2f((v[e] - a) * cl);
+  s = s * __builtin_amdgcn_exp2f((m - a) * cl) + t;
+  m = a;
+}
+
+// The waves' maxima and sums joined, in every thread.
+template <int Waves> __device__ __forceinline__ void student_join(const Joined<Waves>& J, float cl, float& m, float& s) {
+  const int l = threadIdx.x & 63;
+  const float x = l < Waves ? J.m[l] : -FLT_MAX;
+  m = wave_max(x);
+  s = (float)wave_sum(l < Waves ? (double)(J.s[l] * __builtin_amdgcn_exp2f((x - m) * cl)) : 0.0);
+}
+
+struct Scales {
+  float cl;   // log2(e) / T
+  double it;  // the same scale to base e
+};
+__device__ __forceinline__ Scales scales(const DistillParams& P) {
+  const float cl = (float)(1.4426950408889634 / (double)P.temperature);
+  return {cl, (double)cl * 0.69314718055994531};
+}
+
+// Loss and gradient of a row of at most Threads * NV whole vectors; the fewer
+// than one vector's elements after them go to the first threads, one each.
+template <int DT, int Threads, int NV>
+__global__ void __launch_bounds__(Threads, 4) distill_resident(DistillParams P) {
+  typedef typename Elem<DT>::type T;
+  typedef Vec<DT> V;
+  constexpr int kWaves = Threads / 64;
+  __shared__ Joined<kWaves> J;
+  __shared__ int s_id[kTop];
+  __shared__ float s_p[kTop];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int vocab = (int)P.vocab, nvec = vocab / V::N;
+  const int last = nvec * V::N + tid;  // this thread's element past the vectors
+  const auto [cl, it] = scales(P);
+  const int64_t row = blockIdx.x;
+  const T* z = static_cast<const T*>(P.z) + row * P.ldz;
+  T* dz = static_cast<T*>(P.dz) + row * P.lddz;
+  const float w = P.weight ? P.weight[row] : 1.0f;
+
+  // Vector i of this thread: waves past the row's end do nothing, lanes past
+  // it take the last vector (and are left out of the sums and stores).  The
+  // thread index is made opaque in each loop, so that offsets are computed
+  // where they are used and not kept for all vectors at once.
+  auto wave_in = [&](int i) { return i * Threads + wave * 64 < nvec; };
+  auto opaque_tid = [&] {
+    int t = tid;
+    asm volatile("" : "+v"(t));
+    return t;
+  };
+
+  u32x4 v[NV];
+  float rest = -INFINITY, m = -FLT_MAX, sum = 0.0f, c = 0.0f;
+  Entries<Threads> E;
+  int all = 0;
+  if (w != 0.0f) {
+    E.load(P, row);
+    int t = opaque_tid();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (wave_in(i)) v[i] = *reinterpret_cast<const typename V::U*>(z + min(i * Threads + t, nvec - 1) * V::N);
+    if (last < vocab) rest = to_f32(z[last]);
+    E.decode(P);
+    E.gather(z, 0, vocab);
+    t = opaque_tid();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (wave_in(i)) {
+        float x[V::N];
+        V::get(v[i], x);
+        float a = m, b = sum;
+        online(x, cl, a, b);
+        const bool in = i * Threads + t < nvec;
+        m = in ? a : m;
+        sum = in ? b : sum;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const float one[1] = {rest};
+    if (last < vocab) online(one, cl, m, sum);
+    float vm;
+    double ps;
+    teacher_share(E, it, vm, ps);
+    int present = 0;
+#pragma unroll
+    for (int q = 0; q < E.kPer; ++q) {
+      present |= E.id[q] >= 0;
+      if (tid + q * Threads < P.k) s_id[tid + q * Threads] = E.id[q];
+    }
+    const float wm = wave_max(m);
+    const float wsum = wave_sum(sum * __builtin_amdgcn_exp2f((m - wm) * cl));
+    const int flags = (__any(present) ? 1 : 0) | (__any(E.bad) ? 2 : 0);
+    if ((tid & 63) == 0) {
+      J.m[wave] = wm;
+      J.s[wave] = wsum;
+      J.vm[wave] = vm;
+      J.ps[wave] = ps;
+      J.flags[wave] = flags;
+      if (wave == 0) J.dup = 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kWaves; ++q) all |= J.flags[q];
+    all = __builtin_amdgcn_readfirstlane(all);
+  }
+  if (!(all & 1)) {
+    const float g[V::N] = {};
+#pragma unroll 1
+    for (int j = tid; j < nvec; j += Threads) V::store_whole(dz + j * V::N, g);
+    if (last < vocab) dz[last] = from_f32<T>(0.0f);
+    if (tid == 0) P.loss[row] = 0.0f;
+    if (P.stats && tid < 2) P.stats[2 * row + tid] = 0.0f;
+    return;
+  }
+  student_join(J, cl, m, sum);
+  {
+    double logps;
+    float vm;
+    teacher_join(J, it, vm, logps);
+    const double logsum = log((double)sum);
+    double term = 0.0;
+#pragma unroll
+    for (int q = 0; q < E.kPer; ++q) {
+      if (E.id[q] < 0) continue;
+      const double lp = ((double)E.v[q] - (double)vm) * it - logps;
+      const double p = exp(lp);
+      if (p != 0.0) term += p * (lp - (((double)E.z[q] - (double)m) * it - logsum));
+      s_p[tid + q * Threads] = (float)p;
+    }
+    if (wave * 64 < P.k) term = wave_sum(term);
+    if ((tid & 63) == 0) J.term[wave] = term;
+    if (any_twice<Threads>(s_id, P.k)) J.dup = 1;
+    c = (all & 2) ? NAN : w / P.temperature;
+  }
+  const float inv = 1.0f / sum, f = c * inv;
+  const int t = opaque_tid();
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (wave_in(i)) {
+      // opaque: the values unpacked above are not kept for here
+      asm volatile("" : "+v"(v[i]));
+      float g[V::N];
+      V::get(v[i], g);
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) g[e] = __builtin_amdgcn_exp2f((g[e] - m) * cl) * f;
+      if (i * Threads + t < nvec) V::store_whole(dz + (i * Threads + t) * V::N, g);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (last < vocab) dz[last] = from_f32<T>(__builtin_amdgcn_exp2f((rest - m) * cl) * f);
+  __syncthreads();
+  if (tid == 0) {
+    double l = 0.0;
+    for (int q = 0; q < kWaves && q * 64 < P.k; ++q) l += J.term[q];
+    P.loss[row] = (all & 2) ? NAN : (float)(l * w);
+    if (P.stats) {
+      P.stats[2 * row] = m;
+      P.stats[2 * row + 1] = sum;
+    }
+  }
+  scatter<DT, Threads>(P, E, s_id, s_p, J.dup != 0, dz, m, cl, inv, c, 0, vocab);
+}
+
+// The loss, and the row's maximum and sum: one workgroup a row.
+template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) distill_loss(DistillParams P) {
+  typedef typename Elem<DT>::type T;
+  typedef Vec<DT> V;
+  constexpr int kWaves = Threads / 64, kUnroll = 8;
+  __shared__ Joined<kWaves> J;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const auto [cl, it] = scales(P);
+  const int64_t row = blockIdx.x;
+  const T* z = static_cast<const T*>(P.z) + row * P.ldz;
+  const float w = P.weight ? P.weight[row] : 1.0f;
+  bool zero = w == 0.0f;
+  float m = -FLT_MAX, sum = 0.0f, vm;
+  double ps;
+  Entries<Threads> E;
+  int all = 0;
+  if (!zero) {
+    E.load(P, row);
+    int64_t j = (int64_t)tid * V::N;
+    for (; j + (int64_t)((kUnroll - 1) * Threads + 1) * V::N <= P.vocab; j += (int64_t)kUnroll * Threads * V::N) {
+      u32x4 v[kUnroll];
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) v[i] = V::load(z, j + (int64_t)i * Threads * V::N, P.vocab);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        float x[V::N];
+        V::get(v[i], x);
+        online(x, cl, m, sum);
+      }
+    }
+    for (; j < P.vocab; j += (int64_t)Threads * V::N) {
+      float x[V::N];
+      V::get(V::load(z, j, P.vocab), x);
+      online(x, cl, m, sum);
+    }
+    E.decode(P);
+    E.gather(z, 0, (int)P.vocab);
+    teacher_share(E, it, vm, ps);
+    int present = 0;
+#pragma unroll
+    for (int q = 0; q < E.kPer; ++q) present |= E.id[q] >= 0;
+    const float wm = wave_max(m);
+    const float wsum = wave_sum(sum * __builtin_amdgcn_exp2f((m - wm) * cl));
+    const int flags = (__any(present) ? 1 : 0) | (__any(E.bad) ? 2 : 0);
+    if ((tid & 63) == 0) {
+      J.m[wave] = wm;
+      J.s[wave] = wsum;
+      J.vm[wave] = vm;
+      J.ps[wave] = ps;
+      J.flags[wave] = flags;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kWaves; ++q) all |= J.flags[q];
+    zero = !(all & 1);
+  }
+  if (zero) {
+    if (tid == 0) P.loss[row] = 0.0f;
+    if (P.stats && tid < 2) P.stats[2 * row + tid] = 0.0f;
+    return;
+  }
+  student_join(J, cl, m, sum);
+  double logps;
+  teacher_join(J, it, vm, logps);
+  const double logsum = log((double)sum);
+  double term = 0.0;
+#pragma unroll
+  for (int q = 0; q < E.kPer; ++q) {
+    if (E.id[q] < 0) continue;
+    const double lp = ((double)E.v[q] - (double)vm) * it - logps;
+    const double p = exp(lp);
+    if (p != 0.0) term += p * (lp - (((double)E.z[q] - (double)m) * it - logsum));
+  }
+  term = wave_sum(term);
+  if ((tid & 63) == 0) J.term[wave] = term;
+  __syncthreads();
+  if (tid == 0) {
+    double t = 0.0;
+    for (int q = 0; q < kWaves; ++q) t += J.term[q];
+    P.loss[row] = (all & 2) ? NAN : (float)(t * w);
+    if (P.stats) {
+      P.stats[2 * row] = m;
+      P.stats[2 * row + 1] = sum;
+    }
+  }
+}
+
+// The gradient from the row's maximum and sum: workgroup (row, part) does a
+// chunk of the row and the teacher's entries inside it.
+constexpr int kGradThreads = 512, kGradChunk = 16;  // vectors a thread
+template <int DT> __global__ void __launch_bounds__(kGradThreads, 4) distill_grad(DistillParams P, int parts) {
+  typedef typename Elem<DT>::type T;
+  typedef Vec<DT> V;
+  constexpr int Threads = kGradThreads, kWaves = Threads / 64, kUnroll = 8;
+  __shared__ Joined<kWaves> J;
+  __shared__ int s_id[kTop];
+  __shared__ float s_p[kTop];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const auto [cl, it] = scales(P);
+  const int64_t row = blockIdx.x / (unsigned)parts;
+  const int part = blockIdx.x - (unsigned)row * (unsigned)parts;
+  const int64_t per = ((P.vocab + (int64_t)parts * V::N - 1) / ((int64_t)parts * V::N)) * V::N;
+  const int64_t lo = part * per, hi = min(P.vocab, lo + per);
+  const T* z = static_cast<const T*>(P.z) + row * P.ldz;
+  T* dz = static_cast<T*>(P.dz) + row * P.lddz;
+  const float w = P.weight ? P.weight[row] : 1.0f;
+  bool zero = w == 0.0f;
+  float m = 0.0f, c = 0.0f, inv = 0.0f;
+  Entries<Threads> E;
+  if (!zero) {
+    E.load(P, row);
+    m = P.stats[2 * row];
+    inv = 1.0f / P.stats[2 * row + 1];
+    E.decode(P);
+    E.gather(z, (int)lo, (int)hi);
+    float vm;
+    double ps;
+    teacher_share(E, it, vm, ps);
+    int present = 0;
+#pragma unroll
+    for (int q = 0; q < E.kPer; ++q) {
+      present |= E.id[q] >= 0;
+      if (tid + q * Threads < P.k) s_id[tid + q * Threads] = E.id[q];
+    }
+    const int flags = (__any(present) ? 1 : 0) | (__any(E.bad) ? 2 : 0);
+    if ((tid & 63) == 0) {
+      J.vm[wave] = vm;
+      J.ps[wave] = ps;
+      J.flags[wave] = flags;
+      if (wave == 0) J.dup = 0;
+    }
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int q = 0; q < kWaves; ++q) all |= J.flags[q];
+    zero = !(all & 1);
+    c = (all & 2) ? NAN : (P.dloss ? P.dloss[row] : 1.0f) * w / P.temperature;
+    if (!zero) {
+      double logps;
+      teacher_join(J, it, vm, logps);
+#pragma unroll
+      for (int q = 0; q < E.kPer; ++q)
+        if (E.id[q] >= 0) s_p[tid + q * Threads] = (float)exp(((double)E.v[q] - (double)vm) * it - logps);
+      if (any_twice<Threads>(s_id, P.k)) J.dup = 1;
+    }
+  }
+  const float f = c * inv;
+  int64_t j = lo + (int64_t)tid * V::N;
+  for (; j < hi; j += (int64_t)kUnroll * Threads * V::N) {
+    u32x4 v[kUnroll];
+    if (!zero) {
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) v[i] = V::load(z, j + (int64_t)i * Threads * V::N, hi);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int64_t e0 = j + (int64_t)i * Threads * V::N;
+      float g[V::N];
+      if (zero) {
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) g[e] = 0.0f;
+      } else {
+        V::get(v[i], g);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) g[e] = __builtin_amdgcn_exp2f((g[e] - m) * cl) * f;
+      }
+      if (e0 < hi) V::store(dz, e0, hi, g);
+    }
+  }
+  if (zero) return;
+  __syncthreads();
+  scatter<DT, Threads>(P, E, s_id, s_p, J.dup != 0, dz, m, cl, inv, c, (int)lo, (int)hi);
+}
+
+template <int DT> constexpr int64_t resident_limit() { return (int64_t)1024 * 16 * Vec<DT>::N; }
+
+template <int DT, int Threads, int NV> void launch_resident(const DistillParams& P, hipStream_t stream) {
+  distill_resident<DT, Threads, NV><<<(unsigned)P.n, Threads, 0, stream>>>(P);
+}
+
+template <int DT> void launch_loss(const DistillParams& P, hipStream_t stream) {
+  // few rows, or long ones: more threads a row
+  if (P.n <= 512 && P.vocab > 16384) distill_loss<DT, 1024><<<(unsigned)P.n, 1024, 0, stream>>>(P);
+  else if (P.vocab > 8192) distill_loss<DT, 512><<<(unsigned)P.n, 512, 0, stream>>>(P);
+  else distill_loss<DT, 256><<<(unsigned)P.n, 256, 0, stream>>>(P);
+}
+
+template <int DT> void launch_grad(const DistillParams& P, hipStream_t stream) {
+  const int64_t chunk = (int64_t)kGradThreads * kGradChunk * Vec<DT>::N;
+  int64_t parts = (P.vocab + chunk - 1) / chunk;
+  // a grid has fewer than 2^31 workgroups
+  while (parts > 1 && parts * P.n >= ((int64_t)1 << 31)) parts = (parts + 1) / 2;
+  distill_grad<DT><<<(unsigned)(P.n * parts), kGradThreads, 0, stream>>>(P, (int)parts);
+}
+
+template <int DT> hipError_t launch(DistillParams P, hipStream_t stream) {
+  if (!P.dz) {
+    launch_loss<DT>(P, stream);
+    return hipGetLastError();
+  }
+  const int64_t vecs = (P.vocab + Vec<DT>::N - 1) / Vec<DT>::N;
+  if (P.vocab > resident_limit<DT>()) {
+    if (!P.stats) P.stats = static_cast<float*>(P.work);
+    launch_loss<DT>(P, stream);
+    launch_grad<DT>(P, stream);
+  } else if (vecs <= 1024) {
+    launch_resident<DT, 256, 4>(P, stream);
+  } else if (P.n <= 256) {
+    // a row for each CU: all its waves on it
+    if (vecs <= 4096) launch_resident<DT, 1024, 4>(P, stream);
+    else launch_resident<DT, 1024, 16>(P, stream);
+  } else if (vecs <= 4096) {
+    launch_resident<DT, 256, 16>(P, stream);
+  } else if (vecs <= 8192) {
+    launch_resident<DT, 512, 16>(P, stream);
+  } else {
+    launch_resident<DT, 1024, 16>(P, stream);
+  }
+  return hipGetLastError();
+}
+
+template <int DT> hipError_t backward(const DistillParams& P, hipStream_t stream) {
+  launch_grad<DT>(P, stream);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t distill_workspace(int64_t n, int64_t vocab, int dtype) { return 0; }
+// Rows too long for the registers keep their statistics between two launches.
+int64_t distill_workspace(int64_t n, int64_t vocab, int dtype) {
+  const int64_t limit = dtype == kInF32 ? resident_limit<kInF32>() : resident_limit<kInBF16>();
+  return vocab > limit ? n * 8 : 0;
+}
 
 hipError_t launch_distill(const DistillParams& P, int dtype, hipStream_t stream) {
-  return launch<false>(P, dtype, stream);
+  if (dtype == kInBF16) return launch<kInBF16>(P, stream);
+  if (dtype == kInF16) return launch<kInF16>(P, stream);
+  return launch<kInF32>(P, stream);
 }
 hipError_t launch_distill_backward(const DistillParams& P, int dtype, hipStream_t stream) {
-  return launch<true>(P, dtype, stream);
+  if (dtype == kInBF16) return backward<kInBF16>(P, stream);
+  if (dtype == kInF16) return backward<kInF16>(P, stream);
+  return backward<kInF32>(P, stream);
 }
 
 }  // namespace hess

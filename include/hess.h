@@ -632,8 +632,8 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
  * hess_distill_topk -- loss, and optionally the row statistics for a later
  * backward call and the gradient with dloss = 1, in one call.
  *   loss      n floats.
- *   stats     n x 2 floats, or NULL: the maximum of logits / T over the row and
- *             the sum of exp(logits / T - maximum); zeros for rows not read.
+ *   stats     n x 2 floats, or NULL: the row's largest logit and the sum of
+ *             exp((logits - largest) / T); zeros for rows not read.
  *             (A pair, because their log-sum-exp alone would lose the sum
  *             where every logit is the type's lowest value.)
  *   dlogits   n x vocab of dtype, row stride lddz, or NULL.  May be logits
