@@ -51,6 +51,11 @@ hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int edge, int dtype, hipS
 // it up to that are zeros.
 hipError_t launch_ffn_tile16(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream);
 
+// The forward product of at most kFfnFew tokens: operands of any alignment, no
+// workspace.
+constexpr int64_t kFfnFew = 64;
+hipError_t launch_ffn_few(const FfnGemm& g, int dtype, hipStream_t stream);
+
 // Copies rows x cols 16-bit values (row stride ld) to rows of pad >= cols (a
 // multiple of 8) values, zeros past cols.
 hipError_t launch_pack_rows16(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t pad,

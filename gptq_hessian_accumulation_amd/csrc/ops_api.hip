@@ -106,6 +106,7 @@ struct FfnWork {
 };
 FfnWork ffn_work(int64_t n, int64_t d, int64_t f, int dtype, bool backward) {
   FfnWork w{};
+  if (!backward && n <= kFfnFew) return w;
   w.pack = backward ? up(n * 2 * up(f, 8) * elem_bytes(dtype), 256) : 0;
   w.slots = w.pack + (packed(d, dtype) ? pack_bytes(n, d) + 2 * pack_bytes(f, d) : 0);
   w.total = w.slots + (backward ? std::max(slot_bytes(shape(n, d, f), kFfnDx, dtype),
@@ -178,7 +179,9 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* base = static_cast<char*>(work);
   FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
-  if (int rc = place_operands(o, base, n, f, dtype, true, true, s)) return rc;
+  const bool few = n <= kFfnFew;
+  if (!few)
+    if (int rc = place_operands(o, base, n, f, dtype, true, true, s)) return rc;
   FfnGemm g = shape(n, f, o.d);
   g.a = o.x;
   g.lda = o.ldx;
@@ -190,12 +193,17 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
   g.ldo0 = ldh;
   g.o1 = preact;
   g.ldo1 = 2 * fp;
-  g.ws = reinterpret_cast<float*>(base + room.slots);
+  g.ws = few ? nullptr : reinterpret_cast<float*>(base + room.slots);
   g.f = f;
   g.fp = fp;
   g.act = act;
-  const int edge = ffn_schedule(g, kFfnFwd, dtype);
-  const hipError_t e = launch_ffn_gemm(g, kFfnFwd, edge, dtype, s);
+  hipError_t e;
+  if (few) {
+    e = launch_ffn_few(g, dtype, s);
+  } else {
+    const int edge = ffn_schedule(g, kFfnFwd, dtype);
+    e = launch_ffn_gemm(g, kFfnFwd, edge, dtype, s);
+  }
   return e == hipSuccess ? HESS_OK : hip_fail(e, "gated feed-forward launch");
 }
 
