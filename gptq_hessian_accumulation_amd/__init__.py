@@ -633,8 +633,9 @@ def _ffn_args(x, w_gate, w_up):
     for name, t in (("w_gate", w_gate), ("w_up", w_up)):
         if t.dtype != x.dtype or t.device != x.device:
             raise ValueError(f"{name} must have x's dtype and device")
-    # the tiles read 16-bit rows of a multiple of 8 values where they are, if they start at 16 bytes
-    step = 8 if code != HESS_F32 and d % 8 == 0 else 1
+    # the tiles read rows of a multiple of 16 bytes where they are, if they start at 16 bytes
+    step = 4 if code == HESS_F32 else 8
+    step = step if d % step == 0 else 1
     x2, ldx = _rows(x.reshape(-1, d) if x.dim() != 2 else x, step)
     wg, ldg = _rows(w_gate, step)
     wu, ldu = _rows(w_up, step)

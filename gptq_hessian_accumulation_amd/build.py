@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhess.so")
 
 SOURCES = ["hess_api.hip", "chol.hip", "quant.hip", "syrk.hip", "syrk_big.hip", "syrk_thin.hip", "materialize.hip", "local_blocks.hip", "stage.hip",
-           "imatrix.hip", "ops_api.hip", "gated_ffn.hip", "gated_ffn16.hip", "ffn_few.hip",
+           "imatrix.hip", "ops_api.hip", "gated_ffn.hip", "ffn_tile.hip", "ffn_few.hip",
            "distill.hip"]
 
 HIPCC_FLAGS = [

@@ -4,6 +4,7 @@
 
 #include "elem.hpp"
 #include "ffn_internal.hpp"
+#include "hess_device.hpp"
 #include "../../include/hess.h"
 
 namespace hess {
@@ -37,6 +38,23 @@ template <bool Exact> __device__ __forceinline__ void act_both(float g, int act,
     const float s = sigmoidf<Exact>(1.5957691216057308f * (g + 0.044715f * g * g * g));
     a = g * s;
     da = s + g * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
+  }
+}
+
+// acc += A B over 64 bytes of K, of which each 16-lane row holds a 16-byte
+// chunk (in float32 each instruction takes one value of every chunk).
+template <int DT> __device__ __forceinline__ f32x4 mma16(const u32x4& a, const u32x4& b, f32x4 acc) {
+  typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+  if constexpr (DT == kInBF16) {
+    return mfma16x16x32(a, b, acc);
+  } else if constexpr (DT == kInF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0,
+                                                  0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[j]), __uint_as_float(b[j]), acc, 0, 0, 0);
+    return acc;
   }
 }
 
@@ -109,14 +127,6 @@ __device__ __forceinline__ void tile_coords(const FfnGemm& P, int t, int& I, int
 __device__ __forceinline__ int item_of_block(int b, int n) {
   const int q = n >> 3, r = n & 7, x = b & 7;
   return x * q + min(x, r) + (b >> 3);
-}
-
-// Column b of a forward tile's B panel: which projection, and which of the
-// tile's features.  Each wave column (64 wide) holds 32 features' gate
-// columns, then their up columns.
-__device__ __forceinline__ void fwd_column(int b, int& up, int& col) {
-  up = (b >> 5) & 1;
-  col = (b >> 6) * 32 + (b & 31);
 }
 
 }  // namespace hess

@@ -19,24 +19,8 @@ namespace hess {
 
 namespace {
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
-
-// acc += A B over the 64 bytes of K that the 16-byte pieces of four lane rows
-// make up (in float32 each instruction takes one value of every piece).
-template <int DT> __device__ __forceinline__ void multiply(const u32x4& b, const u32x4& a, f32x4& acc) {
-  if constexpr (DT == kInBF16) {
-    acc = mfma16x16x32(b, a, acc);
-  } else if constexpr (DT == kInF16) {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), acc, 0, 0,
-                                                 0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[j]), __uint_as_float(a[j]), acc, 0, 0, 0);
-  }
-}
 
 template <class T> __device__ __forceinline__ u32x4 load16(const T* p) {
   if constexpr (sizeof(T) == 2) return *reinterpret_cast<const u32x4_at2*>(p);
@@ -95,7 +79,7 @@ template <int DT, int MB, int FB, int W, int U> __global__ void __launch_bounds_
 #pragma unroll
       for (int p = 0; p < 2 * FB; ++p)
 #pragma unroll
-        for (int q = 0; q < MB; ++q) multiply<DT>(vb[i][p], va[i][q], acc[p][q]);
+        for (int q = 0; q < MB; ++q) acc[p][q] = mma16<DT>(vb[i][p], va[i][q], acc[p][q]);
     u += C;
   };
   while (u + U <= u1) go(std::integral_constant<int, U>());
@@ -110,7 +94,7 @@ template <int DT, int MB, int FB, int W, int U> __global__ void __launch_bounds_
     for (int p = 0; p < 2 * FB; ++p) {
       const u32x4 vb = load_part(b[p] + (int64_t)units * kUnit, left);
 #pragma unroll
-      for (int q = 0; q < MB; ++q) multiply<DT>(vb, va[q], acc[p][q]);
+      for (int q = 0; q < MB; ++q) acc[p][q] = mma16<DT>(vb, va[q], acc[p][q]);
     }
   }
 #pragma unroll

@@ -37,19 +37,12 @@ struct FfnGemm {
   int tm, tn, ntiles, full, parts, part_len, niter;
 };
 
-// Tiles: float32 operands 128 x 128 by steps of 16 in K, 16-bit operands 256 or
-// 128 by steps of 32.
-constexpr int kFfnStep32 = 16, kFfnStep16 = 32;
-constexpr int kFfnEdge32 = 128;
-
 // Chooses the tile's edge (returned) and fills the schedule.
 int ffn_schedule(FfnGemm& g, int mode, int dtype);
 
+// One product by tiles.  Every operand row 16-byte aligned; where an operand's
+// rows run along K, K is a whole number of 16-byte pieces.
 hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream);
-// The tiles of 16-bit operands.  Every operand row 16-byte aligned; where an
-// operand's rows run along K, K is a multiple of 8 and the row's elements past
-// it up to that are zeros.
-hipError_t launch_ffn_tile16(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream);
 
 // The forward product of at most kFfnFew tokens: operands of any alignment, no
 // workspace.

@@ -1,8 +1,10 @@
-// The gated feed-forward block's products on 16-bit operands: tiles of edge
-// 256 or 128 on v_mfma_f32_16x16x32 (bf16 or fp16), float32 accumulators.
+// The gated feed-forward block's products: tiles of edge 256 or 128 with
+// float32 accumulators, on v_mfma_f32_16x16x32 (bf16 or fp16) or, for float32
+// operands, v_mfma_f32_16x16x4_f32.  A stage is 64 bytes of K: 32 values of a
+// 16-bit type, 16 of float32.
 //
 //  * 8 waves of 128 x 64 (edge 256) or 4 of 64 x 64 (edge 128), one matrix
-//    instruction per 16 x 16 accumulator and stage of 32 values of K.  Two
+//    instruction (float32: four) per 16 x 16 accumulator and stage.  Two
 //    waves share each SIMD (edge 128: two workgroups a CU), so that one's
 //    waits are covered by the other's matrix instructions.  The B
 //    operand goes first, so that a lane holds four consecutive columns; two
@@ -16,7 +18,8 @@
 //    gradient pair for dx) is kept row by row, 64 bytes a row, its 16-byte
 //    chunks XOR-swizzled by bits 1-2 of the row, and read with ds_read_b128.
 //    One whose rows run across K (the weights for dx, both operands of dW)
-//    is kept k by k and read transposed with ds_read_b64_tr_b16.
+//    is kept k by k and read transposed with ds_read_b64_tr_b16 (float32:
+//    value by value).
 //  * Loads need no masks: rows and columns past the matrix get an offset past
 //    every descriptor's range, k past the matrix or past the part of K a
 //    workgroup was given lies outside the descriptor (or its chunk's offset
@@ -29,32 +32,27 @@ namespace hess {
 
 namespace {
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
-template <int DT> __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
-  if constexpr (DT == kInBF16)
-    return mfma16x16x32(a, b, c);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
-                                                  0);
-}
-
 constexpr uint32_t kOOB = 0x80000000u;  // an offset past any descriptor's range
 constexpr int64_t kAll = 0x7fffffff;
 constexpr int kStages = 5, kAhead = 4;
 
 template <int DT, int Mode, int Edge>
-__global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
+__global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
   constexpr bool kRowsA = Mode != kFfnDw;  // A's rows run along K
   constexpr bool kRowsB = Mode == kFfnFwd;
   constexpr int kColWaves = Edge / 64;     // the tile's waves are 2 x kColWaves
   constexpr int kBm = Edge / 32, kBn = 4;  // 16-wide blocks of a wave
-  constexpr int kPanel = Edge * kFfnStep16 * 2;
+  constexpr int kSize = Elem<DT>::size;
+  constexpr int kStep = 64 / kSize, kPiece = 16 / kSize;  // values of K in a stage and a 16-byte chunk
+  constexpr int kPanel = Edge * 64;
   constexpr int kStage = 2 * kPanel;
   constexpr int kLoads = 2;                // 1-KB loads per wave, panel and stage
-  constexpr int kRow = Edge * 2;           // bytes of one k of a panel kept k by k
+  constexpr int kRow = Edge * kSize;           // bytes of one k of a panel kept k by k
   constexpr int kPerK = 1024 / kRow;       // k's in one load of such a panel
   __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+  // place of a chunk of columns in row k of a panel kept k by k; float32: the
+  // lane rows of a read (k = 4 g + j) land in four 64-byte parts of the banks
+  auto place = [](int k, int c) { return kSize == 2 ? chunk_pos(k, c) : c ^ (4 * ((k >> 2) & 3)); };
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -76,11 +74,11 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
   const int64_t i0 = (int64_t)I * Edge;
   const int64_t j0 = (int64_t)J * (Mode == kFfnFwd ? Edge / 2 : Edge);
   const int per_seg = Mode == kFfnDx ? P.niter / 2 : P.niter;
-  const int64_t rowA = P.lda * 2, rowB = P.ldb0 * 2;
+  const int64_t rowA = P.lda * kSize, rowB = P.ldb0 * kSize;
 
   // Offsets of this wave's loads.  Along K: load i holds 16 rows, lane l row
   // l / 4 of them and position l % 4, where chunk (l % 4) ^ (row / 2 % 4)
-  // lives.  Across K: load i holds kPerK values of k, the lane a chunk of 8
+  // lives.  Across K: load i holds kPerK values of k, the lane a chunk of
   // columns of one of them.
   const int chunk = (lane & 3) ^ ((lane >> 3) & 3);
   uint32_t voffA[kLoads], voffB[kLoads];
@@ -88,16 +86,16 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
   for (int i = 0; i < kLoads; ++i) {
     const int row = 16 * (kLoads * wave + i) + (lane >> 2);
     const int k = kPerK * (kLoads * wave + i) + lane / (64 / kPerK);
-    const int col = 8 * chunk_pos(k, lane % (64 / kPerK));
+    const int col = kPiece * place(k, lane % (64 / kPerK));
     if constexpr (kRowsA) voffA[i] = i0 + row < P.M ? (uint32_t)(row * rowA + chunk * 16) : kOOB;
-    else voffA[i] = i0 + col < P.M ? (uint32_t)(k * rowA + col * 2) : kOOB;
+    else voffA[i] = i0 + col < P.M ? (uint32_t)(k * rowA + col * kSize) : kOOB;
     if constexpr (kRowsB) {
       // the wave's B rows are of one projection (see fwd_column)
       const int feat = (wave >> 1) * 32 + 16 * i + (lane >> 2);
-      voffB[i] = j0 + feat < P.N ? (uint32_t)(feat * (int64_t)((wave & 1) ? P.ldb1 : P.ldb0) * 2 + chunk * 16) : kOOB;
+      voffB[i] = j0 + feat < P.N ? (uint32_t)(feat * (int64_t)((wave & 1) ? P.ldb1 : P.ldb0) * kSize + chunk * 16) : kOOB;
     } else {
       const int64_t ld = Mode == kFfnDx ? 0 : rowB;  // dx: the segment's stride, added per iteration
-      voffB[i] = j0 + col < P.N ? (uint32_t)(k * ld + col * 2) : kOOB;
+      voffB[i] = j0 + col < P.N ? (uint32_t)(k * ld + col * kSize) : kOOB;
     }
   }
   // dx reads two weights, whose strides may differ; the wave's k rows are
@@ -107,8 +105,8 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int k = kPerK * (kLoads * wave + i) + lane / (64 / kPerK);
-      voffB1[i] = voffB[i] == kOOB ? kOOB : voffB[i] + (uint32_t)(k * P.ldb1 * 2);
-      if (voffB[i] != kOOB) voffB[i] += (uint32_t)(k * P.ldb0 * 2);
+      voffB1[i] = voffB[i] == kOOB ? kOOB : voffB[i] + (uint32_t)(k * P.ldb1 * kSize);
+      if (voffB[i] != kOOB) voffB[i] += (uint32_t)(k * P.ldb0 * kSize);
     }
   }
 
@@ -120,24 +118,24 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
   auto describe = [&](int j) {
     Next d;
     d.seg = Mode == kFfnDx && j >= per_seg;
-    const int64_t k0 = (int64_t)(j - d.seg * per_seg) * kFfnStep16;
+    const int64_t k0 = (int64_t)(j - d.seg * per_seg) * kStep;
     const int64_t kend = Mode == kFfnDx ? P.fp : P.K;
     const bool live = j < it1;
-    d.lim = (int)((kend - k0 + 7) >> 3);
-    const int64_t valid = live ? max((int64_t)0, min((int64_t)kFfnStep16, P.K - k0)) : 0;
+    d.lim = (int)((kend - k0 + kPiece - 1) / kPiece);
+    const int64_t valid = live ? max((int64_t)0, min((int64_t)kStep, P.K - k0)) : 0;
     const uint64_t a = reinterpret_cast<uint64_t>(P.a);
     if constexpr (kRowsA)
-      d.ra = rsrc_words(a + (uint64_t)(i0 * rowA + (d.seg * P.fp + k0) * 2), live ? kAll : 0);
+      d.ra = rsrc_words(a + (uint64_t)(i0 * rowA + (d.seg * P.fp + k0) * kSize), live ? kAll : 0);
     else
-      d.ra = rsrc_words(a + (uint64_t)(k0 * rowA + i0 * 2), valid * rowA);
+      d.ra = rsrc_words(a + (uint64_t)(k0 * rowA + i0 * kSize), valid * rowA);
     if constexpr (kRowsB) {
       const uint64_t b = reinterpret_cast<uint64_t>((wave & 1) ? P.b1 : P.b0);
       const int64_t ld = (wave & 1) ? P.ldb1 : P.ldb0;
-      d.rb = rsrc_words(b + (uint64_t)((j0 * ld + k0) * 2), live ? kAll : 0);
+      d.rb = rsrc_words(b + (uint64_t)((j0 * ld + k0) * kSize), live ? kAll : 0);
     } else {
       const uint64_t b = reinterpret_cast<uint64_t>(d.seg ? P.b1 : P.b0);
       const int64_t ld = d.seg ? P.ldb1 : P.ldb0;
-      d.rb = rsrc_words(b + (uint64_t)((k0 * ld + j0) * 2), valid * ld * 2);
+      d.rb = rsrc_words(b + (uint64_t)((k0 * ld + j0) * kSize), valid * ld * kSize);
     }
     return d;
   };
@@ -156,25 +154,31 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
     for (int i = 0; i < 2 * kLoads; ++i) load1(stage, d, i);
   };
 
-  // Operand block m of a panel half: lane l holds row (or column) l % 16 of
-  // the block, k = 8 (l / 16) .. + 7.
-  const int rowpos = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
-  const int tl = 8 * (lane >> 4) + ((lane & 15) >> 2);
-  // The block enters as 1024 m (rows) or, by the XOR of the chunks, as a flip
-  // of the bits 5-7 of the address (16 m columns are 2 m chunks).
+  // Operand block m of a wave's share: lane l holds row (or column) l % 16 of
+  // the block, the l / 16-th chunk of K.  The block enters as 1024 m (rows)
+  // or, by the XOR of the chunks, as a flip of address bits (16 m columns are
+  // 2 m or 4 m chunks).
+  const int tl = kPiece * (lane >> 4) + (kSize == 2 ? (lane & 15) >> 2 : 0);
   auto lane_pos = [&](bool rows, int col0) {
-    if (rows) return col0 * 64 + rowpos;
-    const int c = (col0 + 4 * (lane & 3)) >> 3;
-    return tl * kRow + (chunk_pos(tl, c) << 4) + 8 * (lane & 1);
+    if (rows) return col0 * 64 + (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
+    const int col = col0 + (kSize == 2 ? 4 * (lane & 3) : lane & 15);
+    return tl * kRow + (place(tl, col / kPiece) << 4) + (col % kPiece) * kSize;
   };
   const int posA = lane_pos(kRowsA, wr * (Edge / 2)), posB = lane_pos(kRowsB, wc * 64);
   auto read1 = [&](const char* stage, int pos, int m, bool rows) {
     if (rows) return *reinterpret_cast<const u32x4*>(stage + pos + m * 1024);
-    const char* p = stage + (pos ^ (m << 5));
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HESS_LDS s16x4*)(p));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HESS_LDS s16x4*)(p + 4 * kRow));
-    const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
-    return u32x4{a.x, a.y, b.x, b.y};
+    const char* p = stage + (pos ^ (m << (kSize == 2 ? 5 : 6)));
+    if constexpr (kSize == 2) {
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HESS_LDS s16x4*)(p));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HESS_LDS s16x4*)(p + 4 * kRow));
+      const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+      return u32x4{a.x, a.y, b.x, b.y};
+    } else {
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = *reinterpret_cast<const uint32_t*>(p + j * kRow);
+      return o;
+    }
   };
   auto read_a = [&](uint32_t stage, int m) { return read1(lds + stage, posA, m, kRowsA); };
   auto read_b = [&](uint32_t stage, int n) { return read1(lds + stage + kPanel, posB, n, kRowsB); };
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
 #pragma unroll
     for (int m = 0; m < kBm; ++m) {
 #pragma unroll
-      for (int n = 0; n < kBn; ++n) acc[m][n] = mfma16<DT>(b[n], a[m & 3], acc[m][n]);
+      for (int n = 0; n < kBn; ++n) acc[m][n] = mma16<DT>(b[n], a[m & 3], acc[m][n]);
       a[m & 3] = m + 4 < kBm ? read_a(cur, m + 4) : read_a(nxt, m + 4 - kBm);
       if (m >= kBm - kBn) c[m - (kBm - kBn)] = read_b(nxt, m - (kBm - kBn));
       if (kBm == 4 || (m & 1)) load1(lds0 + target, d, kBm == 4 ? m : m >> 1);
@@ -287,16 +291,57 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile16(FfnGemm P) {
   }
 }
 
-template <int DT, int Mode> void launch_mode(const FfnGemm& g, int edge, hipStream_t stream) {
-  const int tail = g.ntiles - g.full;
-  if (edge == 256) ffn_tile16<DT, Mode, 256><<<g.full + tail * g.parts, 512, 0, stream>>>(g);
-  else ffn_tile16<DT, Mode, 128><<<g.full + tail * g.parts, 256, 0, stream>>>(g);
+// Split tiles: the parts' sums added in part order, then the epilogue.  Block
+// (t, s) handles rows s * (1024 / Edge) .. of tile full + t; a thread takes
+// four columns (forward: of both projections).
+template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn_join(FfnGemm P) {
+  const int tail = P.ntiles - P.full, t = blockIdx.x;
+  int I, J;
+  tile_coords(P, P.full + t, I, J);
+  constexpr int kQuads = Mode == kFfnFwd ? Edge / 8 : Edge / 4;  // quads of columns per row
+  const int id = blockIdx.y * 256 + threadIdx.x;
+  const int row = id / kQuads, quad = id % kQuads;
+  const float* W = P.ws + (int64_t)t * (Edge * Edge) + row * Edge;
+  const int64_t stride = (int64_t)tail * (Edge * Edge);
+  if constexpr (Mode == kFfnFwd) {
+    const int w = quad >> 3, q = quad & 7;  // wave column, quad of its features
+    const int cg = w * 64 + 4 * q;
+    float g[4] = {}, u[4] = {};
+    for (int p = 0; p < P.parts; ++p) {
+      const float4 a = *reinterpret_cast<const float4*>(W + p * stride + cg);
+      const float4 b = *reinterpret_cast<const float4*>(W + p * stride + cg + 32);
+      g[0] += a.x, g[1] += a.y, g[2] += a.z, g[3] += a.w;
+      u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
+    }
+    put_fwd<DT>(P, (int64_t)I * Edge + row, (int64_t)J * (Edge / 2) + w * 32 + 4 * q, g, u);
+  } else {
+    float v[4] = {};
+    for (int p = 0; p < P.parts; ++p) {
+      const float4 a = *reinterpret_cast<const float4*>(W + p * stride + 4 * quad);
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+    }
+    put<DT, Mode>(P, (int64_t)I * Edge + row, (int64_t)J * Edge + 4 * quad, v);
+  }
 }
 
-template <int DT> void launch_type(const FfnGemm& g, int mode, int edge, hipStream_t stream) {
-  if (mode == kFfnFwd) launch_mode<DT, kFfnFwd>(g, edge, stream);
-  else if (mode == kFfnDx) launch_mode<DT, kFfnDx>(g, edge, stream);
-  else launch_mode<DT, kFfnDw>(g, edge, stream);
+template <int DT, int Mode, int Edge> void launch_edge(const FfnGemm& g, hipStream_t stream) {
+  const int tail = g.ntiles - g.full;
+  ffn_tile<DT, Mode, Edge><<<g.full + tail * g.parts, 2 * Edge, 0, stream>>>(g);
+  if (tail == 0) return;
+  constexpr int quads = Mode == kFfnFwd ? Edge / 8 : Edge / 4;
+  ffn_join<DT, Mode, Edge><<<dim3(tail, Edge * quads / 256), 256, 0, stream>>>(g);
+}
+
+template <int DT, int Mode> hipError_t launch_mode(const FfnGemm& g, int edge, hipStream_t stream) {
+  if (edge == 256) launch_edge<DT, Mode, 256>(g, stream);
+  else launch_edge<DT, Mode, 128>(g, stream);
+  return hipGetLastError();
+}
+
+template <int DT> hipError_t launch_type(const FfnGemm& g, int mode, int edge, hipStream_t stream) {
+  if (mode == kFfnFwd) return launch_mode<DT, kFfnFwd>(g, edge, stream);
+  if (mode == kFfnDx) return launch_mode<DT, kFfnDx>(g, edge, stream);
+  return launch_mode<DT, kFfnDw>(g, edge, stream);
 }
 
 // Row r of a matrix of `cols` 16-bit values to a row of `pad` (a multiple of
@@ -323,10 +368,10 @@ __global__ void __launch_bounds__(256) pack_rows16(const uint16_t* src, int64_t 
 
 }  // namespace
 
-hipError_t launch_ffn_tile16(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream) {
-  if (dtype == kInBF16) launch_type<kInBF16>(g, mode, edge, stream);
-  else launch_type<kInF16>(g, mode, edge, stream);
-  return hipGetLastError();
+hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream) {
+  if (dtype == kInBF16) return launch_type<kInBF16>(g, mode, edge, stream);
+  if (dtype == kInF16) return launch_type<kInF16>(g, mode, edge, stream);
+  return launch_type<kInF32>(g, mode, edge, stream);
 }
 
 hipError_t launch_pack_rows16(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t pad,

@@ -94,10 +94,11 @@ int64_t slot_bytes(FfnGemm g, int mode, int dtype) {
   return (int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4;
 }
 
-// The 16-bit tiles take 16-byte rows of x and the weights: widths that are no
-// multiple of 8 are copied to padded rows in the workspace.
-bool packed(int64_t d, int dtype) { return dtype != HESS_F32 && d % 8 != 0; }
-int64_t pack_bytes(int64_t rows, int64_t d) { return up(rows * up(d, 8) * 2, 256); }
+// The tiles take 16-byte pieces of the rows of x and the weights: widths that
+// are no whole number of them are copied to padded rows in the workspace.
+int64_t piece(int dtype) { return 16 / elem_bytes(dtype); }
+bool packed(int64_t d, int dtype) { return d % piece(dtype) != 0; }
+int64_t pack_bytes(int64_t rows, int64_t d, int dtype) { return up(rows * up(d, piece(dtype)) * elem_bytes(dtype), 256); }
 
 // Workspace: forward: packed x, gate, up | partial tiles; backward: the
 // gradient pair | packed x, gate, up | partial tiles.
@@ -108,34 +109,35 @@ FfnWork ffn_work(int64_t n, int64_t d, int64_t f, int dtype, bool backward) {
   FfnWork w{};
   if (!backward && n <= kFfnFew) return w;
   w.pack = backward ? up(n * 2 * up(f, 8) * elem_bytes(dtype), 256) : 0;
-  w.slots = w.pack + (packed(d, dtype) ? pack_bytes(n, d) + 2 * pack_bytes(f, d) : 0);
+  w.slots = w.pack + (packed(d, dtype) ? pack_bytes(n, d, dtype) + 2 * pack_bytes(f, d, dtype) : 0);
   w.total = w.slots + (backward ? std::max(slot_bytes(shape(n, d, f), kFfnDx, dtype),
                                            slot_bytes(shape(2 * up(f, 8), d, n), kFfnDw, dtype))
                                 : slot_bytes(shape(n, f, d), kFfnFwd, dtype));
   return w;
 }
 
-// x, gate and up as the tiles take them: where they are, or (widths that are
-// no multiple of 8) copied to padded rows.
+// x, gate and up as the tiles take them: where they are, or copied to padded
+// rows.
 struct FfnOperands {
   const void *x, *wg, *wu;
   int64_t ldx, ldg, ldu, d;
 };
 int place_operands(FfnOperands& o, char* pack, int64_t n, int64_t f, int dtype, bool want_x, bool want_w,
                    hipStream_t s) {
+  const int64_t step = piece(dtype);
   if (!packed(o.d, dtype)) {
-    if (dtype != HESS_F32 && (!aligned(o.x, 16) || !aligned(o.wg, 16) || !aligned(o.wu, 16) ||
-                              (n > 1 && o.ldx % 8 != 0) || (f > 1 && (o.ldg % 8 != 0 || o.ldu % 8 != 0))))
-      return fail(HESS_EALIGN, "rows of x, w_gate and w_up must be 16-byte aligned where d is a multiple of 8");
+    if (!aligned(o.x, 16) || !aligned(o.wg, 16) || !aligned(o.wu, 16) || (n > 1 && o.ldx % step != 0) ||
+        (f > 1 && (o.ldg % step != 0 || o.ldu % step != 0)))
+      return fail(HESS_EALIGN, "rows of x, w_gate and w_up must be 16-byte aligned where a row is a multiple of 16 bytes");
     return HESS_OK;
   }
-  const int64_t pad = up(o.d, 8);
-  char* pg = pack + pack_bytes(n, o.d);
-  char* pu = pg + pack_bytes(f, o.d);
+  const int64_t pad = up(o.d, step), half = elem_bytes(dtype) / 2;  // a float32 moves as two 16-bit halves
+  char* pg = pack + pack_bytes(n, o.d, dtype);
+  char* pu = pg + pack_bytes(f, o.d, dtype);
   hipError_t e = hipSuccess;
-  if (want_x) e = launch_pack_rows16(o.x, o.ldx, n, o.d, pack, pad, s);
-  if (want_w && e == hipSuccess) e = launch_pack_rows16(o.wg, o.ldg, f, o.d, pg, pad, s);
-  if (want_w && e == hipSuccess) e = launch_pack_rows16(o.wu, o.ldu, f, o.d, pu, pad, s);
+  if (want_x) e = launch_pack_rows16(o.x, o.ldx * half, n, o.d * half, pack, pad * half, s);
+  if (want_w && e == hipSuccess) e = launch_pack_rows16(o.wg, o.ldg * half, f, o.d * half, pg, pad * half, s);
+  if (want_w && e == hipSuccess) e = launch_pack_rows16(o.wu, o.ldu * half, f, o.d * half, pu, pad * half, s);
   if (e != hipSuccess) return hip_fail(e, "operand copy launch");
   o = FfnOperands{pack, pg, pu, pad, pad, pad, pad};
   return HESS_OK;
