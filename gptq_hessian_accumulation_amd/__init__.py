@@ -568,9 +568,10 @@ def _on_stream(fn):
 
 
 def _float_code(name: str, t: torch.Tensor) -> int:
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be on the GPU")
-    if t.device.index != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     code = _CODES.get(t.dtype)
     if code is None:
@@ -579,21 +580,25 @@ def _float_code(name: str, t: torch.Tensor) -> int:
 
 
 def _rows(t: torch.Tensor, step: int = 1):
-    """(tensor, row stride) of a 2-D tensor whose rows are contiguous, do not overlap and start at multiples
-    of ``step`` elements (copied if need be)."""
+    """(tensor, pointer, row stride) of a 2-D tensor whose rows are contiguous, do not overlap and start at
+    multiples of ``step`` elements (copied if need be)."""
     n, c = t.shape
-    s0, s1 = t.stride()
-    if ((s1 != 1 and c > 1) or (n > 1 and (s0 < c or s0 % step != 0))
-            or t.data_ptr() % (step * t.element_size()) != 0):
-        t = t.clone(memory_format=torch.contiguous_format)
-        s0 = t.stride(0)
-    return t, (s0 if n > 1 else max(c, 1))
+    ptr = t.data_ptr()
+    if not t.is_contiguous() or (step > 1 and ptr % (step * t.element_size()) != 0):
+        s0, s1 = t.stride()
+        if ((s1 != 1 and c > 1) or (n > 1 and (s0 < c or s0 % step != 0))
+                or (step > 1 and ptr % (step * t.element_size()) != 0)):
+            t = t.clone(memory_format=torch.contiguous_format)
+            ptr = t.data_ptr()
+        elif n > 1:
+            return t, ptr, s0
+    return t, ptr, c or 1
 
 
 def _out(name: str, out, shape, like: torch.Tensor) -> torch.Tensor:
     """``out`` checked, or a new tensor: ``shape`` on like's device and of its dtype, rows contiguous."""
     if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
     if out.dtype != like.dtype or out.device != like.device or tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {like.dtype} {tuple(shape)} tensor on {like.device}")
     if out.dim() != 2 and not out.is_contiguous():
@@ -603,15 +608,15 @@ def _out(name: str, out, shape, like: torch.Tensor) -> torch.Tensor:
     return out
 
 
-def _workspace(work, need: int, device):
+def _workspace(work, need: int, like: torch.Tensor):
     """(pointer, bytes, tensor) of ``work`` if it is large enough, else of a new workspace."""
     if need == 0:
         return None, 0, None
     if need < 0:
         raise HessError(-1, _load().hess_last_error().decode(errors="replace"))
     if work is None or work.numel() * work.element_size() < need:
-        work = torch.empty(need, dtype=torch.uint8, device=device)
-    elif work.device != device or not work.is_contiguous():
+        work = like.new_empty(need, dtype=torch.uint8)
+    elif work.device != like.device or not work.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return work.data_ptr(), work.numel() * work.element_size(), work
 
@@ -624,22 +629,25 @@ def _act_mode(act: str) -> int:
 
 
 def _ffn_args(x, w_gate, w_up):
+    """(code, n, d, f, tensors to keep, (x, stride, gate, stride, up, stride) for the library)."""
     code = _float_code("x", x)
-    if w_gate.dim() != 2 or w_gate.shape != w_up.shape:
+    shape = w_gate.shape
+    if len(shape) != 2 or shape != w_up.shape:
         raise ValueError("w_gate and w_up must be (f, d) matrices of one shape")
-    f, d = w_gate.shape
+    f, d = shape
     if x.dim() < 1 or x.shape[-1] != d:
         raise ValueError(f"last dimension of x {tuple(x.shape)} != d = {d}")
+    dtype, index = x.dtype, x.get_device()
     for name, t in (("w_gate", w_gate), ("w_up", w_up)):
-        if t.dtype != x.dtype or t.device != x.device:
+        if t.dtype != dtype or t.get_device() != index:
             raise ValueError(f"{name} must have x's dtype and device")
     # the tiles read rows of a multiple of 16 bytes where they are, if they start at 16 bytes
     step = 4 if code == HESS_F32 else 8
     step = step if d % step == 0 else 1
-    x2, ldx = _rows(x.reshape(-1, d) if x.dim() != 2 else x, step)
-    wg, ldg = _rows(w_gate, step)
-    wu, ldu = _rows(w_up, step)
-    return code, x2, ldx, wg, ldg, wu, ldu, x2.shape[0], d, f
+    x2, xp, ldx = _rows(x.reshape(-1, d) if x.dim() != 2 else x, step)
+    wg, gp, ldg = _rows(w_gate, step)
+    wu, up, ldu = _rows(w_up, step)
+    return code, x2.shape[0], d, f, (x2, wg, wu), (xp, ldx, gp, ldg, up, ldu)
 
 
 @_on_stream
@@ -653,17 +661,16 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     """
     lib = _load()
     mode = _act_mode(act)
-    code, x2, ldx, wg, ldg, wu, ldu, n, d, f = _ffn_args(x, w_gate, w_up)
+    code, n, d, f, keep, ins = _ffn_args(x, w_gate, w_up)
     h = _out("out", out, (*x.shape[:-1], f), x)
-    pre = None
-    if save:
-        pre = torch.empty((n, 2 * (-(-f // 8) * 8)), dtype=x.dtype, device=x.device)
+    pre = x.new_empty((n, 2 * (-(-f // 8) * 8))) if save else None
     if n > 0:
-        ldh = h.stride(0) if h.dim() == 2 and n > 1 else f
-        wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 0), x.device)
-        _check(lib.hess_gated_ffn_forward(x2.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu, code, mode, n,
-                                          d, f, h.data_ptr(), ldh, pre.data_ptr() if save else None, wp, wb,
-                                          _stream(None, x.device.index)))
+        ldh = h.stride(0) if out is not None and h.dim() == 2 and n > 1 else f
+        wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 0), x)
+        rc = lib.hess_gated_ffn_forward(*ins, code, mode, n, d, f, h.data_ptr(), ldh,
+                                        pre.data_ptr() if save else None, wp, wb, _stream(None, x.get_device()))
+        if rc != 0:
+            _check(rc)
     return (h, pre) if save else h
 
 
@@ -674,23 +681,25 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     """``(dx, dw_gate, dw_up)`` for the gradient dh of gated_ffn_forward's h (entries not needed are None)."""
     lib = _load()
     mode = _act_mode(act)
-    code, x2, ldx, wg, ldg, wu, ldu, n, d, f = _ffn_args(x, w_gate, w_up)
+    code, n, d, f, keep, (xp, ldx, gp, ldg, up, ldu) = _ffn_args(x, w_gate, w_up)
     if tuple(dh.shape) != (*x.shape[:-1], f) or dh.dtype != x.dtype or dh.device != x.device:
         raise ValueError(f"dh must be a {x.dtype} {(*x.shape[:-1], f)} tensor on {x.device}")
     cols = 2 * (-(-f // 8) * 8)
     if tuple(preact.shape) != (n, cols) or preact.dtype != x.dtype or preact.device != x.device \
             or not preact.is_contiguous():
         raise ValueError(f"preact must be the contiguous {x.dtype} ({n}, {cols}) tensor gated_ffn_forward saved")
-    dh2, lddh = _rows(dh.reshape(-1, f) if dh.dim() != 2 else dh)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_x else None
-    dwg = torch.empty((f, d), dtype=x.dtype, device=x.device) if need_w else None
-    dwu = torch.empty((f, d), dtype=x.dtype, device=x.device) if need_w else None
-    wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 1), x.device)
-    _check(lib.hess_gated_ffn_backward(dh2.data_ptr() if n > 0 else None, lddh, x2.data_ptr() if n > 0 else None, ldx,
-                                       wg.data_ptr(), ldg, wu.data_ptr(), ldu, preact.data_ptr() if n > 0 else None,
-                                       code, mode, n, d, f, dx.data_ptr() if need_x and n > 0 else None, d,
-                                       dwg.data_ptr() if need_w else None, d, dwu.data_ptr() if need_w else None, d,
-                                       wp, wb, _stream(None, x.device.index)))
+    dh2, dhp, lddh = _rows(dh.reshape(-1, f) if dh.dim() != 2 else dh)
+    dx = x.new_empty(x.shape) if need_x else None
+    dwg = x.new_empty((f, d)) if need_w else None
+    dwu = x.new_empty((f, d)) if need_w else None
+    wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 1), x)
+    rc = lib.hess_gated_ffn_backward(dhp if n > 0 else None, lddh, xp if n > 0 else None, ldx, gp, ldg, up, ldu,
+                                     preact.data_ptr() if n > 0 else None, code, mode, n, d, f,
+                                     dx.data_ptr() if need_x and n > 0 else None, d,
+                                     dwg.data_ptr() if need_w else None, d, dwu.data_ptr() if need_w else None, d,
+                                     wp, wb, _stream(None, x.get_device()))
+    if rc != 0:
+        _check(rc)
     return dx, dwg, dwu
 
 
@@ -722,53 +731,60 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: st
 # -- distillation from a teacher's top logits -----------------------------------------------------
 
 def _distill_args(logits, ids, values, weight, temperature):
+    """(tensors to keep, leading shape, n, vocab, code, arguments for the library)."""
     code = _float_code("logits", logits)
-    if logits.dim() < 1:
+    shape, short = logits.shape, ids.shape
+    if len(shape) < 1:
         raise ValueError("logits must be (..., vocab)")
-    lead, vocab = logits.shape[:-1], logits.shape[-1]
-    if ids.shape != values.shape or ids.shape[:-1] != lead or ids.dim() < 1:
+    lead, vocab = shape[:-1], shape[-1]
+    if len(short) < 1 or short != values.shape or short[:-1] != lead:
         raise ValueError("ids and values must be (..., k) with the leading dimensions of logits")
-    if ids.dtype not in (torch.int32, torch.int64):
+    if ids.dtype == torch.int64:
+        ids64 = 1
+    elif ids.dtype == torch.int32:
+        ids64 = 0
+    else:
         raise TypeError("ids must be int32 or int64")
     vcode = _float_code("values", values)
-    for name, t in (("ids", ids), ("values", values)):
-        if t.device != logits.device:
-            raise ValueError(f"{name} must be on the device of logits")
-    k = ids.shape[-1]
-    z2, ldz = _rows(logits.reshape(-1, vocab) if logits.dim() != 2 else logits)
-    i2, ldi = _rows(ids.reshape(-1, k) if ids.dim() != 2 else ids)
-    v2, ldv = _rows(values.reshape(-1, k) if values.dim() != 2 else values)
+    if ids.get_device() != logits.get_device():
+        raise ValueError("ids must be on the device of logits")
+    k = short[-1]
+    flat = len(shape) == 2
+    z2, zp, ldz = _rows(logits if flat else logits.reshape(-1, vocab))
+    i2, ip, ldi = _rows(ids if flat else ids.reshape(-1, k))
+    v2, vp, ldv = _rows(values if flat else values.reshape(-1, k))
     n = z2.shape[0]
-    w = _row_floats("weight", weight, lead, logits.device)
-    return (z2, i2, v2, w), lead, n, vocab, (
-        z2.data_ptr(), ldz, code, n, vocab, i2.data_ptr(), 1 if ids.dtype == torch.int64 else 0, ldi, v2.data_ptr(),
-        vcode, ldv, k, w.data_ptr() if w is not None else None, float(temperature))
+    w = _row_floats("weight", weight, lead, logits)
+    return (z2, i2, v2, w), lead, n, vocab, code, (zp, ldz, code, n, vocab, ip, ids64, ldi, vp, vcode, ldv, k,
+                                                   w.data_ptr() if w is not None else None, float(temperature))
 
 
-def _row_floats(name, t, lead, device):
+def _row_floats(name, t, lead, like):
     """A float32 value for each row, contiguous (a broadcast one is written out)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(lead) or t.dtype != torch.float32 or t.device != device:
-        raise ValueError(f"{name} must be a float32 {tuple(lead)} tensor on {device}")
+    if t.shape != lead or t.dtype != torch.float32 or t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be a float32 {tuple(lead)} tensor on {like.device}")
     return t.contiguous()
 
 
 def _grad_out(out, logits):
     grad = _out("out", out, logits.shape, logits)
-    return grad, (grad.stride(0) if grad.dim() == 2 and grad.shape[0] > 1 else logits.shape[-1])
+    return grad, (grad.stride(0) if out is not None and grad.dim() == 2 and grad.shape[0] > 1 else logits.shape[-1])
 
 
 def _distill_call(logits, ids, values, weight, temperature, want_stats, want_grad, out, workspace):
     lib = _load()
-    keep, lead, n, vocab, args = _distill_args(logits, ids, values, weight, temperature)
-    dev = logits.device
-    loss = torch.empty(lead, dtype=torch.float32, device=dev)
-    stats = torch.empty((*lead, 2), dtype=torch.float32, device=dev) if want_stats else None
+    keep, lead, n, vocab, code, args = _distill_args(logits, ids, values, weight, temperature)
+    loss = logits.new_empty(lead, dtype=torch.float32)
+    stats = logits.new_empty((*lead, 2), dtype=torch.float32) if want_stats else None
     grad, ldg = _grad_out(out, logits) if want_grad else (None, 0)
-    wp, wb, work = _workspace(workspace, lib.hess_distill_topk_workspace(n, vocab, args[2]), dev)
-    _check(lib.hess_distill_topk(*args, loss.data_ptr(), stats.data_ptr() if want_stats else None,
-                                 grad.data_ptr() if want_grad else None, ldg, wp, wb, _stream(None, dev.index)))
+    wp, wb, work = _workspace(workspace, lib.hess_distill_topk_workspace(n, vocab, code), logits)
+    rc = lib.hess_distill_topk(*args, loss.data_ptr(), stats.data_ptr() if want_stats else None,
+                               grad.data_ptr() if want_grad else None, ldg, wp, wb,
+                               _stream(None, logits.get_device()))
+    if rc != 0:
+        _check(rc)
     return loss, stats, grad
 
 
@@ -800,14 +816,16 @@ def distill_topk_backward(dloss: torch.Tensor, logits: torch.Tensor, ids: torch.
                           out: torch.Tensor | None = None) -> torch.Tensor:
     """dlogits for the gradient dloss of distill_topk_forward's loss (``out`` may be logits)."""
     lib = _load()
-    keep, lead, n, vocab, args = _distill_args(logits, ids, values, weight, temperature)
-    dl = _row_floats("dloss", dloss, lead, logits.device)
+    keep, lead, n, vocab, code, args = _distill_args(logits, ids, values, weight, temperature)
+    dl = _row_floats("dloss", dloss, lead, logits)
     if tuple(stats.shape) != (*lead, 2) or stats.dtype != torch.float32 or stats.device != logits.device \
             or not stats.is_contiguous():
         raise ValueError(f"stats must be the contiguous float32 {(*lead, 2)} tensor distill_topk_forward returned")
     grad, ldg = _grad_out(out, logits)
-    _check(lib.hess_distill_topk_backward(dl.data_ptr(), *args, stats.data_ptr(), grad.data_ptr(), ldg,
-                                          _stream(None, logits.device.index)))
+    rc = lib.hess_distill_topk_backward(dl.data_ptr(), *args, stats.data_ptr(), grad.data_ptr(), ldg,
+                                        _stream(None, logits.get_device()))
+    if rc != 0:
+        _check(rc)
     return grad
 
 
