@@ -190,29 +190,36 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
     for (int n = 0; n < kBn; ++n) acc[m][n] = f32x4{};
 
   // Iteration j on the stage at cur (its first four A blocks are in a, its B
-  // blocks in b): wait for my loads of the next iteration, meet the other
-  // waves (the next stage is then complete, and nobody reads the one before
-  // cur), then group by group the matrix instructions of one A block, the
+  // blocks in b), group by group: the matrix instructions of one A block, the
   // read of the A block four groups later (of the next stage at the end), a
-  // read of the next stage's B (into c) and a load of iteration j + 4.
+  // read of the next stage's B (into c) and a load of iteration j + 4.  Before
+  // the first read of the next stage the wave waits for its own loads of it
+  // and meets the others (the next stage is then complete, and nobody reads
+  // the one before cur); up to there it works on operands already read, so
+  // that the matrix instructions run on from one iteration to the next.
+  constexpr int kMeet = kBm - 6 > 0 ? kBm - 6 : 0;
   u32x4 a[4];
   auto step = [&](uint32_t cur, uint32_t nxt, uint32_t target, int j, const u32x4 (&b)[kBn], u32x4 (&c)[kBn]) {
     const Next d = describe(j + kAhead);
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 2)));
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int m = 0; m < kBm; ++m) {
+      if (m == kMeet) {
+        __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 2)));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int n = 0; n < kBn; ++n) acc[m][n] = mma16<DT>(b[n], a[m & 3], acc[m][n]);
       a[m & 3] = m + 4 < kBm ? read_a(cur, m + 4) : read_a(nxt, m + 4 - kBm);
-      if (m >= kBm - kBn) c[m - (kBm - kBn)] = read_b(nxt, m - (kBm - kBn));
-      if (kBm == 4 || (m & 1)) load1(lds0 + target, d, kBm == 4 ? m : m >> 1);
+      if (m >= kMeet && m < kMeet + 4) {
+        c[m - kMeet] = read_b(nxt, m - kMeet);
+        load1(lds0 + target, d, m - kMeet);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  static_assert(2 * kLoads == 4, "a load for every one (edge 128) or two groups");
+  static_assert(2 * kLoads == 4 && kBn == 4, "one load and one read of B in each of four groups");
 
 #pragma unroll
   for (int q = 0; q < kAhead; ++q) load_stage(lds0 + q * kStage, it0 + q);
