@@ -25,6 +25,8 @@
 //    workgroup was given lies outside the descriptor (or its chunk's offset
 //    does), and all of these read as zeros.
 
+#include <type_traits>
+
 #include "ffn_device.hpp"
 #include "hess_device.hpp"
 
@@ -249,53 +251,80 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
   __builtin_amdgcn_s_waitcnt(0x0070);
   __builtin_amdgcn_sched_barrier(0);
 
-  int lv = lane;
-  asm volatile("" : "+v"(lv));  // the output's offsets are computed here, not kept through the loop
-  const int rr = wr * (Edge / 2) + (lv & 15);
   if (!whole) {
-    float* W = P.ws + ((int64_t)part * tail + (t - P.full)) * (Edge * Edge);
-    const int cc = wc * 64 + 4 * (lv >> 4);
+    float* W = P.ws + ((int64_t)part * tail + (t - P.full)) * (Edge * Edge) +
+               (wr * (Edge / 2) + (lane & 15)) * Edge + wc * 64 + 4 * (lane >> 4);
 #pragma unroll
     for (int m = 0; m < kBm; ++m)
 #pragma unroll
       for (int n = 0; n < kBn; ++n) {
-        const f32x4 a = acc[m][n];
-        *reinterpret_cast<float4*>(W + (rr + 16 * m) * Edge + cc + 16 * n) = float4{a[0], a[1], a[2], a[3]};
+        const f32x4 x = acc[m][n];
+        *reinterpret_cast<float4*>(W + 16 * m * Edge + 16 * n) = float4{x[0], x[1], x[2], x[3]};
       }
     return;
   }
-  // Blocks n, n + 1: after exchanging the odd 16-lane rows of the first with
-  // the even ones of the second, lane row g holds columns 8 (g / 2) .. + 7 of
-  // block n + g % 2.
-  const int cc = 16 * ((lv >> 4) & 1) + 8 * (lv >> 5);
-  auto eight = [&](const f32x4& p, const f32x4& q, float (&o)[8]) {
+  // A tile's outputs.  Blocks n, n + 1: after exchanging the odd 16-lane rows
+  // of the first with the even ones of the second, lane row g holds columns
+  // 8 (g / 2) .. + 7 of block n + g % 2.  In: the tile lies inside the matrix.
+  auto put_tile = [&](auto in) __attribute__((always_inline)) {
+    constexpr bool In = decltype(in)::value;
+    typedef typename Elem<DT>::type T;
+    int lv = lane;
+    asm volatile("" : "+v"(lv));  // the offsets are computed here, not kept through the loop
+    const int cc = 16 * ((lv >> 4) & 1) + 8 * (lv >> 5);
+    auto eight = [&](const f32x4& p, const f32x4& q, float (&o)[8]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[j]), __float_as_uint(q[j]), false, false);
-      o[j] = __uint_as_float(s[0]);
-      o[4 + j] = __uint_as_float(s[1]);
+      for (int j = 0; j < 4; ++j) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[j]), __float_as_uint(q[j]), false, false);
+        o[j] = __uint_as_float(s[0]);
+        o[4 + j] = __uint_as_float(s[1]);
+      }
+    };
+#pragma unroll
+    for (int m = 0; m < kBm; ++m) {
+      const int64_t r = i0 + wr * (Edge / 2) + (lv & 15) + 16 * m;
+      if constexpr (Mode == kFfnFwd) {
+        const int64_t col = j0 + wc * 32 + cc;
+        float g[8], u[8];
+        eight(acc[m][0], acc[m][1], g);
+        eight(acc[m][2], acc[m][3], u);
+        if constexpr (In) {
+          float h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = act_value<DT == kInF32>(g[e], P.act) * u[e];
+          store_n(static_cast<T*>(P.o0) + r * P.ldo0 + col, h, 8);
+          if (P.o1) {
+            T* pre = static_cast<T*>(P.o1) + r * 2 * P.fp + col;
+            store_n(pre, g, 8);
+            store_n(pre + P.fp, u, 8);
+          }
+        } else {
+          put_fwd<DT>(P, r, col, g, u);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < kBn; n += 2) {
+          const int64_t col = j0 + wc * 64 + 16 * n + cc;
+          float v[8];
+          eight(acc[m][n], acc[m][n + 1], v);
+          if constexpr (In) {
+            T* o = static_cast<T*>(P.o0) + r * P.ldo0;
+            if constexpr (Mode == kFfnDw)
+              if (r >= P.fp) o = static_cast<T*>(P.o1) + (r - P.fp) * P.ldo1;
+            store_n(o + col, v, 8);
+          } else {
+            put<DT, Mode>(P, r, col, v);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-#pragma unroll
-  for (int m = 0; m < kBm; ++m) {
-    const int64_t r = i0 + rr + 16 * m;
-    if constexpr (Mode == kFfnFwd) {
-#pragma unroll
-      for (int n = 0; n < kBn / 2; n += 2) {
-        float g[8], u[8];
-        eight(acc[m][n], acc[m][n + 1], g);
-        eight(acc[m][n + kBn / 2], acc[m][n + 1 + kBn / 2], u);
-        put_fwd<DT>(P, r, j0 + wc * 32 + 16 * n + cc, g, u);
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < kBn; n += 2) {
-        float v[8];
-        eight(acc[m][n], acc[m][n + 1], v);
-        put<DT, Mode>(P, r, j0 + wc * 64 + 16 * n + cc, v);
-      }
-    }
-  }
+
+  const bool inside = i0 + Edge <= P.M && j0 + (Mode == kFfnFwd ? Edge / 2 : Edge) <= P.N &&
+                      (Mode != kFfnDw || P.f == P.fp);
+  if (inside) put_tile(std::true_type());
+  else put_tile(std::false_type());
 }
 
 // Split tiles: the parts' sums added in part order, then the epilogue.  Block
