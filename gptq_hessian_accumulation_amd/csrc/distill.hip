@@ -38,14 +38,15 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
 
-template <class T> __device__ __forceinline__ T wave_sum(T v) {
+// Sum and maximum over groups of Lanes lanes, in every lane.
+template <int Lanes = 64, class T> __device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  for (int o = Lanes / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
+template <int Lanes = 64> __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  for (int o = Lanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
   return v;
 }
 
@@ -98,6 +99,8 @@ template <int Threads> struct Entries {
   int id[kPer];
   float v[kPer], z[kPer];
   int bad;
+  // entries fill the waves in order: whether this one has any
+  static __device__ __forceinline__ bool mine(int k) { return (int)(threadIdx.x & ~63u) < k; }
   uint32_t raw_lo[kPer], raw_hi[kPer], raw_v[kPer];
 
   // Issues the loads (nothing waits for them here) ...
@@ -152,29 +155,49 @@ template <int Waves> struct Joined {
   int flags[Waves], dup;
 };
 
-// A wave's share of the teacher's softmax: its largest value, and the sum of
-// exponentials above it.
-template <int Threads>
-__device__ __forceinline__ void teacher_share(const Entries<Threads>& E, double it, float& vm, double& ps) {
-  vm = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < E.kPer; ++q) vm = fmaxf(vm, E.v[q]);
-  vm = wave_max(vm);
-  ps = 0.0;
-  if (__any(E.id[0] >= 0) || (E.kPer > 1 && vm != -INFINITY)) {
-#pragma unroll
-    for (int q = 0; q < E.kPer; ++q)
-      if (E.id[q] >= 0) ps += exp(((double)E.v[q] - (double)vm) * it);
-    ps = wave_sum(ps);
-  }
-}
 // The waves' shares joined, in every thread: vm, and log of the whole sum.
 template <int Waves>
 __device__ __forceinline__ void teacher_join(const Joined<Waves>& J, double it, float& vm, double& logps) {
-  const int l = threadIdx.x & 63;
-  const float x = l < Waves ? J.vm[l] : -INFINITY;
-  vm = wave_max(x);
-  logps = log(wave_sum(x == -INFINITY ? 0.0 : J.ps[l] * exp(((double)x - (double)vm) * it)));
+  const int l = threadIdx.x & (Waves - 1);
+  const float x = J.vm[l];
+  vm = wave_max<Waves>(x);
+  logps = log(wave_sum<Waves>(x == -INFINITY ? 0.0 : J.ps[l] * exp(((double)x - (double)vm) * it)));
+}
+
+// A wave's share of the teacher's softmax: its largest value, and the sum of
+// exponentials above it.
+template <int Threads>
+__device__ __forceinline__ void teacher_share(const Entries<Threads>& E, int k, double it, float& vm, double& ps) {
+  vm = -INFINITY;
+  ps = 0.0;
+  if (!E.mine(k)) return;
+#pragma unroll
+  for (int q = 0; q < E.kPer; ++q) vm = fmaxf(vm, E.v[q]);
+  vm = wave_max(vm);
+#pragma unroll
+  for (int q = 0; q < E.kPer; ++q)
+    if (E.id[q] >= 0) ps += exp(((double)E.v[q] - (double)vm) * it);
+  ps = wave_sum(ps);
+}
+
+// Its terms of the loss; p, float32, to s_p where that is wanted.
+template <int Threads, int Waves>
+__device__ __forceinline__ double teacher_terms(const Entries<Threads>& E, const Joined<Waves>& J, double it, float m,
+                                                float sum, float* s_p) {
+  float vm;
+  double logps;
+  teacher_join(J, it, vm, logps);
+  const double logsum = log((double)sum);
+  double term = 0.0;
+#pragma unroll
+  for (int q = 0; q < E.kPer; ++q) {
+    if (E.id[q] < 0) continue;
+    const double lp = ((double)E.v[q] - (double)vm) * it - logps;
+    const double p = exp(lp);
+    if (p != 0.0) term += p * (lp - (((double)E.z[q] - (double)m) * it - logsum));
+    if (s_p) s_p[threadIdx.x + q * Threads] = (float)p;
+  }
+  return wave_sum(term);
 }
 
 // Whether two entries of ids[0 .. k) name the same word: groups of threads
@@ -230,10 +253,10 @@ template <int N> __device__ __forceinline__ void online(const float (&v)[N], flo
 
 // The waves' maxima and sums joined, in every thread.
 template <int Waves> __device__ __forceinline__ void student_join(const Joined<Waves>& J, float cl, float& m, float& s) {
-  const int l = threadIdx.x & 63;
-  const float x = l < Waves ? J.m[l] : -FLT_MAX;
-  m = wave_max(x);
-  s = (float)wave_sum(l < Waves ? (double)(J.s[l] * __builtin_amdgcn_exp2f((x - m) * cl)) : 0.0);
+  const int l = threadIdx.x & (Waves - 1);
+  const float x = J.m[l];
+  m = wave_max<Waves>(x);
+  s = (float)wave_sum<Waves>((double)(J.s[l] * __builtin_amdgcn_exp2f((x - m) * cl)));
 }
 
 struct Scales {
@@ -307,7 +330,7 @@ __global__ void __launch_bounds__(Threads, 4) distill_resident(DistillParams P) 
     if (last < vocab) online(one, cl, m, sum);
     float vm;
     double ps;
-    teacher_share(E, it, vm, ps);
+    teacher_share(E, P.k, it, vm, ps);
     int present = 0;
 #pragma unroll
     for (int q = 0; q < E.kPer; ++q) {
@@ -340,25 +363,12 @@ __global__ void __launch_bounds__(Threads, 4) distill_resident(DistillParams P) 
     return;
   }
   student_join(J, cl, m, sum);
-  {
-    double logps;
-    float vm;
-    teacher_join(J, it, vm, logps);
-    const double logsum = log((double)sum);
-    double term = 0.0;
-#pragma unroll
-    for (int q = 0; q < E.kPer; ++q) {
-      if (E.id[q] < 0) continue;
-      const double lp = ((double)E.v[q] - (double)vm) * it - logps;
-      const double p = exp(lp);
-      if (p != 0.0) term += p * (lp - (((double)E.z[q] - (double)m) * it - logsum));
-      s_p[tid + q * Threads] = (float)p;
-    }
-    if (wave * 64 < P.k) term = wave_sum(term);
+  if (E.mine(P.k)) {
+    const double term = teacher_terms(E, J, it, m, sum, s_p);
     if ((tid & 63) == 0) J.term[wave] = term;
-    if (any_twice<Threads>(s_id, P.k)) J.dup = 1;
-    c = (all & 2) ? NAN : w / P.temperature;
   }
+  if (any_twice<Threads>(s_id, P.k)) J.dup = 1;
+  c = (all & 2) ? NAN : w / P.temperature;
   const float inv = 1.0f / sum, f = c * inv;
   const int t = opaque_tid();
 #pragma unroll
@@ -410,7 +420,7 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
     for (; j + (int64_t)((kUnroll - 1) * Threads + 1) * V::N <= P.vocab; j += (int64_t)kUnroll * Threads * V::N) {
       u32x4 v[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) v[i] = V::load(z, j + (int64_t)i * Threads * V::N, P.vocab);
+      for (int i = 0; i < kUnroll; ++i) v[i] = *reinterpret_cast<const typename V::U*>(z + j + (int64_t)i * Threads * V::N);
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         float x[V::N];
@@ -425,7 +435,7 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
     }
     E.decode(P);
     E.gather(z, 0, (int)P.vocab);
-    teacher_share(E, it, vm, ps);
+    teacher_share(E, P.k, it, vm, ps);
     int present = 0;
 #pragma unroll
     for (int q = 0; q < E.kPer; ++q) present |= E.id[q] >= 0;
@@ -450,23 +460,14 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
     return;
   }
   student_join(J, cl, m, sum);
-  double logps;
-  teacher_join(J, it, vm, logps);
-  const double logsum = log((double)sum);
-  double term = 0.0;
-#pragma unroll
-  for (int q = 0; q < E.kPer; ++q) {
-    if (E.id[q] < 0) continue;
-    const double lp = ((double)E.v[q] - (double)vm) * it - logps;
-    const double p = exp(lp);
-    if (p != 0.0) term += p * (lp - (((double)E.z[q] - (double)m) * it - logsum));
+  if (E.mine(P.k)) {
+    const double term = teacher_terms(E, J, it, m, sum, nullptr);
+    if ((tid & 63) == 0) J.term[wave] = term;
   }
-  term = wave_sum(term);
-  if ((tid & 63) == 0) J.term[wave] = term;
   __syncthreads();
   if (tid == 0) {
     double t = 0.0;
-    for (int q = 0; q < kWaves; ++q) t += J.term[q];
+    for (int q = 0; q < kWaves && q * 64 < P.k; ++q) t += J.term[q];
     P.loss[row] = (all & 2) ? NAN : (float)(t * w);
     if (P.stats) {
       P.stats[2 * row] = m;
@@ -505,7 +506,7 @@ template <int DT> __global__ void __launch_bounds__(kGradThreads, 4) distill_gra
     E.gather(z, (int)lo, (int)hi);
     float vm;
     double ps;
-    teacher_share(E, it, vm, ps);
+    teacher_share(E, P.k, it, vm, ps);
     int present = 0;
 #pragma unroll
     for (int q = 0; q < E.kPer; ++q) {
@@ -525,44 +526,57 @@ template <int DT> __global__ void __launch_bounds__(kGradThreads, 4) distill_gra
     for (int q = 0; q < kWaves; ++q) all |= J.flags[q];
     zero = !(all & 1);
     c = (all & 2) ? NAN : (P.dloss ? P.dloss[row] : 1.0f) * w / P.temperature;
-    if (!zero) {
+    if (!zero && E.mine(P.k)) {
       double logps;
       teacher_join(J, it, vm, logps);
 #pragma unroll
       for (int q = 0; q < E.kPer; ++q)
         if (E.id[q] >= 0) s_p[tid + q * Threads] = (float)exp(((double)E.v[q] - (double)vm) * it - logps);
-      if (any_twice<Threads>(s_id, P.k)) J.dup = 1;
     }
+    if (!zero && any_twice<Threads>(s_id, P.k)) J.dup = 1;
   }
+  // blocks of kUnroll whole vectors a thread, then the rest vector by vector
   const float f = c * inv;
   int64_t j = lo + (int64_t)tid * V::N;
-  for (; j < hi; j += (int64_t)kUnroll * Threads * V::N) {
-    u32x4 v[kUnroll];
-    if (!zero) {
+  const int64_t step = (int64_t)Threads * V::N, block = kUnroll * step;
+  auto slope = [&](const u32x4& r, float (&g)[V::N]) {
+    V::get(r, g);
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) v[i] = V::load(z, j + (int64_t)i * Threads * V::N, hi);
-    }
+    for (int e = 0; e < V::N; ++e) g[e] = __builtin_amdgcn_exp2f((g[e] - m) * cl) * f;
+  };
+  const float none[V::N] = {};
+  for (int64_t b0 = lo; b0 + block <= hi; b0 += block, j += block) {
+    if (zero) {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int64_t e0 = j + (int64_t)i * Threads * V::N;
-      float g[V::N];
-      if (zero) {
+      for (int i = 0; i < kUnroll; ++i) V::store_whole(dz + j + i * step, none);
+    } else {
+      u32x4 v[kUnroll];
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) g[e] = 0.0f;
-      } else {
-        V::get(v[i], g);
+      for (int i = 0; i < kUnroll; ++i) v[i] = *reinterpret_cast<const typename V::U*>(z + j + i * step);
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) g[e] = __builtin_amdgcn_exp2f((g[e] - m) * cl) * f;
+      for (int i = 0; i < kUnroll; ++i) {
+        float g[V::N];
+        slope(v[i], g);
+        V::store_whole(dz + j + i * step, g);
       }
-      if (e0 < hi) V::store(dz, e0, hi, g);
     }
+  }
+  for (; j < hi; j += step) {
+    float g[V::N];
+    if (zero) {
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) g[e] = 0.0f;
+    } else {
+      slope(V::load(z, j, hi), g);
+    }
+    V::store(dz, j, hi, g);
   }
   if (zero) return;
   __syncthreads();
   scatter<DT, Threads>(P, E, s_id, s_p, J.dup != 0, dz, m, cl, inv, c, (int)lo, (int)hi);
 }
 
-template <int DT> constexpr int64_t resident_limit() { return (int64_t)1024 * 16 * Vec<DT>::N; }
+template <int DT> constexpr int64_t resident_limit() { return ((int64_t)1024 * 16 + 1) * Vec<DT>::N - 1; }
 
 template <int DT, int Threads, int NV> void launch_resident(const DistillParams& P, hipStream_t stream) {
   distill_resident<DT, Threads, NV><<<(unsigned)P.n, Threads, 0, stream>>>(P);
@@ -588,7 +602,7 @@ template <int DT> hipError_t launch(DistillParams P, hipStream_t stream) {
     launch_loss<DT>(P, stream);
     return hipGetLastError();
   }
-  const int64_t vecs = (P.vocab + Vec<DT>::N - 1) / Vec<DT>::N;
+  const int64_t vecs = P.vocab / Vec<DT>::N;
   if (P.vocab > resident_limit<DT>()) {
     if (!P.stats) P.stats = static_cast<float*>(P.work);
     launch_loss<DT>(P, stream);

@@ -1,6 +1,6 @@
 // The gated feed-forward block, forward, for few tokens (a decoding step).
 //
-// Bound by the weights' bytes.  A workgroup takes 16 or 32 features of both
+// Bound by the weights' bytes.  A workgroup takes 16 to 64 features of both
 // projections and the whole of K: its waves split K, each lane loads 16 bytes
 // of one weight row straight into the matrix instruction's operand (no LDS,
 // any alignment; 64 consecutive bytes a row and instruction), x comes from L2
@@ -123,10 +123,21 @@ template <int DT, int MB, int FB, int W, int U> __global__ void __launch_bounds_
   }
 }
 
+template <int DT, int MB, int FB, int U> void launch_few(const FfnGemm& g, hipStream_t stream) {
+  ffn_few<DT, MB, FB, 4, U><<<(unsigned)((g.N + 16 * FB - 1) / (16 * FB)), 256, 0, stream>>>(g);
+}
+
+// More features a workgroup read x less often, but need many features to have
+// a workgroup for each CU: at 4096 x 11264, fp16, 32 tokens 48.6 us with 32
+// features and 51.7 with 16, 64 tokens 61.1 with 64 and 68.6 with 16; at
+// 1001 x 2731, 24 tokens 15.2 against 11.5, 64 tokens 30.1 against 16.2.
 template <int DT> void launch_type(const FfnGemm& g, hipStream_t stream) {
-  if (g.M <= 16) ffn_few<DT, 1, 1, 4, 8><<<(unsigned)((g.N + 15) / 16), 256, 0, stream>>>(g);
-  else if (g.M <= 32) ffn_few<DT, 2, 1, 4, 4><<<(unsigned)((g.N + 15) / 16), 256, 0, stream>>>(g);
-  else ffn_few<DT, 4, 2, 4, 2><<<(unsigned)((g.N + 31) / 32), 256, 0, stream>>>(g);
+  const bool wide = g.N >= 8192;
+  if (g.M <= 16) launch_few<DT, 1, 1, 4>(g, stream);
+  else if (g.M <= 32 && wide) launch_few<DT, 2, 2, 2>(g, stream);
+  else if (g.M <= 32) launch_few<DT, 2, 1, 4>(g, stream);
+  else if (wide) launch_few<DT, 4, 4, 1>(g, stream);
+  else launch_few<DT, 4, 1, 2>(g, stream);
 }
 
 }  // namespace
