@@ -109,7 +109,7 @@ template <int Threads> struct Entries {
     for (int q = 0; q < kPer; ++q) {
       const int i = threadIdx.x + q * Threads;
       raw_lo[q] = raw_hi[q] = raw_v[q] = 0;
-      if (i < P.k) {
+      if (q * Threads < P.k && i < P.k) {
         if (P.ids64) {
           const uint2 t = static_cast<const uint2*>(P.ids)[row * P.ldi + i];
           raw_lo[q] = t.x;
@@ -127,6 +127,9 @@ template <int Threads> struct Entries {
     bad = 0;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
+      id[q] = -1;
+      v[q] = -INFINITY;
+      if (q * Threads >= P.k) continue;
       const int64_t t = P.ids64 ? (int64_t)(((uint64_t)raw_hi[q] << 32) | raw_lo[q]) : (int64_t)(int32_t)raw_lo[q];
       const float x = P.values_dtype == kInF32    ? __uint_as_float(raw_v[q])
                       : P.values_dtype == kInBF16 ? __uint_as_float(raw_v[q] << 16)
@@ -139,11 +142,11 @@ template <int Threads> struct Entries {
     }
   }
   // the student's logits of the entries in [lo, hi)
-  template <class T> __device__ __forceinline__ void gather(const T* zr, int lo, int hi) {
+  template <class T> __device__ __forceinline__ void gather(const T* zr, int k, int lo, int hi) {
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       z[q] = 0.0f;
-      if (id[q] >= lo && id[q] < hi) z[q] = to_f32(zr[id[q]]);
+      if (q * Threads < k && id[q] >= lo && id[q] < hi) z[q] = to_f32(zr[id[q]]);
     }
   }
 };
@@ -176,13 +179,13 @@ __device__ __forceinline__ void teacher_share(const Entries<Threads>& E, int k, 
   vm = wave_max(vm);
 #pragma unroll
   for (int q = 0; q < E.kPer; ++q)
-    if (E.id[q] >= 0) ps += exp(((double)E.v[q] - (double)vm) * it);
+    if (q * Threads < k && E.id[q] >= 0) ps += exp(((double)E.v[q] - (double)vm) * it);
   ps = wave_sum(ps);
 }
 
 // Its terms of the loss; p, float32, to s_p where that is wanted.
 template <int Threads, int Waves>
-__device__ __forceinline__ double teacher_terms(const Entries<Threads>& E, const Joined<Waves>& J, double it, float m,
+__device__ __forceinline__ double teacher_terms(const Entries<Threads>& E, int k, const Joined<Waves>& J, double it, float m,
                                                 float sum, float* s_p) {
   float vm;
   double logps;
@@ -191,7 +194,7 @@ __device__ __forceinline__ double teacher_terms(const Entries<Threads>& E, const
   double term = 0.0;
 #pragma unroll
   for (int q = 0; q < E.kPer; ++q) {
-    if (E.id[q] < 0) continue;
+    if (q * Threads >= k || E.id[q] < 0) continue;
     const double lp = ((double)E.v[q] - (double)vm) * it - logps;
     const double p = exp(lp);
     if (p != 0.0) term += p * (lp - (((double)E.z[q] - (double)m) * it - logsum));
@@ -201,17 +204,25 @@ __device__ __forceinline__ double teacher_terms(const Entries<Threads>& E, const
 }
 
 // Whether two entries of ids[0 .. k) name the same word: groups of threads
-// compare each entry with a part of those before it.
+// compare each entry with a part of them (four at a time, the same ones in
+// every lane of a group; ids is 16-byte aligned and padded to a multiple of 4
+// with negative values).
 template <int Threads> __device__ __forceinline__ bool any_twice(const int* ids, int k) {
   const int lg = k <= 64 ? 6 : 32 - __clz(k - 1);
   const int groups = max(1, Threads >> lg);
-  const int g = lg < 31 ? threadIdx.x >> lg : 0;
+  const int g = __builtin_amdgcn_readfirstlane(threadIdx.x >> lg);
+  const int quads = (k + 3) >> 2;
   bool twice = false;
   if (g < groups) {
+    const int q0 = quads * g / groups, q1 = quads * (g + 1) / groups;
     for (int i = threadIdx.x & ((1 << lg) - 1); i < k; i += Threads) {
       const int id = ids[i];
-      const int j0 = (int)((int64_t)i * g / groups), j1 = (int)((int64_t)i * (g + 1) / groups);
-      for (int j = j0; j < j1; ++j) twice |= id >= 0 && ids[j] == id;
+      for (int q = q0; q < q1; ++q) {
+        const int4 x = reinterpret_cast<const int4*>(ids)[q];
+        const int at = i - 4 * q;
+        twice |= id >= 0 && ((x.x == id && at != 0) || (x.y == id && at != 1) || (x.z == id && at != 2) ||
+                             (x.w == id && at != 3));
+      }
     }
   }
   return twice;
@@ -227,11 +238,18 @@ __device__ __forceinline__ void scatter(const DistillParams& P, const Entries<Th
 #pragma unroll
   for (int q = 0; q < E.kPer; ++q) {
     const int id = E.id[q];
-    if (id < lo || id >= hi) continue;
+    if (q * Threads >= P.k || id < lo || id >= hi) continue;
     float p;
     if (twice) {
       p = 0.0f;
-      for (int j = 0; j < P.k; ++j) p += ids[j] == id ? ps[j] : 0.0f;
+      for (int j = 0; j < P.k; j += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(ids + j);
+        const float4 y = *reinterpret_cast<const float4*>(ps + j);
+        p += x.x == id ? y.x : 0.0f;
+        p += x.y == id ? y.y : 0.0f;
+        p += x.z == id ? y.z : 0.0f;
+        p += x.w == id ? y.w : 0.0f;
+      }
     } else {
       p = ps[threadIdx.x + q * Threads];
     }
@@ -276,8 +294,8 @@ __global__ void __launch_bounds__(Threads, 4) distill_resident(DistillParams P) 
   typedef Vec<DT> V;
   constexpr int kWaves = Threads / 64;
   __shared__ Joined<kWaves> J;
-  __shared__ int s_id[kTop];
-  __shared__ float s_p[kTop];
+  __shared__ __attribute__((aligned(16))) int s_id[kTop];
+  __shared__ __attribute__((aligned(16))) float s_p[kTop];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int vocab = (int)P.vocab, nvec = vocab / V::N;
@@ -311,7 +329,7 @@ __global__ void __launch_bounds__(Threads, 4) distill_resident(DistillParams P) 
       if (wave_in(i)) v[i] = *reinterpret_cast<const typename V::U*>(z + min(i * Threads + t, nvec - 1) * V::N);
     if (last < vocab) rest = to_f32(z[last]);
     E.decode(P);
-    E.gather(z, 0, vocab);
+    E.gather(z, P.k, 0, vocab);
     t = opaque_tid();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -335,7 +353,7 @@ __global__ void __launch_bounds__(Threads, 4) distill_resident(DistillParams P) 
 #pragma unroll
     for (int q = 0; q < E.kPer; ++q) {
       present |= E.id[q] >= 0;
-      if (tid + q * Threads < P.k) s_id[tid + q * Threads] = E.id[q];
+      if (q * Threads < P.k && tid + q * Threads < ((P.k + 3) & ~3)) s_id[tid + q * Threads] = E.id[q];
     }
     const float wm = wave_max(m);
     const float wsum = wave_sum(sum * __builtin_amdgcn_exp2f((m - wm) * cl));
@@ -364,7 +382,7 @@ __global__ void __launch_bounds__(Threads, 4) distill_resident(DistillParams P) 
   }
   student_join(J, cl, m, sum);
   if (E.mine(P.k)) {
-    const double term = teacher_terms(E, J, it, m, sum, s_p);
+    const double term = teacher_terms(E, P.k, J, it, m, sum, s_p);
     if ((tid & 63) == 0) J.term[wave] = term;
   }
   if (any_twice<Threads>(s_id, P.k)) J.dup = 1;
@@ -416,25 +434,33 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
   int all = 0;
   if (!zero) {
     E.load(P, row);
-    int64_t j = (int64_t)tid * V::N;
-    for (; j + (int64_t)((kUnroll - 1) * Threads + 1) * V::N <= P.vocab; j += (int64_t)kUnroll * Threads * V::N) {
+    // blocks of kUnroll vectors a thread; in the last one, lanes past the row
+    // take its last vector and leave it out.  The fewer than one vector's
+    // elements after the vectors go to the first threads, one each.
+    const int64_t nvec = P.vocab / V::N;
+    for (int64_t b0 = 0; b0 < nvec; b0 += kUnroll * Threads) {
+      const bool whole = b0 + kUnroll * Threads <= nvec;
       u32x4 v[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) v[i] = *reinterpret_cast<const typename V::U*>(z + j + (int64_t)i * Threads * V::N);
+      for (int i = 0; i < kUnroll; ++i)
+        v[i] = *reinterpret_cast<const typename V::U*>(z + min(b0 + i * Threads + tid, nvec - 1) * V::N);
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
-        float x[V::N];
+        if (!whole && b0 + i * Threads + (tid & ~63) >= nvec) continue;
+        float x[V::N], a = m, s = sum;
         V::get(v[i], x);
-        online(x, cl, m, sum);
+        online(x, cl, a, s);
+        const bool in = b0 + i * Threads + tid < nvec;
+        m = in ? a : m;
+        sum = in ? s : sum;
       }
     }
-    for (; j < P.vocab; j += (int64_t)Threads * V::N) {
-      float x[V::N];
-      V::get(V::load(z, j, P.vocab), x);
-      online(x, cl, m, sum);
+    if (nvec * V::N + tid < P.vocab) {
+      const float one[1] = {to_f32(z[nvec * V::N + tid])};
+      online(one, cl, m, sum);
     }
     E.decode(P);
-    E.gather(z, 0, (int)P.vocab);
+    E.gather(z, P.k, 0, (int)P.vocab);
     teacher_share(E, P.k, it, vm, ps);
     int present = 0;
 #pragma unroll
@@ -461,7 +487,7 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
   }
   student_join(J, cl, m, sum);
   if (E.mine(P.k)) {
-    const double term = teacher_terms(E, J, it, m, sum, nullptr);
+    const double term = teacher_terms(E, P.k, J, it, m, sum, nullptr);
     if ((tid & 63) == 0) J.term[wave] = term;
   }
   __syncthreads();
@@ -478,14 +504,13 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
 
 // The gradient from the row's maximum and sum: workgroup (row, part) does a
 // chunk of the row and the teacher's entries inside it.
-constexpr int kGradThreads = 512, kGradChunk = 16;  // vectors a thread
-template <int DT> __global__ void __launch_bounds__(kGradThreads, 4) distill_grad(DistillParams P, int parts) {
+template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) distill_grad(DistillParams P, int parts) {
   typedef typename Elem<DT>::type T;
   typedef Vec<DT> V;
-  constexpr int Threads = kGradThreads, kWaves = Threads / 64, kUnroll = 8;
+  constexpr int kWaves = Threads / 64, kUnroll = 8;
   __shared__ Joined<kWaves> J;
-  __shared__ int s_id[kTop];
-  __shared__ float s_p[kTop];
+  __shared__ __attribute__((aligned(16))) int s_id[kTop];
+  __shared__ __attribute__((aligned(16))) float s_p[kTop];
   const int tid = threadIdx.x, wave = tid >> 6;
   const auto [cl, it] = scales(P);
   const int64_t row = blockIdx.x / (unsigned)parts;
@@ -503,7 +528,7 @@ template <int DT> __global__ void __launch_bounds__(kGradThreads, 4) distill_gra
     m = P.stats[2 * row];
     inv = 1.0f / P.stats[2 * row + 1];
     E.decode(P);
-    E.gather(z, (int)lo, (int)hi);
+    E.gather(z, P.k, (int)lo, (int)hi);
     float vm;
     double ps;
     teacher_share(E, P.k, it, vm, ps);
@@ -511,7 +536,7 @@ template <int DT> __global__ void __launch_bounds__(kGradThreads, 4) distill_gra
 #pragma unroll
     for (int q = 0; q < E.kPer; ++q) {
       present |= E.id[q] >= 0;
-      if (tid + q * Threads < P.k) s_id[tid + q * Threads] = E.id[q];
+      if (q * Threads < P.k && tid + q * Threads < ((P.k + 3) & ~3)) s_id[tid + q * Threads] = E.id[q];
     }
     const int flags = (__any(present) ? 1 : 0) | (__any(E.bad) ? 2 : 0);
     if ((tid & 63) == 0) {
@@ -531,7 +556,7 @@ template <int DT> __global__ void __launch_bounds__(kGradThreads, 4) distill_gra
       teacher_join(J, it, vm, logps);
 #pragma unroll
       for (int q = 0; q < E.kPer; ++q)
-        if (E.id[q] >= 0) s_p[tid + q * Threads] = (float)exp(((double)E.v[q] - (double)vm) * it - logps);
+        if (q * Threads < P.k && E.id[q] >= 0) s_p[tid + q * Threads] = (float)exp(((double)E.v[q] - (double)vm) * it - logps);
     }
     if (!zero && any_twice<Threads>(s_id, P.k)) J.dup = 1;
   }
@@ -561,15 +586,26 @@ template <int DT> __global__ void __launch_bounds__(kGradThreads, 4) distill_gra
       }
     }
   }
-  for (; j < hi; j += step) {
+  // what is left: at most kUnroll vectors a thread, the last perhaps not whole
+  const int64_t first = j - (int64_t)(tid & 63) * V::N;  // the wave's first element
+  u32x4 v[kUnroll];
+  if (!zero && hi - lo >= V::N) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+      if (first + i * step < hi) v[i] = *reinterpret_cast<const typename V::U*>(z + min(j + i * step, hi - V::N));
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const int64_t at = j + i * step;
+    if (at >= hi) break;
     float g[V::N];
     if (zero) {
 #pragma unroll
       for (int e = 0; e < V::N; ++e) g[e] = 0.0f;
     } else {
-      slope(V::load(z, j, hi), g);
+      slope(at + V::N <= hi ? v[i] : V::load(z, at, hi), g);
     }
-    V::store(dz, j, hi, g);
+    V::store(dz, at, hi, g);
   }
   if (zero) return;
   __syncthreads();
@@ -586,15 +622,22 @@ template <int DT> void launch_loss(const DistillParams& P, hipStream_t stream) {
   // few rows, or long ones: more threads a row
   if (P.n <= 512 && P.vocab > 16384) distill_loss<DT, 1024><<<(unsigned)P.n, 1024, 0, stream>>>(P);
   else if (P.vocab > 8192) distill_loss<DT, 512><<<(unsigned)P.n, 512, 0, stream>>>(P);
-  else distill_loss<DT, 256><<<(unsigned)P.n, 256, 0, stream>>>(P);
+  else if (P.vocab > 2048) distill_loss<DT, 256><<<(unsigned)P.n, 256, 0, stream>>>(P);
+  else distill_loss<DT, 128><<<(unsigned)P.n, 128, 0, stream>>>(P);
 }
 
 template <int DT> void launch_grad(const DistillParams& P, hipStream_t stream) {
-  const int64_t chunk = (int64_t)kGradThreads * kGradChunk * Vec<DT>::N;
-  int64_t parts = (P.vocab + chunk - 1) / chunk;
+  // up to 16 vectors a thread; short rows take fewer threads (8192 rows of
+  // 1000: 128 threads 29 us, 512 threads 56 us)
+  const int64_t vecs = P.vocab / Vec<DT>::N;
+  const int threads = vecs <= 1024 ? 128 : vecs <= 2048 ? 256 : 512;
+  int64_t parts = (vecs + 16 * threads) / (16 * threads);
   // a grid has fewer than 2^31 workgroups
   while (parts > 1 && parts * P.n >= ((int64_t)1 << 31)) parts = (parts + 1) / 2;
-  distill_grad<DT><<<(unsigned)(P.n * parts), kGradThreads, 0, stream>>>(P, (int)parts);
+  const unsigned grid = (unsigned)(P.n * parts);
+  if (threads == 128) distill_grad<DT, 128><<<grid, 128, 0, stream>>>(P, (int)parts);
+  else if (threads == 256) distill_grad<DT, 256><<<grid, 256, 0, stream>>>(P, (int)parts);
+  else distill_grad<DT, 512><<<grid, 512, 0, stream>>>(P, (int)parts);
 }
 
 template <int DT> hipError_t launch(DistillParams P, hipStream_t stream) {
@@ -607,6 +650,8 @@ template <int DT> hipError_t launch(DistillParams P, hipStream_t stream) {
     if (!P.stats) P.stats = static_cast<float*>(P.work);
     launch_loss<DT>(P, stream);
     launch_grad<DT>(P, stream);
+  } else if (vecs <= 512) {
+    launch_resident<DT, 128, 4>(P, stream);
   } else if (vecs <= 1024) {
     launch_resident<DT, 256, 4>(P, stream);
   } else if (P.n <= 256) {
