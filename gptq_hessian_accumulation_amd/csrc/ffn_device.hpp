@@ -10,12 +10,15 @@
 namespace hess {
 
 // act(g) and act'(g) in float32.  tanh goes through the sigmoid
-// (0.5 (1 + tanh s) = sigmoid(2 s)), so the left tail keeps its relative
-// accuracy.  Exact: float32 outputs, where the exponential's last bits count;
-// otherwise the hardware exponential of a rounded argument.
+// (0.5 (1 + tanh s) = sigmoid(2 s)) and the sigmoid through exp(-|v|), so the
+// left tails keep their relative accuracy down to the smallest numbers.
+// Exact: float32 outputs, where the exponential's last bits count; otherwise
+// the hardware exponential of a rounded argument.
 template <bool Exact> __device__ __forceinline__ float sigmoidf(float v) {
-  if constexpr (Exact) return 1.0f / (1.0f + expf(-v));
-  else return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+  const float e = Exact ? expf(-fabsf(v)) : __expf(-fabsf(v));
+  const float top = v >= 0.0f ? 1.0f : e;
+  if constexpr (Exact) return top / (1.0f + e);
+  else return top * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // 0.5 erfcx(z) / t by powers of t, and what the float constant -0.72134751

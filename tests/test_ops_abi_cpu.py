@@ -133,3 +133,17 @@ def test_binding_refuses_host_tensors_and_unknown_names():
         hs.distill_topk_forward(z, ids, v)
     with pytest.raises(ValueError, match="constants"):
         hs.distill_topk(z, ids, v.requires_grad_())
+
+
+def test_ffn_refuses_rows_off_16_bytes():
+    """More tokens than the kernel that takes any alignment: the C entry refuses, the binding copies."""
+    for dtype, off in ((0, 2), (1, 4), (2, 8)):
+        for p in range(3):
+            ptrs = [_ptr(i, off if i == p else 0) for i in range(4)]
+            assert _forward(n=100, dtype=dtype, ptrs=ptrs) == EALIGN and b"16-byte" in _message()
+    assert _forward(n=100, ld=(25, 24, 24, 40)) == EALIGN
+    assert _forward(n=100, ld=(24, 28, 24, 40)) == EALIGN
+    assert hs._load().hess_gated_ffn_workspace(5, 24, 40, 0, 0) == 0
+    # rows that are copied need room for x and both weights
+    room = hs._load().hess_gated_ffn_workspace(100, 25, 40, 0, 0) - hs._load().hess_gated_ffn_workspace(100, 32, 40, 0, 0)
+    assert room >= 2 * 32 * (100 + 2 * 40)
