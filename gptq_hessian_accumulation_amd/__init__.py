@@ -769,14 +769,18 @@ def _row_floats(name, t, lead, like):
 
 
 def _grad_out(out, logits):
+    if out is None:
+        # contiguous whatever the strides of logits
+        return torch.empty_like(logits, memory_format=torch.contiguous_format), logits.shape[-1]
     grad = _out("out", out, logits.shape, logits)
-    return grad, (grad.stride(0) if out is not None and grad.dim() == 2 and grad.shape[0] > 1 else logits.shape[-1])
+    return grad, (grad.stride(0) if grad.dim() == 2 and grad.shape[0] > 1 else logits.shape[-1])
 
 
 def _distill_call(logits, ids, values, weight, temperature, want_stats, want_grad, out, workspace):
     lib = _load()
     keep, lead, n, vocab, code, args = _distill_args(logits, ids, values, weight, temperature)
-    loss = logits.new_empty(lead, dtype=torch.float32)
+    w = keep[3]
+    loss = torch.empty_like(w) if w is not None else logits.new_empty(lead, dtype=torch.float32)
     stats = logits.new_empty((*lead, 2), dtype=torch.float32) if want_stats else None
     grad, ldg = _grad_out(out, logits) if want_grad else (None, 0)
     wp, wb, work = _workspace(workspace, lib.hess_distill_topk_workspace(n, vocab, code), logits)

@@ -49,10 +49,15 @@ hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int edge, int dtype, hipS
 constexpr int64_t kFfnFew = 64;
 hipError_t launch_ffn_few(const FfnGemm& g, int dtype, hipStream_t stream);
 
-// Copies rows x cols 16-bit values (row stride ld) to rows of pad >= cols (a
-// multiple of 8) values, zeros past cols.
-hipError_t launch_pack_rows16(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t pad,
-                              hipStream_t stream);
+// Copies up to three matrices of rows[m] x cols 16-bit values (row stride
+// ld[m]) to rows of pad >= cols (a multiple of 8) values, zeros past cols.
+struct PackRows {
+  const void* src[3];
+  void* dst[3];
+  int64_t ld[3], rows[3];
+  int count, cols, pad;
+};
+hipError_t launch_pack_rows16(const PackRows& p, hipStream_t stream);
 
 // dg = dh u act'(g), du = dh act(g) into the n x 2 fp pair dgu (columns past f zero).
 hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f,

@@ -380,17 +380,19 @@ template <int DT> hipError_t launch_type(const FfnGemm& g, int mode, int edge, h
   return launch_mode<DT, kFfnDw>(g, edge, stream);
 }
 
-// Row r of a matrix of `cols` 16-bit values to a row of `pad` (a multiple of
-// 8), the rest zeros; 8 values a thread.
-__global__ void __launch_bounds__(256) pack_rows16(const uint16_t* src, int64_t ld, int cols, uint16_t* dst, int pad,
-                                                   int64_t total) {
+// Matrix blockIdx.y: rows of `cols` 16-bit values to rows of `pad` (a multiple
+// of 8), the rest zeros; 8 values a thread.
+__global__ void __launch_bounds__(256) pack_rows16(PackRows P) {
   typedef uint16_t V __attribute__((ext_vector_type(8)));
   typedef V VU __attribute__((aligned(2)));
-  const int per = pad / 8;
+  const int m = blockIdx.y, cols = P.cols, per = P.pad / 8;
+  const uint16_t* src = static_cast<const uint16_t*>(P.src[m]);
+  uint16_t* dst = static_cast<uint16_t*>(P.dst[m]);
+  const int64_t total = P.rows[m] * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per) * 8;
-    const uint16_t* p = src + r * ld + c;
+    const uint16_t* p = src + r * P.ld[m] + c;
     V v;
     if (c + 8 <= cols) {
       v = *reinterpret_cast<const VU*>(p);
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(256) pack_rows16(const uint16_t* src, int64_t 
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? p[j] : (uint16_t)0;
     }
-    *reinterpret_cast<V*>(dst + r * pad + c) = v;
+    *reinterpret_cast<V*>(dst + r * P.pad + c) = v;
   }
 }
 
@@ -410,13 +412,13 @@ hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int edge, int dtype, hipS
   return launch_type<kInF32>(g, mode, edge, stream);
 }
 
-hipError_t launch_pack_rows16(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t pad,
-                              hipStream_t stream) {
-  const int64_t total = rows * (pad / 8);
+hipError_t launch_pack_rows16(const PackRows& p, hipStream_t stream) {
+  int64_t most = 0;
+  for (int m = 0; m < p.count; ++m) most = p.rows[m] > most ? p.rows[m] : most;
+  const int64_t total = most * (p.pad / 8);
   if (total == 0) return hipSuccess;
-  const int grid = (int)(total < 256 * 4096 ? (total + 255) / 256 : 4096);
-  pack_rows16<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(src), ld, (int)cols, static_cast<uint16_t*>(dst),
-                                        (int)pad, total);
+  const int grid = (int)(total < 256 * 2048 ? (total + 255) / 256 : 2048);
+  pack_rows16<<<dim3(grid, p.count), 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 

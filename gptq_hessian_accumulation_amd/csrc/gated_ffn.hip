@@ -22,13 +22,24 @@ namespace hess {
 
 namespace {
 
-// dg, du from dh and the saved pair, 8 columns a thread.
-template <int DT, bool Vec>
+// dg, du from dh and the saved pair, 8 columns a thread; dh's rows may start
+// anywhere.  Bound by its 5 n f elements (bf16, 8192 x 11264: 175 us, 5.3
+// TB/s).
+//
+// Roundings: g, u were rounded to the operands' type when the forward pass
+// saved them, and dg, du are rounded to it here, because the two products that
+// follow take matrix instructions of that type.  Together they put a relative
+// error of about one and a half steps of the final rounding (bf16 0.0026 root
+// mean square) into the gradients, spread evenly.  Avoiding it would take the
+// pair in float32 (twice the memory a training step keeps) and a second 16-bit
+// term of dg and du (twice the matrix work of the backward pass).
+template <int DT>
 __global__ void __launch_bounds__(256) ffn_dgu(const typename Elem<DT>::type* dh, int64_t lddh,
                                                const typename Elem<DT>::type* pre, typename Elem<DT>::type* out,
                                                int64_t f, int64_t fp, int act) {
   typedef typename Elem<DT>::type T;
   typedef T T8 __attribute__((ext_vector_type(8)));
+  typedef T8 T8u __attribute__((aligned(sizeof(T))));
   const int64_t row = blockIdx.y;
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (c >= fp) return;
@@ -36,8 +47,8 @@ __global__ void __launch_bounds__(256) ffn_dgu(const typename Elem<DT>::type* dh
   const T8 g8 = *reinterpret_cast<const T8*>(q), u8 = *reinterpret_cast<const T8*>(q + fp);
   T8 h8;
   const T* hp = dh + row * lddh + c;
-  if (Vec && c + 8 <= f) {
-    h8 = *reinterpret_cast<const T8*>(hp);
+  if (c + 8 <= f) {
+    h8 = *reinterpret_cast<const T8u*>(hp);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) h8[j] = c + j < f ? hp[j] : (T)0.0f;
@@ -65,7 +76,6 @@ template <int DT>
 hipError_t dgu_dtype(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f, int64_t fp,
                      int act, hipStream_t stream) {
   typedef typename Elem<DT>::type T;
-  const bool vec = ((reinterpret_cast<uintptr_t>(dh) | (uint64_t)(lddh * sizeof(T))) & 15u) == 0;
   const unsigned gx = (unsigned)((fp / 8 + 255) / 256);
   // a grid has at most 65,535 rows
   for (int64_t r0 = 0; r0 < n; r0 += 65535) {
@@ -73,8 +83,7 @@ hipError_t dgu_dtype(const void* dh, int64_t lddh, const void* preact, void* dgu
     const T* d = static_cast<const T*>(dh) + r0 * lddh;
     const T* p = static_cast<const T*>(preact) + r0 * 2 * fp;
     T* o = static_cast<T*>(dgu) + r0 * 2 * fp;
-    if (vec) ffn_dgu<DT, true><<<dim3(gx, rows), 256, 0, stream>>>(d, lddh, p, o, f, fp, act);
-    else ffn_dgu<DT, false><<<dim3(gx, rows), 256, 0, stream>>>(d, lddh, p, o, f, fp, act);
+    ffn_dgu<DT><<<dim3(gx, rows), 256, 0, stream>>>(d, lddh, p, o, f, fp, act);
   }
   return hipGetLastError();
 }

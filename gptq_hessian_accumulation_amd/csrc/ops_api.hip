@@ -134,11 +134,22 @@ int place_operands(FfnOperands& o, char* pack, int64_t n, int64_t f, int dtype, 
   const int64_t pad = up(o.d, step), half = elem_bytes(dtype) / 2;  // a float32 moves as two 16-bit halves
   char* pg = pack + pack_bytes(n, o.d, dtype);
   char* pu = pg + pack_bytes(f, o.d, dtype);
-  hipError_t e = hipSuccess;
-  if (want_x) e = launch_pack_rows16(o.x, o.ldx * half, n, o.d * half, pack, pad * half, s);
-  if (want_w && e == hipSuccess) e = launch_pack_rows16(o.wg, o.ldg * half, f, o.d * half, pg, pad * half, s);
-  if (want_w && e == hipSuccess) e = launch_pack_rows16(o.wu, o.ldu * half, f, o.d * half, pu, pad * half, s);
-  if (e != hipSuccess) return hip_fail(e, "operand copy launch");
+  PackRows p{};
+  p.cols = (int)(o.d * half);
+  p.pad = (int)(pad * half);
+  auto add = [&](const void* src, int64_t ld, int64_t rows, void* dst) {
+    p.src[p.count] = src;
+    p.dst[p.count] = dst;
+    p.ld[p.count] = ld * half;
+    p.rows[p.count++] = rows;
+  };
+  if (want_x) add(o.x, o.ldx, n, pack);
+  if (want_w) add(o.wg, o.ldg, f, pg);
+  if (want_w) add(o.wu, o.ldu, f, pu);
+  if (p.count > 0) {
+    const hipError_t e = launch_pack_rows16(p, s);
+    if (e != hipSuccess) return hip_fail(e, "operand copy launch");
+  }
   o = FfnOperands{pack, pg, pu, pad, pad, pad, pad};
   return HESS_OK;
 }
