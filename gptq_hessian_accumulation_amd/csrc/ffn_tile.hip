@@ -39,29 +39,37 @@ constexpr int64_t kAll = 0x7fffffff;
 constexpr int kStages = 5, kAhead = 4;
 
 template <int DT, int Mode, int Edge>
-__global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
+__global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) ffn_tile(FfnGemm P) {
   constexpr bool kRowsA = Mode != kFfnDw;  // A's rows run along K
   constexpr bool kRowsB = Mode == kFfnFwd;
-  constexpr int kColWaves = Edge / 64;     // the tile's waves are 2 x kColWaves
-  constexpr int kBm = Edge / 32, kBn = 4;  // 16-wide blocks of a wave
+  constexpr int kColWaves = Edge == 256 ? 4 : 2;  // the tile's waves are 2 x kColWaves
+  constexpr int kCols = Edge / kColWaves;         // columns of a wave
+  constexpr int kBm = Edge / 32, kBn = kCols / 16;  // 16-wide blocks of a wave
   constexpr int kSize = Elem<DT>::size;
   constexpr int kStep = 64 / kSize, kPiece = 16 / kSize;  // values of K in a stage and a 16-byte chunk
   constexpr int kPanel = Edge * 64;
   constexpr int kStage = 2 * kPanel;
-  constexpr int kLoads = 2;                // 1-KB loads per wave, panel and stage
+  constexpr int kLoads = kPanel / 1024 / (2 * kColWaves);  // 1-KB loads per wave, panel and stage
   constexpr int kRow = Edge * kSize;           // bytes of one k of a panel kept k by k
   constexpr int kPerK = 1024 / kRow;       // k's in one load of such a panel
   __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
   // place of a chunk of columns in row k of a panel kept k by k; float32: the
   // lane rows of a read (k = 4 g + j) land in four 64-byte parts of the banks
-  auto place = [](int k, int c) { return kSize == 2 ? chunk_pos(k, c) : c ^ (4 * ((k >> 2) & 3)); };
+  // (a 16-bit row of edge 64 has 8 chunks, the others 16 or more)
+  auto place = [](int k, int c) {
+    return kSize == 4 ? c ^ (4 * ((k >> 2) & 3)) : Edge == 64 ? c ^ (2 * (k & 3)) : chunk_pos(k, c);
+  };
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / kColWaves, wc = wave % kColWaves;
   const uint32_t lds0 = (uint32_t) reinterpret_cast<uintptr_t>((HESS_LDS char*)lds);
 
-  const int item = item_of_block(blockIdx.x, gridDim.x);
+  // the whole tiles and the parts are dealt to the XCDs separately, so that
+  // each has its share of either
+  const int block = blockIdx.x;
+  const int item = block < P.full ? item_of_block(block, P.full)
+                                  : P.full + item_of_block(block - P.full, (int)gridDim.x - P.full);
   const int tail = P.ntiles - P.full;
   int t = item, part = 0;
   const bool whole = item < P.full;
@@ -93,7 +101,7 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
     else voffA[i] = i0 + col < P.M ? (uint32_t)(k * rowA + col * kSize) : kOOB;
     if constexpr (kRowsB) {
       // the wave's B rows are of one projection (see fwd_column)
-      const int feat = (wave >> 1) * 32 + 16 * i + (lane >> 2);
+      const int feat = (wave >> 1) * (kCols / 2) + 16 * i + (lane >> 2);
       voffB[i] = j0 + feat < P.N ? (uint32_t)(feat * (int64_t)((wave & 1) ? P.ldb1 : P.ldb0) * kSize + chunk * 16) : kOOB;
     } else {
       const int64_t ld = Mode == kFfnDx ? 0 : rowB;  // dx: the segment's stride, added per iteration
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
     const int col = col0 + (kSize == 2 ? 4 * (lane & 3) : lane & 15);
     return tl * kRow + (place(tl, col / kPiece) << 4) + (col % kPiece) * kSize;
   };
-  const int posA = lane_pos(kRowsA, wr * (Edge / 2)), posB = lane_pos(kRowsB, wc * 64);
+  const int posA = lane_pos(kRowsA, wr * (Edge / 2)), posB = lane_pos(kRowsB, wc * kCols);
   auto read1 = [&](const char* stage, int pos, int m, bool rows) {
     if (rows) return *reinterpret_cast<const u32x4*>(stage + pos + m * 1024);
     const char* p = stage + (pos ^ (m << (kSize == 2 ? 5 : 6)));
@@ -199,8 +207,9 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
   // and meets the others (the next stage is then complete, and nobody reads
   // the one before cur); up to there it works on operands already read, so
   // that the matrix instructions run on from one iteration to the next.
+  constexpr int kRot = kBm < 4 ? kBm : 4;  // A blocks in registers
   constexpr int kMeet = kBm - 6 > 0 ? kBm - 6 : 0;
-  u32x4 a[4];
+  u32x4 a[kRot];
   auto step = [&](uint32_t cur, uint32_t nxt, uint32_t target, int j, const u32x4 (&b)[kBn], u32x4 (&c)[kBn]) {
     const Next d = describe(j + kAhead);
     __builtin_amdgcn_sched_barrier(0);
@@ -212,16 +221,16 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int n = 0; n < kBn; ++n) acc[m][n] = mma16<DT>(b[n], a[m & 3], acc[m][n]);
-      a[m & 3] = m + 4 < kBm ? read_a(cur, m + 4) : read_a(nxt, m + 4 - kBm);
-      if (m >= kMeet && m < kMeet + 4) {
+      for (int n = 0; n < kBn; ++n) acc[m][n] = mma16<DT>(b[n], a[m % kRot], acc[m][n]);
+      a[m % kRot] = m + kRot < kBm ? read_a(cur, m + kRot) : read_a(nxt, m + kRot - kBm);
+      if (m >= kMeet && m < kMeet + kRot) {
         c[m - kMeet] = read_b(nxt, m - kMeet);
         load1(lds0 + target, d, m - kMeet);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  static_assert(2 * kLoads == 4 && kBn == 4, "one load and one read of B in each of four groups");
+  static_assert(2 * kLoads == kRot && kBn == kRot, "one load and one read of B in each of kRot groups");
 
 #pragma unroll
   for (int q = 0; q < kAhead; ++q) load_stage(lds0 + q * kStage, it0 + q);
@@ -230,7 +239,7 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
   __builtin_amdgcn_sched_barrier(0);
   u32x4 b[kBn], c[kBn];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) a[q] = read_a(0, q);
+  for (int q = 0; q < kRot; ++q) a[q] = read_a(0, q);
 #pragma unroll
   for (int q = 0; q < kBn; ++q) b[q] = read_b(0, q);
   // two iterations a trip (two sets of B registers); an extra iteration
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
 
   if (!whole) {
     float* W = P.ws + ((int64_t)part * tail + (t - P.full)) * (Edge * Edge) +
-               (wr * (Edge / 2) + (lane & 15)) * Edge + wc * 64 + 4 * (lane >> 4);
+               (wr * (Edge / 2) + (lane & 15)) * Edge + wc * kCols + 4 * (lane >> 4);
 #pragma unroll
     for (int m = 0; m < kBm; ++m)
 #pragma unroll
@@ -280,31 +289,43 @@ __global__ void __launch_bounds__(2 * Edge, 2) ffn_tile(FfnGemm P) {
         o[4 + j] = __uint_as_float(s[1]);
       }
     };
+    // features of one row, forward
+    auto put_features = [&](int64_t r, int64_t col, const float (&g)[8], const float (&u)[8]) {
+      if constexpr (In) {
+        float h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = act_value<DT == kInF32>(g[e], P.act) * u[e];
+        store_n(static_cast<T*>(P.o0) + r * P.ldo0 + col, h, 8);
+        if (P.o1) {
+          T* pre = static_cast<T*>(P.o1) + r * 2 * P.fp + col;
+          store_n(pre, g, 8);
+          store_n(pre + P.fp, u, 8);
+        }
+      } else {
+        put_fwd<DT>(P, r, col, g, u);
+      }
+    };
+    if constexpr (Mode == kFfnFwd && kBn == 2) {
+      // one block of either projection: two rows of blocks are exchanged
+      // instead, and lane row g holds row block g % 2
+      float g[8], u[8];
+      eight(acc[0][0], acc[1][0], g);
+      eight(acc[0][1], acc[1][1], u);
+      put_features(i0 + wr * (Edge / 2) + (lv & 15) + 16 * ((lv >> 4) & 1), j0 + wc * (kCols / 2) + 8 * (lv >> 5), g, u);
+      return;
+    }
 #pragma unroll
     for (int m = 0; m < kBm; ++m) {
       const int64_t r = i0 + wr * (Edge / 2) + (lv & 15) + 16 * m;
       if constexpr (Mode == kFfnFwd) {
-        const int64_t col = j0 + wc * 32 + cc;
         float g[8], u[8];
         eight(acc[m][0], acc[m][1], g);
-        eight(acc[m][2], acc[m][3], u);
-        if constexpr (In) {
-          float h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = act_value<DT == kInF32>(g[e], P.act) * u[e];
-          store_n(static_cast<T*>(P.o0) + r * P.ldo0 + col, h, 8);
-          if (P.o1) {
-            T* pre = static_cast<T*>(P.o1) + r * 2 * P.fp + col;
-            store_n(pre, g, 8);
-            store_n(pre + P.fp, u, 8);
-          }
-        } else {
-          put_fwd<DT>(P, r, col, g, u);
-        }
+        eight(acc[m][kBn / 2], acc[m][kBn / 2 + 1], u);
+        put_features(r, j0 + wc * (kCols / 2) + cc, g, u);
       } else {
 #pragma unroll
         for (int n = 0; n < kBn; n += 2) {
-          const int64_t col = j0 + wc * 64 + 16 * n + cc;
+          const int64_t col = j0 + wc * kCols + 16 * n + cc;
           float v[8];
           eight(acc[m][n], acc[m][n + 1], v);
           if constexpr (In) {
@@ -340,16 +361,17 @@ template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn
   const float* W = P.ws + (int64_t)t * (Edge * Edge) + row * Edge;
   const int64_t stride = (int64_t)tail * (Edge * Edge);
   if constexpr (Mode == kFfnFwd) {
-    const int w = quad >> 3, q = quad & 7;  // wave column, quad of its features
-    const int cg = w * 64 + 4 * q;
+    constexpr int cols = Edge == 64 ? 32 : 64;  // of a wave: half gate, half up
+    const int w = quad / (cols / 8), q = quad % (cols / 8);
+    const int cg = w * cols + 4 * q;
     float g[4] = {}, u[4] = {};
     for (int p = 0; p < P.parts; ++p) {
       const float4 a = *reinterpret_cast<const float4*>(W + p * stride + cg);
-      const float4 b = *reinterpret_cast<const float4*>(W + p * stride + cg + 32);
+      const float4 b = *reinterpret_cast<const float4*>(W + p * stride + cg + cols / 2);
       g[0] += a.x, g[1] += a.y, g[2] += a.z, g[3] += a.w;
       u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
     }
-    put_fwd<DT>(P, (int64_t)I * Edge + row, (int64_t)J * (Edge / 2) + w * 32 + 4 * q, g, u);
+    put_fwd<DT>(P, (int64_t)I * Edge + row, (int64_t)J * (Edge / 2) + w * (cols / 2) + 4 * q, g, u);
   } else {
     float v[4] = {};
     for (int p = 0; p < P.parts; ++p) {
@@ -362,7 +384,7 @@ template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn
 
 template <int DT, int Mode, int Edge> void launch_edge(const FfnGemm& g, hipStream_t stream) {
   const int tail = g.ntiles - g.full;
-  ffn_tile<DT, Mode, Edge><<<g.full + tail * g.parts, 2 * Edge, 0, stream>>>(g);
+  ffn_tile<DT, Mode, Edge><<<g.full + tail * g.parts, Edge == 256 ? 512 : 256, 0, stream>>>(g);
   if (tail == 0) return;
   constexpr int quads = Mode == kFfnFwd ? Edge / 8 : Edge / 4;
   ffn_join<DT, Mode, Edge><<<dim3(tail, Edge * quads / 256), 256, 0, stream>>>(g);
@@ -370,7 +392,8 @@ template <int DT, int Mode, int Edge> void launch_edge(const FfnGemm& g, hipStre
 
 template <int DT, int Mode> hipError_t launch_mode(const FfnGemm& g, int edge, hipStream_t stream) {
   if (edge == 256) launch_edge<DT, Mode, 256>(g, stream);
-  else launch_edge<DT, Mode, 128>(g, stream);
+  else if (edge == 128) launch_edge<DT, Mode, 128>(g, stream);
+  else launch_edge<DT, Mode, 64>(g, stream);
   return hipGetLastError();
 }
 

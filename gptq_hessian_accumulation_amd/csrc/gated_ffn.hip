@@ -92,22 +92,27 @@ hipError_t dgu_dtype(const void* dh, int64_t lddh, const void* preact, void* dgu
 
 namespace {
 
-// What a launch of `groups` workgroups, at most one round of the card, takes
-// per stage of K (us), from forward, dx and dW products timed at 128 .. 8192
-// tokens.  Edge 256 keeps one workgroup a CU, edge 128 two.  16-bit products
-// are slowed by the card's power and by operand traffic as it fills (0.50 us
-// alone, 0.83 us on all CUs); two workgroups of edge 128 reach 0.75 of edge
-// 256's rate.  Float32 products are bound by the matrix cores.
+// Places for workgroups on the card: a CU holds one of edge 256, two of edge
+// 128, four of edge 64.
+int slots_of(int edge) { return edge == 256 ? 256 : edge == 128 ? 512 : 1024; }
+
+// What `groups` workgroups at once, at most one for each place, take per stage
+// of K (us), from products timed at 64 .. 8192 tokens.  Float32 is bound by
+// the matrix cores; 16-bit products of edge 256 are slowed by the card's power
+// as it fills (0.50 us alone, 0.83 us on all CUs), and smaller edges reach
+// 0.7 (128) and 0.4 (64) of its rate, but divide the work more evenly over the
+// CUs: 300 tokens at 704 x 1000, bf16, take 7.7 us with edge 64, 11.6 with 128
+// and 24 with 256; 1999 at 2560 x 9728 take 400, 260 and 213.
 double stage_us(int edge, int groups, bool f32) {
-  const bool two = groups > 256;
-  if (f32) return edge == 256 ? 3.7 : two ? 1.94 : 1.03;
-  if (edge == 256) return 0.50 + 0.33 * groups / 256;
-  return two ? 0.50 + 0.12 * groups / 512 : 0.24 + 0.10 * groups / 256;
+  const int each = (groups + 255) / 256;  // on the busiest CU
+  if (edge == 256) return f32 ? 3.7 : 0.50 + 0.33 * groups / 256;
+  if (edge == 128) return f32 ? (each == 1 ? 1.03 : 0.97 * each) : (each == 1 ? 0.27 : 0.31 * each);
+  return f32 ? std::max(0.35, 0.27 * each) : std::max(0.20, 0.135 * each);
 }
 
 // The schedule for tiles of one edge, and its estimated time in us.
 double schedule_for(FfnGemm& g, int mode, int edge, bool f32) {
-  const int step = f32 ? 16 : 32, slots = edge == 256 ? 256 : 512;
+  const int step = f32 ? 16 : 32, slots = slots_of(edge);
   const int cols = mode == kFfnFwd ? edge / 2 : edge;
   g.tm = (int)((g.M + edge - 1) / edge);
   g.tn = (int)((g.N + cols - 1) / cols);
@@ -119,8 +124,8 @@ double schedule_for(FfnGemm& g, int mode, int edge, bool f32) {
   g.part_len = g.niter;
   // whole tiles fill complete rounds of the card; the tiles of a last, partly
   // empty round may be cut along K into parts of at least 256 values, whose
-  // sums go through memory (written and read at 4 TB/s) and a second launch
-  const double enter = 5.0, join = 8.0;
+  // sums go through memory (written and read at 5 TB/s) and a second launch
+  const double enter = edge == 256 ? 5.0 : 4.0, join = 4.0;
   const int tail = g.ntiles % slots;
   double us = (double)(g.ntiles / slots) * (g.niter * stage_us(edge, slots, f32) + enter);
   if (tail == 0) return us;
@@ -128,7 +133,7 @@ double schedule_for(FfnGemm& g, int mode, int edge, bool f32) {
   for (int parts = 1; parts <= std::max(1, std::min(slots / tail, g.niter / (256 / step))); ++parts) {
     const int len = (g.niter + parts - 1) / parts;
     double t = len * stage_us(edge, tail * parts, f32) + enter;
-    if (parts > 1) t += join + (double)tail * parts * edge * edge * 8.0 / 4e6;
+    if (parts > 1) t += join + (double)tail * parts * edge * edge * 8.0 / 5e6;
     if (t >= best) continue;
     best = t;
     if (parts > 1) {
@@ -143,12 +148,19 @@ double schedule_for(FfnGemm& g, int mode, int edge, bool f32) {
 }  // namespace
 
 int ffn_schedule(FfnGemm& g, int mode, int dtype) {
-  FfnGemm small = g;
-  const double big_us = schedule_for(g, mode, 256, dtype == kInF32);
-  const double small_us = schedule_for(small, mode, 128, dtype == kInF32);
-  if (big_us <= small_us) return 256;
-  g = small;
-  return 128;
+  int edge = 0;
+  double least = 1e30;
+  FfnGemm chosen{};
+  for (int e : {256, 128, 64}) {
+    FfnGemm s = g;
+    const double us = schedule_for(s, mode, e, dtype == kInF32);
+    if (us >= least) continue;
+    least = us;
+    edge = e;
+    chosen = s;
+  }
+  g = chosen;
+  return edge;
 }
 
 hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f,
