@@ -103,10 +103,10 @@ int slots_of(int edge) { return edge == 256 ? 256 : edge == 128 ? 512 : 1024; }
 // 0.7 (128) and 0.4 (64) of its rate, but divide the work more evenly over the
 // CUs: 300 tokens at 704 x 1000, bf16, take 7.7 us with edge 64, 11.6 with 128
 // and 24 with 256; 1999 at 2560 x 9728 take 400, 260 and 213.
-double stage_us(int edge, int groups, bool f32) {
+double stage_us(int edge, int groups, bool f32, int mode) {
   const int each = (groups + 255) / 256;  // on the busiest CU
   if (edge == 256) return f32 ? 3.7 : 0.50 + 0.33 * groups / 256;
-  if (edge == 128) return f32 ? (each == 1 ? 1.03 : 0.97 * each) : (each == 1 ? 0.27 : 0.31 * each);
+  if (edge == 128) return f32 ? (each == 1 ? 1.03 : 0.97 * each) : (each > 1 ? 0.31 * each : mode == kFfnFwd ? 0.27 : 0.33);
   return f32 ? std::max(0.35, 0.27 * each) : std::max(0.20, 0.135 * each);
 }
 
@@ -124,16 +124,17 @@ double schedule_for(FfnGemm& g, int mode, int edge, bool f32) {
   g.part_len = g.niter;
   // whole tiles fill complete rounds of the card; the tiles of a last, partly
   // empty round may be cut along K into parts of at least 256 values, whose
-  // sums go through memory (written and read at 5 TB/s) and a second launch
-  const double enter = edge == 256 ? 5.0 : 4.0, join = 4.0;
+  // sums go through the last-level cache (written and read at 12 TB/s) and a
+  // second launch
+  const double enter = edge == 256 ? 8.0 : 4.0, join = 3.0;
   const int tail = g.ntiles % slots;
-  double us = (double)(g.ntiles / slots) * (g.niter * stage_us(edge, slots, f32) + enter);
+  double us = (double)(g.ntiles / slots) * (g.niter * stage_us(edge, slots, f32, mode) + enter);
   if (tail == 0) return us;
   double best = 1e30;
   for (int parts = 1; parts <= std::max(1, std::min(slots / tail, g.niter / (256 / step))); ++parts) {
     const int len = (g.niter + parts - 1) / parts;
-    double t = len * stage_us(edge, tail * parts, f32) + enter;
-    if (parts > 1) t += join + (double)tail * parts * edge * edge * 8.0 / 5e6;
+    double t = len * stage_us(edge, tail * parts, f32, mode) + enter;
+    if (parts > 1) t += join + (double)tail * parts * edge * edge * 8.0 / 12e6;
     if (t >= best) continue;
     best = t;
     if (parts > 1) {
