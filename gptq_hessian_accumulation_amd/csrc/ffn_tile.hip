@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) f
   const int it0 = __builtin_amdgcn_readfirstlane(whole ? 0 : part * P.part_len);
   const int it1 = __builtin_amdgcn_readfirstlane(whole ? P.niter : min(P.niter, it0 + P.part_len));
   int I, J;
-  tile_coords(P, t, I, J);
+  tile_coords<Mode>(P, t, I, J);
   const int64_t i0 = (int64_t)I * Edge;
   const int64_t j0 = (int64_t)J * (Mode == kFfnFwd ? Edge / 2 : Edge);
   const int per_seg = Mode == kFfnDx ? P.niter / 2 : P.niter;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) f
 template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn_join(FfnGemm P) {
   const int tail = P.ntiles - P.full, t = blockIdx.x;
   int I, J;
-  tile_coords(P, P.full + t, I, J);
+  tile_coords<Mode>(P, P.full + t, I, J);
   constexpr int kQuads = Mode == kFfnFwd ? Edge / 8 : Edge / 4;  // quads of columns per row
   const int id = blockIdx.y * 256 + threadIdx.x;
   const int row = id / kQuads, quad = id % kQuads;

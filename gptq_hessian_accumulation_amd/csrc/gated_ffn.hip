@@ -131,10 +131,11 @@ double schedule_for(FfnGemm& g, int mode, int edge, bool f32) {
   double us = (double)(g.ntiles / slots) * (g.niter * stage_us(edge, slots, f32, mode) + enter);
   if (tail == 0) return us;
   double best = 1e30;
-  for (int parts = 1; parts <= std::max(1, std::min(slots / tail, g.niter / (256 / step))); ++parts) {
-    const int len = (g.niter + parts - 1) / parts;
-    double t = len * stage_us(edge, tail * parts, f32, mode) + enter;
-    if (parts > 1) t += join + (double)tail * parts * edge * edge * 8.0 / 12e6;
+  for (int parts = 1; parts <= std::max(1, std::min(2 * slots / tail, g.niter / (256 / step))); ++parts) {
+    const int len = (g.niter + parts - 1) / parts, work = tail * parts;
+    double t = work / slots * (len * stage_us(edge, slots, f32, mode) + enter);
+    if (work % slots > 0) t += len * stage_us(edge, work % slots, f32, mode) + enter;
+    if (parts > 1) t += join + (double)work * edge * edge * 8.0 / 12e6;
     if (t >= best) continue;
     best = t;
     if (parts > 1) {
