@@ -126,6 +126,22 @@ __device__ __forceinline__ void put(const FfnGemm& P, int64_t r, int64_t c, cons
   }
 }
 
+// The pre-activations of row r, features c .. c + N - 1.
+template <class T, int N>
+__device__ __forceinline__ void put_preact(const FfnGemm& P, int64_t r, int64_t c, const float (&g)[N],
+                                           const float (&u)[N]) {
+  const int64_t at = r * 2 * P.fp + c;
+  if (sizeof(T) == 4 || P.pre32) {
+    float* q = static_cast<float*>(P.o1) + at;
+    store_n(q, g, N);
+    store_n(q + P.fp, u, N);
+  } else {
+    T* q = static_cast<T*>(P.o1) + at;
+    store_n(q, g, N);
+    store_n(q + P.fp, u, N);
+  }
+}
+
 // Outputs of row r, features c .. c + N - 1 of the forward pass.
 template <int DT, int N>
 __device__ __forceinline__ void put_fwd(const FfnGemm& P, int64_t r, int64_t c, const float (&g)[N],
@@ -136,12 +152,8 @@ __device__ __forceinline__ void put_fwd(const FfnGemm& P, int64_t r, int64_t c, 
 #pragma unroll
   for (int j = 0; j < N; ++j) h[j] = act_value<DT == kInF32>(g[j], P.act) * u[j];
   if (c < P.N) store_n(static_cast<T*>(P.o0) + r * P.ldo0 + c, h, (int)min((int64_t)N, P.N - c));
-  if (P.o1) {
-    // columns f .. fp - 1 are the zeros their absent weight rows gave
-    T* q = static_cast<T*>(P.o1) + r * 2 * P.fp + c;
-    store_n(q, g, N);
-    store_n(q + P.fp, u, N);
-  }
+  // columns f .. fp - 1 are the zeros their absent weight rows gave
+  if (P.o1) put_preact<T>(P, r, c, g, u);
 }
 
 // Tile t of the blocked order: groups of 8 (dW: 4) tile rows, column by column

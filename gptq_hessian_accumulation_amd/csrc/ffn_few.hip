@@ -5,7 +5,11 @@
 // of one weight row straight into the matrix instruction's operand (no LDS,
 // any alignment; 64 consecutive bytes a row and instruction), x comes from L2
 // the same way, and the waves' sums meet in LDS before the activation.  One
-// launch, no workspace, every weight byte read once.
+// launch, no workspace, every weight byte read once.  One bf16 token at 4096 x
+// 11264: 32.5 us, 5.7 TB/s (a large read reaches 5.6; the last-level cache
+// holds some of the weights); 24 fp16 tokens at 2560 x 9728: 31 us, 3.2 TB/s,
+// where x, read again for every 32 features, costs about as much as a third of
+// the weights.
 //
 // Rows of x past n and features past f read the last row instead; their sums
 // are not stored.

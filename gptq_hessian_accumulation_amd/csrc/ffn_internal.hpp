@@ -31,6 +31,7 @@ struct FfnGemm {
   int64_t M, N, K;
   int64_t f, fp;
   int act;
+  int pre32;       // fwd: o1 is float32 whatever the type
   // schedule: tiles 0 .. full - 1 of the blocked order are done whole; each of
   // the others is cut into `parts` ranges of part_len K-iterations, whose
   // partial sums go to workspace slot part * (ntiles - full) + (tile - full)
@@ -60,8 +61,8 @@ struct PackRows {
 hipError_t launch_pack_rows16(const PackRows& p, hipStream_t stream);
 
 // dg = dh u act'(g), du = dh act(g) into the n x 2 fp pair dgu (columns past f zero).
-hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f,
-                          int64_t fp, int act, int dtype, hipStream_t stream);
+hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, bool pre32, void* dgu, int64_t n,
+                          int64_t f, int64_t fp, int act, int dtype, hipStream_t stream);
 
 // Zeros rows x cols elements of esize bytes at p (row stride ld elements).
 hipError_t launch_zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int esize, hipStream_t stream);

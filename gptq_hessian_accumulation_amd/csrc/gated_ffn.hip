@@ -22,29 +22,28 @@ namespace hess {
 
 namespace {
 
-// dg, du from dh and the saved pair, 8 columns a thread; dh's rows may start
-// anywhere.  Bound by its 5 n f elements (bf16, 8192 x 11264: 175 us, 5.3
-// TB/s).
+// dg, du from dh and the saved pair (of PT), 8 columns a thread; dh's rows may
+// start anywhere.  Bound by its bytes (bf16, 8192 x 11264, the pair in bf16:
+// 175 us, 5.3 TB/s).
 //
-// Roundings: g, u were rounded to the operands' type when the forward pass
-// saved them, and dg, du are rounded to it here, because the two products that
-// follow take matrix instructions of that type.  Together they put a relative
-// error of about one and a half steps of the final rounding (bf16 0.0026 root
-// mean square) into the gradients, spread evenly.  Avoiding it would take the
-// pair in float32 (twice the memory a training step keeps) and a second 16-bit
-// term of dg and du (twice the matrix work of the backward pass).
-template <int DT>
-__global__ void __launch_bounds__(256) ffn_dgu(const typename Elem<DT>::type* dh, int64_t lddh,
-                                               const typename Elem<DT>::type* pre, typename Elem<DT>::type* out,
-                                               int64_t f, int64_t fp, int act) {
+// Roundings: dg and du are rounded to the operands' type here, because the two
+// products that follow take matrix instructions of that type; with the
+// gradients' own last rounding that is an error of 1.4 times the last
+// rounding alone (1.8 times where the pair was kept in a 16-bit type too).
+// Without it the products would need a second 16-bit term of dg and du, twice
+// the matrix work of the backward pass.
+template <int DT, class PT>
+__global__ void __launch_bounds__(256) ffn_dgu(const typename Elem<DT>::type* dh, int64_t lddh, const PT* pre,
+                                               typename Elem<DT>::type* out, int64_t f, int64_t fp, int act) {
   typedef typename Elem<DT>::type T;
   typedef T T8 __attribute__((ext_vector_type(8)));
   typedef T8 T8u __attribute__((aligned(sizeof(T))));
+  typedef PT P8 __attribute__((ext_vector_type(8)));
   const int64_t row = blockIdx.y;
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (c >= fp) return;
-  const T* q = pre + row * 2 * fp + c;
-  const T8 g8 = *reinterpret_cast<const T8*>(q), u8 = *reinterpret_cast<const T8*>(q + fp);
+  const PT* q = pre + row * 2 * fp + c;
+  const P8 g8 = *reinterpret_cast<const P8*>(q), u8 = *reinterpret_cast<const P8*>(q + fp);
   T8 h8;
   const T* hp = dh + row * lddh + c;
   if (c + 8 <= f) {
@@ -72,18 +71,17 @@ template <class T> __global__ void __launch_bounds__(256) zero_rows(T* p, int64_
     p[i / cols * ld + i % cols] = T(0);
 }
 
-template <int DT>
-hipError_t dgu_dtype(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f, int64_t fp,
-                     int act, hipStream_t stream) {
+template <int DT, class PT>
+hipError_t launch_dgu(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f, int64_t fp,
+                      int act, hipStream_t stream) {
   typedef typename Elem<DT>::type T;
   const unsigned gx = (unsigned)((fp / 8 + 255) / 256);
   // a grid has at most 65,535 rows
   for (int64_t r0 = 0; r0 < n; r0 += 65535) {
     const unsigned rows = (unsigned)std::min<int64_t>(65535, n - r0);
-    const T* d = static_cast<const T*>(dh) + r0 * lddh;
-    const T* p = static_cast<const T*>(preact) + r0 * 2 * fp;
-    T* o = static_cast<T*>(dgu) + r0 * 2 * fp;
-    ffn_dgu<DT><<<dim3(gx, rows), 256, 0, stream>>>(d, lddh, p, o, f, fp, act);
+    ffn_dgu<DT, PT><<<dim3(gx, rows), 256, 0, stream>>>(static_cast<const T*>(dh) + r0 * lddh, lddh,
+                                                        static_cast<const PT*>(preact) + r0 * 2 * fp,
+                                                        static_cast<T*>(dgu) + r0 * 2 * fp, f, fp, act);
   }
   return hipGetLastError();
 }
@@ -165,11 +163,14 @@ int ffn_schedule(FfnGemm& g, int mode, int dtype) {
   return edge;
 }
 
-hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f,
-                          int64_t fp, int act, int dtype, hipStream_t stream) {
-  if (dtype == kInBF16) return dgu_dtype<kInBF16>(dh, lddh, preact, dgu, n, f, fp, act, stream);
-  if (dtype == kInF16) return dgu_dtype<kInF16>(dh, lddh, preact, dgu, n, f, fp, act, stream);
-  return dgu_dtype<kInF32>(dh, lddh, preact, dgu, n, f, fp, act, stream);
+hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, bool pre32, void* dgu, int64_t n,
+                          int64_t f, int64_t fp, int act, int dtype, hipStream_t stream) {
+  if (dtype == kInF32) return launch_dgu<kInF32, float>(dh, lddh, preact, dgu, n, f, fp, act, stream);
+  if (dtype == kInBF16)
+    return pre32 ? launch_dgu<kInBF16, float>(dh, lddh, preact, dgu, n, f, fp, act, stream)
+                 : launch_dgu<kInBF16, __bf16>(dh, lddh, preact, dgu, n, f, fp, act, stream);
+  return pre32 ? launch_dgu<kInF16, float>(dh, lddh, preact, dgu, n, f, fp, act, stream)
+               : launch_dgu<kInF16, _Float16>(dh, lddh, preact, dgu, n, f, fp, act, stream);
 }
 
 hipError_t launch_zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int esize, hipStream_t stream) {

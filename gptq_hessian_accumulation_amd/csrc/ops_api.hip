@@ -32,7 +32,8 @@ struct Mat {
   const char* name;
   const void* p;
   int64_t ld, rows, cols;
-  int64_t bytes(int64_t es) const { return rows > 0 ? ((rows - 1) * ld + cols) * es : 0; }
+  int64_t own = 0;  // bytes of an element, where it is not the call's type
+  int64_t bytes(int64_t es) const { return rows > 0 ? ((rows - 1) * ld + cols) * (own ? own : es) : 0; }
 };
 
 int check_mat(const Mat& m, int64_t es) {
@@ -176,11 +177,13 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
                            int dtype, int act, int64_t n, int64_t d, int64_t f, void* h, int64_t ldh, void* preact,
                            void* work, int64_t work_bytes, hess_stream_t stream) {
   if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
+  const bool pre32 = act >= 0 && (act & HESS_PREACT_F32);
+  if (pre32) act &= ~HESS_PREACT_F32;
   if (act < HESS_SILU || act > HESS_GELU_TANH) return fail(HESS_EINVAL, "unknown activation %d", act);
   if (n == 0) return HESS_OK;
   const int64_t es = elem_bytes(dtype), fp = up(f, 8);
   const Mat ins[3] = {{"x", x, ldx, n, d}, {"w_gate", w_gate, ldg, f, d}, {"w_up", w_up, ldu, f, d}};
-  const Mat outs[2] = {{"h", h, ldh, n, f}, {"preact", preact, 2 * fp, n, 2 * fp}};
+  const Mat outs[2] = {{"h", h, ldh, n, f}, {"preact", preact, 2 * fp, n, 2 * fp, pre32 ? 4 : 0}};
   for (const Mat& m : ins)
     if (int rc = check_mat(m, es)) return rc;
   if (int rc = check_mat(outs[0], es)) return rc;
@@ -210,6 +213,7 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
   g.f = f;
   g.fp = fp;
   g.act = act;
+  g.pre32 = pre32;
   hipError_t e;
   if (few) {
     e = launch_ffn_few(g, dtype, s);
@@ -225,6 +229,8 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
                             int64_t d, int64_t f, void* dx, int64_t lddx, void* dw_gate, int64_t lddg, void* dw_up,
                             int64_t lddu, void* work, int64_t work_bytes, hess_stream_t stream) {
   if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
+  const bool pre32 = act >= 0 && (act & HESS_PREACT_F32);
+  if (pre32) act &= ~HESS_PREACT_F32;
   if (act < HESS_SILU || act > HESS_GELU_TANH) return fail(HESS_EINVAL, "unknown activation %d", act);
   if (!dw_gate != !dw_up) return fail(HESS_EINVAL, "dw_gate and dw_up: both or neither");
   const int64_t es = elem_bytes(dtype), fp = up(f, 8);
@@ -233,7 +239,7 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
                       {"x", x, ldx, n, d},
                       {"w_gate", w_gate, ldg, f, d},
                       {"w_up", w_up, ldu, f, d},
-                      {"preact", preact, 2 * fp, n, 2 * fp}};
+                      {"preact", preact, 2 * fp, n, 2 * fp, pre32 ? 4 : 0}};
   const Mat outs[3] = {{"dx", dx, lddx, n, d}, {"dw_gate", dw_gate, lddg, f, d}, {"dw_up", dw_up, lddu, f, d}};
   for (const Mat& m : ins) {
     if (n == 0 && m.rows == 0) continue;
@@ -260,7 +266,7 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
   float* slots = reinterpret_cast<float*>(dgu + room.slots);
   FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
   if (int rc = place_operands(o, dgu + room.pack, n, f, dtype, dw_gate != nullptr, dx != nullptr, s)) return rc;
-  e = launch_ffn_dgu(dh, lddh, preact, dgu, n, f, fp, act, dtype, s);
+  e = launch_ffn_dgu(dh, lddh, preact, pre32, dgu, n, f, fp, act, dtype, s);
   if (e != hipSuccess) return hip_fail(e, "gate gradient launch");
   if (dx) {
     FfnGemm g = shape(n, d, f);

@@ -147,3 +147,12 @@ def test_ffn_refuses_rows_off_16_bytes():
     # rows that are copied need room for x and both weights
     room = hs._load().hess_gated_ffn_workspace(100, 25, 40, 0, 0) - hs._load().hess_gated_ffn_workspace(100, 32, 40, 0, 0)
     assert room >= 2 * 32 * (100 + 2 * 40)
+
+
+def test_ffn_float32_pair_flag():
+    """HESS_PREACT_F32 (16) doubles what the pair spans; activations past it stay unknown."""
+    assert _forward(act=16 + 3) == EINVAL and b"activation" in _message()
+    assert _forward(act=32) == EINVAL and b"activation" in _message()
+    # bf16 pair of 5 rows of 80: 800 bytes; h right behind it meets the float32 one
+    ptrs = [_ptr(0), _ptr(1), _ptr(2), _ptr(4, 800)]
+    assert _forward(act=16, ptrs=ptrs) == EINVAL and b"h overlaps preact" in _message()

@@ -168,3 +168,38 @@ def test_logits_past_32_bit_offsets():
     D.compare(grad[rows], g, tg, "gradient")
     hs.distill_topk_backward(torch.ones(n, device="cuda"), z, i, v, stats, out=grad)
     D.compare(grad[rows], g, tg, "backward's gradient")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n,d,f", [(20, 72, 65), (300, 200, 520), (2100, 96, 1160)])
+def test_preactivations_kept_in_float32(n, d, f, dt):
+    """The forward pass's float32 pair, and the backward pass at such a pair."""
+    act = R.ACTS[n % 3]
+    G.say(f"float32 pair {dt} {n}x{d}x{f} {act}")
+    x, xn = G.draw(81, dt, n, d)
+    wg, gn = G.draw(82, dt, f, d, scale=1.5 / d ** 0.5)
+    wu, un = G.draw(83, dt, f, d, scale=1.5 / d ** 0.5)
+    dh, dn = G.draw(84, dt, n, f)
+    h, pre = hs.gated_ffn_forward(x, wg, wu, act=act, save=True)
+    h16, pre16 = hs.gated_ffn_forward(x, wg, wu, act=act, save=G.TYPES[dt])
+    assert pre.dtype == torch.float32 and pre16.dtype == G.TYPES[dt]
+    assert torch.equal(h, h16) and torch.equal(pre.to(G.TYPES[dt]), pre16)
+    _, g, u = R.gated_ffn(xn, gn, un, act)
+    fp = -(-f // 8) * 8
+    k = (d + 8) * G.U
+    G.check("g", pre[:, :f], g, k * (np.abs(xn) @ np.abs(gn).T))
+    G.check("u", pre[:, fp:fp + f], u, k * (np.abs(xn) @ np.abs(un).T))
+    pair = torch.zeros((n, 2 * fp), dtype=torch.float32)
+    pair[:, :f], pair[:, fp:fp + f] = torch.from_numpy(g), torch.from_numpy(u)
+    g, u = pair[:, :f].double().numpy(), pair[:, fp:fp + f].double().numpy()
+    grads = hs.gated_ffn_backward(dh, x, wg, wu, pair.cuda(), act=act)
+    torch.cuda.synchronize()
+    *want, dg, du = R.gated_ffn_grads(dn, xn, gn, un, g, u, act)
+    tol = G.backward_tolerance(dn, xn, gn, un, dg, du, g, act, dt)
+    for name, got, w, t in zip(("dx", "dw_gate", "dw_up"), grads, want, tol):
+        G.check(name, got, w, t * (1 + G.half(dt)) + G.half(dt) * np.abs(w) + G.FLOOR[dt])
+    other = torch.float16 if dt == "bf16" else torch.bfloat16
+    with pytest.raises(ValueError):
+        hs.gated_ffn_forward(x, wg, wu, save=other)
+    with pytest.raises(ValueError):
+        hs.gated_ffn_backward(dh, x, wg, wu, pre.to(other))
