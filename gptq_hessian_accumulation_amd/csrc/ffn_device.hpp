@@ -71,7 +71,8 @@ template <bool Exact> __device__ __forceinline__ void act_both(float g, int act,
   } else {
     const float s = sigmoidf<Exact>(1.5957691216057308f * (g + 0.044715f * g * g * g));
     a = g * s;
-    da = s + g * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
+    // (the cap keeps 0 times infinity out of the far ends)
+    da = s + g * s * (1.0f - s) * 1.5957691216057308f * fminf(1.0f + 0.134145f * g * g, 1e30f);
   }
 }
 

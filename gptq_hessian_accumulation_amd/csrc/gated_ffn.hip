@@ -24,7 +24,7 @@ namespace {
 
 // dg, du from dh and the saved pair (of PT), 8 columns a thread; dh's rows may
 // start anywhere.  Bound by its bytes (bf16, 8192 x 11264: 175 us with the pair
-// in bf16, 5.3 TB/s, and 245 us with it in float32).
+// in bf16, 5.3 TB/s, and 250 us with it in float32).
 //
 // Roundings: dg and du are rounded to the operands' type here, because the two
 // products that follow take matrix instructions of that type; with the

@@ -203,3 +203,17 @@ def test_preactivations_kept_in_float32(n, d, f, dt):
         hs.gated_ffn_forward(x, wg, wu, save=other)
     with pytest.raises(ValueError):
         hs.gated_ffn_backward(dh, x, wg, wu, pre.to(other))
+
+
+def test_slopes_far_out():
+    """gelu_tanh's and silu's derivatives where their polynomial overflows: 1 far right, 0 far left."""
+    G.say("slopes far out")
+    g = torch.tensor([3e19, -3e19, 1e30, -1e30], device="cuda")
+    one = torch.ones((1, 1), device="cuda")
+    for act in ("gelu_tanh", "silu", "gelu"):
+        pre = torch.zeros((4, 16), device="cuda")
+        pre[:, 0], pre[:, 8] = g, 1.0
+        # dx = dg + du with dh = 2^-100: dg = dh act'(g), du = dh act(g); only dg through w_up = 0
+        dx = hs.gated_ffn_backward(torch.full((4, 1), 2.0 ** -100, device="cuda"), g[:, None], one, 0 * one, pre,
+                                   act=act, need_w=False)[0][:, 0]
+        assert torch.equal(dx, torch.tensor([2.0 ** -100, 0.0, 2.0 ** -100, 0.0], device="cuda")), (act, dx)
