@@ -164,6 +164,7 @@ def exported_symbols() -> list:
 # The current stream's raw handle without building a Stream object (about 2.5 us
 # per call saved, which matters at one call per short calibration batch).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None, device=None) -> int:
@@ -556,7 +557,8 @@ _CODES = {torch.bfloat16: HESS_BF16, torch.float32: HESS_F32, torch.float16: HES
 
 
 def _on_stream(fn):
-    """Adds ``stream``: the call, its temporaries and its outputs belong to that stream instead of the current one."""
+    """Gives ``stream`` its meaning: the call, its temporaries and its outputs belong to that stream instead of
+    the current one.  The function itself sees ``stream=None``."""
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
@@ -572,7 +574,7 @@ def _float_code(name: str, t: torch.Tensor) -> int:
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be on the GPU")
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     code = _CODES.get(t.dtype)
     if code is None:
@@ -582,18 +584,16 @@ def _float_code(name: str, t: torch.Tensor) -> int:
 
 def _rows(t: torch.Tensor, step: int = 1):
     """(tensor, pointer, row stride) of a 2-D tensor whose rows are contiguous, do not overlap and start at
-    multiples of ``step`` elements (copied if need be)."""
-    n, c = t.shape
+    multiples of ``step`` elements: 1, or 16 bytes' worth for rows of a multiple of that (copied if need be)."""
     ptr = t.data_ptr()
-    if not t.is_contiguous() or (step > 1 and ptr % (step * t.element_size()) != 0):
-        s0, s1 = t.stride()
-        if ((s1 != 1 and c > 1) or (n > 1 and (s0 < c or s0 % step != 0))
-                or (step > 1 and ptr % (step * t.element_size()) != 0)):
-            t = t.clone(memory_format=torch.contiguous_format)
-            ptr = t.data_ptr()
-        elif n > 1:
-            return t, ptr, s0
-    return t, ptr, c or 1
+    if t.is_contiguous() and (step == 1 or ptr % 16 == 0):
+        return t, ptr, t.shape[1] or 1
+    n, c = t.shape
+    s0, s1 = t.stride()
+    if (s1 != 1 and c > 1) or (n > 1 and (s0 < c or s0 % step != 0)) or (step > 1 and ptr % 16 != 0):
+        t = t.clone(memory_format=torch.contiguous_format)
+        return t, t.data_ptr(), c or 1
+    return t, ptr, (s0 if n > 1 else c or 1)
 
 
 def _out(name: str, out, shape, like: torch.Tensor) -> torch.Tensor:
@@ -636,16 +636,19 @@ def _ffn_args(x, w_gate, w_up):
     if len(shape) != 2 or shape != w_up.shape:
         raise ValueError("w_gate and w_up must be (f, d) matrices of one shape")
     f, d = shape
-    if x.dim() < 1 or x.shape[-1] != d:
-        raise ValueError(f"last dimension of x {tuple(x.shape)} != d = {d}")
+    given = x.shape
+    if len(given) < 1 or given[-1] != d:
+        raise ValueError(f"last dimension of x {tuple(given)} != d = {d}")
     dtype, index = x.dtype, x.get_device()
-    for name, t in (("w_gate", w_gate), ("w_up", w_up)):
-        if t.dtype != dtype or t.get_device() != index:
-            raise ValueError(f"{name} must have x's dtype and device")
+    if w_gate.dtype != dtype or w_gate.get_device() != index:
+        raise ValueError("w_gate must have x's dtype and device")
+    if w_up.dtype != dtype or w_up.get_device() != index:
+        raise ValueError("w_up must have x's dtype and device")
     # the tiles read rows of a multiple of 16 bytes where they are, if they start at 16 bytes
     step = 4 if code == HESS_F32 else 8
-    step = step if d % step == 0 else 1
-    x2, xp, ldx = _rows(x.reshape(-1, d) if x.dim() != 2 else x, step)
+    if d % step != 0:
+        step = 1
+    x2, xp, ldx = _rows(x if len(given) == 2 else x.reshape(-1, d), step)
     wg, gp, ldg = _rows(w_gate, step)
     wu, up, ldu = _rows(w_up, step)
     return code, x2.shape[0], d, f, (x2, wg, wu), (xp, ldx, gp, ldg, up, ldu)
@@ -676,7 +679,8 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
             mode |= _PREACT_F32
     if n > 0:
         ldh = h.stride(0) if out is not None and h.dim() == 2 and n > 1 else f
-        wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 0), x)
+        need = lib.hess_gated_ffn_workspace(n, d, f, code, 0)
+        wp, wb, work = _workspace(workspace, need, x) if need else (None, 0, None)
         rc = lib.hess_gated_ffn_forward(*ins, code, mode, n, d, f, h.data_ptr(), ldh,
                                         pre.data_ptr() if save else None, wp, wb, _stream(None, x.get_device()))
         if rc != 0:
@@ -761,27 +765,29 @@ def _distill_args(logits, ids, values, weight, temperature):
         ids64 = 0
     else:
         raise TypeError("ids must be int32 or int64")
-    vcode = _float_code("values", values)
-    if ids.get_device() != logits.get_device():
+    index = logits.get_device()
+    vcode = _CODES.get(values.dtype)
+    if vcode is None or values.get_device() != index:
+        vcode = _float_code("values", values)
+    if ids.get_device() != index:
         raise ValueError("ids must be on the device of logits")
     k = short[-1]
-    flat = len(shape) == 2
-    z2, zp, ldz = _rows(logits if flat else logits.reshape(-1, vocab))
-    i2, ip, ldi = _rows(ids if flat else ids.reshape(-1, k))
-    v2, vp, ldv = _rows(values if flat else values.reshape(-1, k))
+    if len(shape) != 2:
+        logits, ids, values = logits.reshape(-1, vocab), ids.reshape(-1, k), values.reshape(-1, k)
+    z2, zp, ldz = _rows(logits)
+    i2, ip, ldi = _rows(ids)
+    v2, vp, ldv = _rows(values)
     n = z2.shape[0]
-    w = _row_floats("weight", weight, lead, logits)
+    w = _row_floats("weight", weight, lead, logits) if weight is not None else None
     return (z2, i2, v2, w), lead, n, vocab, code, (zp, ldz, code, n, vocab, ip, ids64, ldi, vp, vcode, ldv, k,
                                                    w.data_ptr() if w is not None else None, float(temperature))
 
 
 def _row_floats(name, t, lead, like):
     """A float32 value for each row, contiguous (a broadcast one is written out)."""
-    if t is None:
-        return None
     if t.shape != lead or t.dtype != torch.float32 or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be a float32 {tuple(lead)} tensor on {like.device}")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _grad_out(out, logits):
@@ -799,7 +805,8 @@ def _distill_call(logits, ids, values, weight, temperature, want_stats, want_gra
     loss = torch.empty_like(w) if w is not None else logits.new_empty(lead, dtype=torch.float32)
     stats = logits.new_empty((*lead, 2), dtype=torch.float32) if want_stats else None
     grad, ldg = _grad_out(out, logits) if want_grad else (None, 0)
-    wp, wb, work = _workspace(workspace, lib.hess_distill_topk_workspace(n, vocab, code), logits)
+    need = lib.hess_distill_topk_workspace(n, vocab, code)
+    wp, wb, work = _workspace(workspace, need, logits) if need else (None, 0, None)
     rc = lib.hess_distill_topk(*args, loss.data_ptr(), stats.data_ptr() if want_stats else None,
                                grad.data_ptr() if want_grad else None, ldg, wp, wb,
                                _stream(None, logits.get_device()))
