@@ -19,7 +19,6 @@ There is no CPU fallback: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import re
 
@@ -556,20 +555,6 @@ _PREACT_F32 = 16
 _CODES = {torch.bfloat16: HESS_BF16, torch.float32: HESS_F32, torch.float16: HESS_F16}
 
 
-def _on_stream(fn):
-    """Gives ``stream`` its meaning: the call, its temporaries and its outputs belong to that stream instead of
-    the current one.  The function itself sees ``stream=None``."""
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-
-    return call
-
-
 def _float_code(name: str, t: torch.Tensor) -> int:
     index = t.get_device()
     if index < 0:
@@ -654,9 +639,9 @@ def _ffn_args(x, w_gate, w_up):
     return code, x2.shape[0], d, f, (x2, wg, wu), (xp, ldx, gp, ldg, up, ldu)
 
 
-@_on_stream
 def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu",
-                      save: bool | torch.dtype = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+                      save: bool | torch.dtype = False, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
     """``h = act(x w_gate^T) * (x w_up^T)`` for x (..., d) and weights (f, d); not recorded by autograd.
 
     bfloat16, float16 or float32 throughout; ``act`` is ``"silu"``, ``"gelu"`` or ``"gelu_tanh"``.
@@ -665,6 +650,9 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     (``save=True``) or in the dtype given: float32 or x's, which takes half the memory and leaves
     16-bit gradients about 1.3 times as far off.
     """
+    if stream is not None:  # the call, its temporaries and its outputs belong to it
+        with torch.cuda.stream(stream):
+            return gated_ffn_forward(x, w_gate, w_up, act, save, out, workspace)
     lib = _load()
     mode = _act_mode(act)
     code, n, d, f, keep, ins = _ffn_args(x, w_gate, w_up)
@@ -688,11 +676,13 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     return (h, pre) if save else h
 
 
-@_on_stream
 def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
                        preact: torch.Tensor, act: str = "silu", need_x: bool = True, need_w: bool = True,
-                       workspace: torch.Tensor | None = None):
+                       workspace: torch.Tensor | None = None, stream=None):
     """``(dx, dw_gate, dw_up)`` for the gradient dh of gated_ffn_forward's h (entries not needed are None)."""
+    if stream is not None:  # the call, its temporaries and its outputs belong to it
+        with torch.cuda.stream(stream):
+            return gated_ffn_backward(dh, x, w_gate, w_up, preact, act, need_x, need_w, workspace)
     lib = _load()
     mode = _act_mode(act)
     code, n, d, f, keep, (xp, ldx, gp, ldg, up, ldu) = _ffn_args(x, w_gate, w_up)
@@ -815,33 +805,39 @@ def _distill_call(logits, ids, values, weight, temperature, want_stats, want_gra
     return loss, stats, grad
 
 
-@_on_stream
 def distill_topk_forward(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
                          weight: torch.Tensor | None = None, temperature: float = 1.0,
-                         workspace: torch.Tensor | None = None):
+                         workspace: torch.Tensor | None = None, stream=None):
     """``(loss, stats)``: each row's divergence from the teacher's top entries, and what the backward pass needs.
 
     logits (..., vocab) bfloat16, float16 or float32; ids (..., k) int32 or int64 (negative: absent);
     values (..., k) the teacher's logits there; weight (...) float32, 0 for rows to leave out.  loss (...)
     and stats (..., 2), the largest logit and the sum of exp((logits - largest) / temperature), are float32.
     """
+    if stream is not None:  # the call, its temporaries and its outputs belong to it
+        with torch.cuda.stream(stream):
+            return distill_topk_forward(logits, ids, values, weight, temperature, workspace)
     return _distill_call(logits, ids, values, weight, temperature, True, False, None, workspace)[:2]
 
 
-@_on_stream
 def distill_topk_step(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
                       weight: torch.Tensor | None = None, temperature: float = 1.0, out: torch.Tensor | None = None,
-                      workspace: torch.Tensor | None = None):
+                      workspace: torch.Tensor | None = None, stream=None):
     """``(loss, dlogits)`` in one call: each row's loss and the gradient of their sum (``out`` may be logits)."""
+    if stream is not None:  # the call, its temporaries and its outputs belong to it
+        with torch.cuda.stream(stream):
+            return distill_topk_step(logits, ids, values, weight, temperature, out, workspace)
     loss, _, grad = _distill_call(logits, ids, values, weight, temperature, False, True, out, workspace)
     return loss, grad
 
 
-@_on_stream
 def distill_topk_backward(dloss: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
                           stats: torch.Tensor, weight: torch.Tensor | None = None, temperature: float = 1.0,
-                          out: torch.Tensor | None = None) -> torch.Tensor:
+                          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dlogits for the gradient dloss of distill_topk_forward's loss (``out`` may be logits)."""
+    if stream is not None:  # the call, its temporaries and its outputs belong to it
+        with torch.cuda.stream(stream):
+            return distill_topk_backward(dloss, logits, ids, values, stats, weight, temperature, out)
     lib = _load()
     keep, lead, n, vocab, code, args = _distill_args(logits, ids, values, weight, temperature)
     dl = _row_floats("dloss", dloss, lead, logits)
