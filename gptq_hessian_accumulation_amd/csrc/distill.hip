@@ -101,7 +101,9 @@ template <int DT> struct Vec {
 };
 
 // A thread's teacher entries i = tid + q Threads of one row.  id -1: absent,
-// as is an entry of value -infinity (p = 0) or past the vocabulary (bad).
+// as is an entry of value -infinity (p = 0).  An id past the vocabulary (bad)
+// takes no part either, but makes the row NaN whatever its value and whatever
+// stands beside it: only a row with neither kind is one without entries.
 template <int Threads> struct Entries {
   static constexpr int kPer = kTop / Threads;
   int id[kPer];
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(Threads, 4) distill_resident(DistillParams P) 
     for (int q = 0; q < kWaves; ++q) all |= J.flags[q];
     all = __builtin_amdgcn_readfirstlane(all);
   }
-  if (!(all & 1)) {
+  if (all == 0) {
     const float g[V::N] = {};
 #pragma unroll 1
     for (int j = tid; j < nvec; j += Threads) V::store_whole(dz + j * V::N, g);
@@ -486,7 +488,7 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < kWaves; ++q) all |= J.flags[q];
-    zero = !(all & 1);
+    zero = all == 0;
   }
   if (zero) {
     if (tid == 0) P.loss[row] = 0.0f;
@@ -557,7 +559,7 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
     int all = 0;
 #pragma unroll
     for (int q = 0; q < kWaves; ++q) all |= J.flags[q];
-    zero = !(all & 1);
+    zero = all == 0;
     c = (all & 2) ? NAN : (P.dloss ? P.dloss[row] : 1.0f) * w / P.temperature;
     if (!zero && E.mine(P.k)) {
       double logps;

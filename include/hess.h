@@ -630,14 +630,15 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
  *             ldz; any element alignment.
  *   ids       n x k, row stride ldi; int32, or int64 with ids64 nonzero.  A
  *             negative id marks an absent entry (lists shorter than k); an id
- *             >= vocab makes the row's loss and gradient NaN.  Repeated ids
- *             add their probabilities.
+ *             >= vocab makes the row's loss and gradient NaN, whatever its
+ *             value and whether or not the row has other entries.  Repeated
+ *             ids add their probabilities.
  *   values    n x k teacher logits (or log-probabilities) of values_dtype,
  *             row stride ldv; not read where the entry is absent.  A value
  *             of -infinity makes the entry absent too.
- *   weight    n floats, or NULL for ones.  A row of weight 0, or without a
- *             present entry, has loss 0 and a zero gradient whatever its
- *             logits hold (they are not read).
+ *   weight    n floats, or NULL for ones.  A row of weight 0, or one whose
+ *             entries are all absent, has loss 0 and a zero gradient whatever
+ *             its logits hold.
  *   T         temperature, > 0 and finite.  The loss is not multiplied by T^2.
  * Limits: 0 <= n <= 2^24, 1 <= vocab <= 2^28, 1 <= k <= 1024.  Exponentials
  * and sums are float32, the k terms of the loss float64.

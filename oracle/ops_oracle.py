@@ -51,16 +51,19 @@ def distill_topk(logits, ids, values, weight, temperature):
     """(loss, stats, grad): each row's weighted divergence, (max, sum exp(. - max)) of logits / T, its gradient.
 
     Entries with a negative id or a value of -infinity are absent; a row of weight 0 or without a
-    present entry has loss 0, a zero gradient and zero statistics; an id past the vocabulary gives NaN.
+    present entry has loss 0, a zero gradient and zero statistics; an id past the vocabulary gives NaN,
+    whatever its value.
     """
     n, vocab = logits.shape
     loss, stats, grad = np.zeros(n), np.zeros((n, 2)), np.zeros((n, vocab))
     for r in range(n):
         here = (ids[r] >= 0) & ~(values[r] == -np.inf)
-        if weight[r] == 0.0 or not here.any():
+        if weight[r] == 0.0:
             continue
         if (ids[r] >= vocab).any():
             loss[r], stats[r], grad[r] = np.nan, np.nan, np.nan
+            continue
+        if not here.any():
             continue
         with np.errstate(all="ignore"):
             z = logits[r] / temperature

@@ -104,3 +104,11 @@ def test_every_logit_the_lowest_value():
     z = np.full((1, 8), np.finfo(np.float32).min, dtype=np.float64)
     loss, _, grad = R.distill_topk(z, np.array([[0, 1]]), np.array([[3.0, 3.0]]), np.ones(1), 1.0)
     assert abs(loss[0] - math.log(4.0)) < 1e-14 and np.allclose(grad[0], [-0.375] * 2 + [0.125] * 6)
+
+
+def test_rows_of_ids_past_the_vocabulary_only():
+    ids = np.array([[3, 3], [-1, 4], [5, -1], [-1, -1], [9, 9]])
+    vals = np.array([[1.0, 2.0], [1.0, 2.0], [-np.inf, 0.0], [1.0, 1.0], [0.0, 0.0]])
+    loss, _, grad = R.distill_topk(np.zeros((5, 3)), ids, vals, np.array([1.0, 1.0, 1.0, 1.0, 0.0]), 1.0)
+    assert np.isnan(loss[:3]).all() and np.isnan(grad[:3]).all()
+    assert not loss[3:].any() and not grad[3:].any()
