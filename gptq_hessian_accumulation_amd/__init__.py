@@ -23,6 +23,7 @@ import os
 import re
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 __all__ = [
     "Hessian",
@@ -709,6 +710,15 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     return dx, dwg, dwu
 
 
+def _refuse_forward_mode(name: str, *tensors) -> None:
+    """A dual tensor does not require a gradient: without this its tangent would be dropped in silence."""
+    if _forward_ad._current_level < 0:
+        return
+    for t in tensors:
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{name} has no forward-mode derivative")
+
+
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, act, save):
@@ -731,8 +741,10 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: st
               save: bool | torch.dtype = True) -> torch.Tensor:
     """gated_ffn_forward under autograd: the backward pass is gated_ffn_backward (once differentiable).
 
-    ``save``: in which type the pre-activations are kept for it, as for gated_ffn_forward.
+    ``save``: in which type the pre-activations are kept for it, as for gated_ffn_forward.  Reverse mode
+    only: dual tensors of forward mode raise NotImplementedError.
     """
+    _refuse_forward_mode("gated_ffn", x, w_gate, w_up)
     if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
         return _GatedFfn.apply(x, w_gate, w_up, act, save or True)
     return gated_ffn_forward(x, w_gate, w_up, act=act)
@@ -873,7 +885,9 @@ def distill_topk(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, 
     """Each row's loss under autograd (gradient for logits only, once differentiable).
 
     ``values`` and ``weight`` are constants of the loss: an error is raised if they require a gradient.
+    Reverse mode only: dual tensors of forward mode raise NotImplementedError.
     """
+    _refuse_forward_mode("distill_topk", logits, values, weight)
     if torch.is_grad_enabled():
         if values.requires_grad or (weight is not None and weight.requires_grad):
             raise ValueError("values and weight are constants of the loss: detach them")
