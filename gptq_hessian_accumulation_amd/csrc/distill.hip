@@ -168,13 +168,15 @@ template <int Waves> struct Joined {
   int flags[Waves], dup;
 };
 
-// The waves' shares joined, in every thread: vm, and log of the whole sum.
+// The waves' shares joined, in every thread: vm, and log of the whole sum.  A
+// share without a maximum is empty (sum 0) or holds nothing but NaN (sum NaN):
+// either sum is taken as it is.
 template <int Waves>
 __device__ __forceinline__ void teacher_join(const Joined<Waves>& J, double it, float& vm, double& logps) {
   const int l = threadIdx.x & (Waves - 1);
   const float x = J.vm[l];
   vm = wave_max<Waves>(x);
-  logps = log(wave_sum<Waves>(x == -INFINITY ? 0.0 : J.ps[l] * exp(((double)x - (double)vm) * it)));
+  logps = log(wave_sum<Waves>(x == -INFINITY ? J.ps[l] : J.ps[l] * exp(((double)x - (double)vm) * it)));
 }
 
 // A wave's share of the teacher's softmax: its largest value, and the sum of

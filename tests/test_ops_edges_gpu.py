@@ -34,3 +34,20 @@ def test_only_ids_past_the_vocabulary(dt, k, vocab):
     back = hs.distill_topk_backward(torch.ones(6, device="cuda"), z, i, v, hs.distill_topk_forward(z, i, v, weight=w)[1],
                                     weight=w)
     assert torch.isnan(back[1:4]).all() and not back[4:].any()
+
+
+@pytest.mark.parametrize("vocab", [3000, 30001, 140000])
+@pytest.mark.parametrize("dt", list(D.TYPES))
+def test_nan_among_the_teachers_values(dt, vocab):
+    """One NaN makes every teacher probability of its row NaN, wherever in the list it stands."""
+    D.say(f"NaN teacher {dt} {vocab}")
+    z, i, v, w = D.make(32, dt, 5, vocab, 200)
+    v[0, 64:128] = float("nan")     # all entries of one wave
+    v[1, 128:] = float("nan")
+    v[2, 70] = float("nan")
+    v[3] = float("nan")
+    loss, _, grad = D.run_all(z, i, v, w, 1.0, dt)
+    assert torch.isnan(loss[:4]).all() and torch.isfinite(loss[4])
+    for r in range(4):
+        assert torch.isnan(grad[r, i[r]]).all()
+        assert int(torch.isnan(grad[r]).sum()) == 200
