@@ -626,30 +626,49 @@ template <int DT, int Threads> __global__ void __launch_bounds__(Threads, 4) dis
 
 template <int DT> constexpr int64_t resident_limit() { return ((int64_t)1024 * 16 + 1) * Vec<DT>::N - 1; }
 
-template <int DT, int Threads, int NV> void launch_resident(const DistillParams& P, hipStream_t stream) {
-  distill_resident<DT, Threads, NV><<<(unsigned)P.n, Threads, 0, stream>>>(P);
+// Launches `go` on ranges of rows: `parts` workgroups of Threads each a row, and
+// fewer than 2^32 threads a grid.
+template <int DT, int Threads, class Go> void launch_rows(const DistillParams& P, int64_t parts, Go go) {
+  const int64_t most = distill_rows_per_launch(Threads, parts);
+  for (int64_t r = 0; r < P.n; r += most) {
+    const DistillParams Q = distill_rows(P, Elem<DT>::size, r, most);
+    go(Q, (unsigned)(Q.n * parts));
+  }
 }
 
+template <int DT, int Threads, int NV> void launch_resident(const DistillParams& P, hipStream_t stream) {
+  launch_rows<DT, Threads>(P, 1, [&](const DistillParams& Q, unsigned grid) {
+    distill_resident<DT, Threads, NV><<<grid, Threads, 0, stream>>>(Q);
+  });
+}
+
+template <int DT, int Threads> void launch_loss_of(const DistillParams& P, hipStream_t stream) {
+  launch_rows<DT, Threads>(P, 1, [&](const DistillParams& Q, unsigned grid) {
+    distill_loss<DT, Threads><<<grid, Threads, 0, stream>>>(Q);
+  });
+}
 template <int DT> void launch_loss(const DistillParams& P, hipStream_t stream) {
   // few rows, or long ones: more threads a row
-  if (P.n <= 512 && P.vocab > 16384) distill_loss<DT, 1024><<<(unsigned)P.n, 1024, 0, stream>>>(P);
-  else if (P.vocab > 8192) distill_loss<DT, 512><<<(unsigned)P.n, 512, 0, stream>>>(P);
-  else if (P.vocab > 2048) distill_loss<DT, 256><<<(unsigned)P.n, 256, 0, stream>>>(P);
-  else distill_loss<DT, 128><<<(unsigned)P.n, 128, 0, stream>>>(P);
+  if (P.n <= 512 && P.vocab > 16384) launch_loss_of<DT, 1024>(P, stream);
+  else if (P.vocab > 8192) launch_loss_of<DT, 512>(P, stream);
+  else if (P.vocab > 2048) launch_loss_of<DT, 256>(P, stream);
+  else launch_loss_of<DT, 128>(P, stream);
 }
 
+template <int DT, int Threads> void launch_grad_of(const DistillParams& P, int64_t parts, hipStream_t stream) {
+  launch_rows<DT, Threads>(P, parts, [&](const DistillParams& Q, unsigned grid) {
+    distill_grad<DT, Threads><<<grid, Threads, 0, stream>>>(Q, (int)parts);
+  });
+}
 template <int DT> void launch_grad(const DistillParams& P, hipStream_t stream) {
   // up to 16 vectors a thread; short rows take fewer threads (8192 rows of
   // 1000: 128 threads 29 us, 512 threads 56 us)
   const int64_t vecs = P.vocab / Vec<DT>::N;
   const int threads = vecs <= 1024 ? 128 : vecs <= 2048 ? 256 : 512;
-  int64_t parts = (vecs + 16 * threads) / (16 * threads);
-  // a grid has fewer than 2^31 workgroups
-  while (parts > 1 && parts * P.n >= ((int64_t)1 << 31)) parts = (parts + 1) / 2;
-  const unsigned grid = (unsigned)(P.n * parts);
-  if (threads == 128) distill_grad<DT, 128><<<grid, 128, 0, stream>>>(P, (int)parts);
-  else if (threads == 256) distill_grad<DT, 256><<<grid, 256, 0, stream>>>(P, (int)parts);
-  else distill_grad<DT, 512><<<grid, 512, 0, stream>>>(P, (int)parts);
+  const int64_t parts = (vecs + 16 * threads) / (16 * threads);
+  if (threads == 128) launch_grad_of<DT, 128>(P, parts, stream);
+  else if (threads == 256) launch_grad_of<DT, 256>(P, parts, stream);
+  else launch_grad_of<DT, 512>(P, parts, stream);
 }
 
 template <int DT> hipError_t launch(DistillParams P, hipStream_t stream) {

@@ -1,5 +1,9 @@
 """Refusals of the feed-forward block and the distillation loss at the ends of what they promise; no GPU."""
 
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
@@ -29,3 +33,43 @@ def test_forward_mode_is_refused(recording):
             hs.gated_ffn(x, w, w)
         with pytest.raises(ValueError, match="on the GPU"):
             hs.distill_topk(z, ids, v)
+
+
+ROWS = r"""
+#include <cstdio>
+#include "distill_internal.hpp"
+using namespace hess;
+int main() {
+  for (int threads : {128, 256, 512, 1024})
+    for (int64_t parts : {1, 2, 3, 4097, 8193}) {
+      const int64_t most = distill_rows_per_launch(threads, parts);
+      if (most < 1 || most * parts * threads >= (int64_t)1 << 32) return 1;
+      if ((most + 1) * parts * threads < (int64_t)1 << 32) return 2;
+    }
+  DistillParams P{};
+  P.z = (void*)4096, P.ldz = 11, P.n = 10, P.ids = (void*)8192, P.ids64 = 1, P.ldi = 7;
+  P.values = (void*)16384, P.values_dtype = 0, P.ldv = 5, P.loss = (float*)32768, P.stats = (float*)65536;
+  const DistillParams Q = distill_rows(P, 2, 4, 4), T = distill_rows(P, 4, 8, 4);
+  if (Q.n != 4 || T.n != 2 || Q.weight || Q.dz || Q.dloss) return 3;
+  if (Q.z != (void*)(4096 + 4 * 11 * 2) || T.z != (void*)(4096 + 8 * 11 * 4)) return 4;
+  if (Q.ids != (void*)(8192 + 4 * 7 * 8) || Q.values != (void*)(16384 + 4 * 5 * 2)) return 5;
+  if (Q.loss != P.loss + 4 || Q.stats != P.stats + 8) return 6;
+  P.ids64 = 0, P.values_dtype = 1;
+  P.weight = (float*)1024, P.dloss = (float*)2048, P.dz = (void*)512, P.lddz = (int64_t)1 << 30;
+  const DistillParams S = distill_rows(P, 4, 6, 100);
+  if (S.n != 4 || S.ids != (void*)(8192 + 6 * 7 * 4) || S.values != (void*)(16384 + 6 * 5 * 4)) return 7;
+  if (S.weight != P.weight + 6 || S.dloss != P.dloss + 6 || S.dz != (void*)(512 + ((int64_t)24 << 30))) return 8;
+  return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include/hip"),
+                    reason="needs a host compiler and HIP's headers")
+def test_rows_of_a_launch(tmp_path):
+    """A grid stays below 2^32 threads, and a range of rows moves every pointer by its own stride."""
+    csrc = os.path.join(os.path.dirname(os.path.abspath(hs.__file__)), "csrc")
+    (tmp_path / "rows.cpp").write_text(ROWS)
+    subprocess.run(["g++", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include", "-I", csrc,
+                    str(tmp_path / "rows.cpp"), "-o", str(tmp_path / "rows")], check=True)
+    assert subprocess.run([str(tmp_path / "rows")]).returncode == 0

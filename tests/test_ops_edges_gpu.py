@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import gptq_hessian_accumulation_amd as hs
+from oracle import ops_oracle as R
 from tests import test_distill_gpu as D
 
 pytestmark = [pytest.mark.gpu,
@@ -51,3 +52,36 @@ def test_nan_among_the_teachers_values(dt, vocab):
     for r in range(4):
         assert torch.isnan(grad[r, i[r]]).all()
         assert int(torch.isnan(grad[r]).sum()) == 200
+
+
+def test_more_rows_than_a_grid_takes():
+    """2^24 rows of 256 threads are 2^32 threads: two launches, in the loss and in the gradient (137 GB)."""
+    n, vocab = 1 << 24, 4104
+    D.say(f"{n} rows of {vocab}")
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GiB of free GPU memory")
+    z = torch.zeros((n, vocab), dtype=torch.bfloat16, device="cuda")
+    ids = (torch.arange(n, device="cuda", dtype=torch.int32) % vocab)[:, None].contiguous()
+    v = torch.zeros((n, 1), device="cuda")
+    rows = [0, 1, n - 3, n - 2, n - 1]
+    z[rows] = torch.randn((5, vocab), generator=torch.Generator("cuda").manual_seed(33), device="cuda").bfloat16()
+    zn, inn, vn = D.f64(z[rows]), ids[rows].cpu().numpy(), D.f64(v[rows])
+    l, _, g = R.distill_topk(zn, inn, vn, np.ones(5), 1.0)
+    tl, tg = D.tolerances(zn, inn, vn, np.ones(5), 1.0, vocab, l, g, "bf16")
+    loss, stats = hs.distill_topk_forward(z, ids, v)
+    D.compare(loss[rows], l, tl, "loss")
+    assert stats[2, 0] == 0 and stats[n - 4, 0] == 0
+    # every other row is the same one: equal logits
+    lz, _, gz = R.distill_topk(np.zeros((1, vocab)), np.zeros((1, 1), dtype=np.int64), np.zeros((1, 1)), np.ones(1), 1.0)
+    tz = D.tolerances(np.zeros((1, vocab)), np.zeros((1, 1), dtype=np.int64), np.zeros((1, 1)), np.ones(1), 1.0, vocab,
+                      lz, gz, "bf16")[0][0]
+    assert float((loss[2:n - 3].double() - lz[0]).abs().max()) <= tz
+    loss2, _ = hs.distill_topk_step(z, ids, v, out=z)
+    torch.cuda.synchronize()
+    D.compare(loss2[rows], l, tl, "step's loss")
+    D.compare(z[rows], g, tg, "gradient")
+    at = z[2:n - 3].gather(1, ids[2:n - 3].long())
+    assert (at == at[0]).all() and abs(float(at[0]) - gz[0, 0]) <= 2.0 ** -8
+    del z, at
+    torch.cuda.empty_cache()
