@@ -153,8 +153,16 @@ __device__ __forceinline__ void put_fwd(const FfnGemm& P, int64_t r, int64_t c, 
 #pragma unroll
   for (int j = 0; j < N; ++j) h[j] = act_value<DT == kInF32>(g[j], P.act) * u[j];
   if (c < P.N) store_n(static_cast<T*>(P.o0) + r * P.ldo0 + c, h, (int)min((int64_t)N, P.N - c));
-  // columns f .. fp - 1 are the zeros their absent weight rows gave
-  if (P.o1) put_preact<T>(P, r, c, g, u);
+  if (!P.o1) return;
+  // columns f .. fp - 1 are zeros: absent weight rows read as zeros, but times
+  // an infinite x they are none
+  float gz[N], uz[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    gz[j] = c + j < P.N ? g[j] : 0.0f;
+    uz[j] = c + j < P.N ? u[j] : 0.0f;
+  }
+  put_preact<T>(P, r, c, gz, uz);
 }
 
 // Tile t of the blocked order: groups of 8 (dW: 4) tile rows, column by column

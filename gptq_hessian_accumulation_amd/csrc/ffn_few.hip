@@ -119,10 +119,7 @@ template <int DT, int MB, int FB, int W, int U> __global__ void __launch_bounds_
     const int64_t c = f0 + 16 * p + 4 * (l >> 4);
     float gg[4], uu[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      gg[j] = c + j < P.N ? g[j] : 0.0f;
-      uu[j] = c + j < P.N ? v[j] : 0.0f;
-    }
+    for (int j = 0; j < 4; ++j) gg[j] = g[j], uu[j] = v[j];
     put_fwd<DT>(P, 16 * q + (l & 15), c, gg, uu);
   }
 }

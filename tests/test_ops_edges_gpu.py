@@ -85,3 +85,19 @@ def test_more_rows_than_a_grid_takes():
     assert (at == at[0]).all() and abs(float(at[0]) - gz[0, 0]) <= 2.0 ** -8
     del z, at
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n", [20, 70, 300])
+@pytest.mark.parametrize("dt", list(D.TYPES))
+def test_padding_of_the_saved_pair_is_zero(dt, n):
+    """Columns f .. f' - 1 of the saved pair are zeros whatever x and the weights hold."""
+    D.say(f"padding {dt} {n}")
+    d, f = 72, 61
+    gen = torch.Generator("cuda").manual_seed(34)
+    x = torch.randn((n, d), generator=gen, device="cuda").to(D.TYPES[dt])
+    wg, wu = (torch.randn((2 * f, d), generator=gen, device="cuda") / 8).to(D.TYPES[dt]).split(f)
+    x[3, 5], x[7, 70], wg[f - 1, 2] = float("inf"), float("nan"), float("-inf")
+    for save in (True, D.TYPES[dt]):
+        pre = hs.gated_ffn_forward(x, wg, wu, save=save)[1]
+        assert not pre[:, f:64].any() and not pre[:, 64 + f:].any()
+        assert torch.isnan(pre[7, :f]).all() and not torch.isfinite(pre[3, 64:64 + f]).any()
