@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/hess.h"
@@ -325,8 +326,9 @@ int check_distill(const DistillParams& P, int dtype, int values_dtype) {
   if (P.vocab < 1 || P.vocab > kMaxVocab)
     return fail(HESS_EINVAL, "vocab = %lld outside [1, 2^28]", (long long)P.vocab);
   if (P.k < 1 || P.k > kMaxTop) return fail(HESS_EINVAL, "k = %d outside [1, %d]", P.k, kMaxTop);
-  if (!(P.temperature > 0.0f) || !std::isfinite(P.temperature))
-    return fail(HESS_EINVAL, "temperature %g not positive and finite", (double)P.temperature);
+  // (the reciprocal of a subnormal one passes float32's range)
+  if (!(P.temperature >= FLT_MIN) || !std::isfinite(P.temperature))
+    return fail(HESS_EINVAL, "temperature %g not positive and finite, or below 2^-126", (double)P.temperature);
   if (P.n == 0) return HESS_OK;
   if (!P.z || !P.ids || !P.values) return fail(HESS_EINVAL, "null logits, ids or values");
   const int64_t es = elem_bytes(dtype);

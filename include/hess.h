@@ -639,7 +639,8 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
  *   weight    n floats, or NULL for ones.  A row of weight 0, or one whose
  *             entries are all absent, has loss 0 and a zero gradient whatever
  *             its logits hold.
- *   T         temperature, > 0 and finite.  The loss is not multiplied by T^2.
+ *   T         temperature, at least 2^-126 and finite.  The loss is not
+ *             multiplied by T^2.
  * Limits: 0 <= n <= 2^24, 1 <= vocab <= 2^28, 1 <= k <= 1024.  Exponentials
  * and sums are float32, the k terms of the loss float64.
  *

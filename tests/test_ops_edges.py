@@ -1,5 +1,6 @@
 """Refusals of the feed-forward block and the distillation loss at the ends of what they promise; no GPU."""
 
+import ctypes
 import os
 import shutil
 import subprocess
@@ -73,3 +74,16 @@ def test_rows_of_a_launch(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include", "-I", csrc,
                     str(tmp_path / "rows.cpp"), "-o", str(tmp_path / "rows")], check=True)
     assert subprocess.run([str(tmp_path / "rows")]).returncode == 0
+
+
+@pytest.mark.parametrize("t", [1e-40, 1.4e-45, 2.0 ** -127, 0.0, -1.0, float("inf"), float("nan")])
+def test_temperatures_without_a_reciprocal(t):
+    """A subnormal temperature has no float32 reciprocal: refused, like those that are no temperature."""
+    lib = hs._load()
+    p = [ctypes.c_void_p((1 << 40) + (q << 36)) for q in range(8)]
+    assert lib.hess_distill_topk(p[0], 100, 0, 4, 100, p[1], 0, 8, p[2], 1, 8, 8, p[3], t, p[4], p[5], p[6], 100, p[7],
+                                 1 << 30, None) == -1
+    assert b"temperature" in lib.hess_last_error()
+    assert lib.hess_distill_topk_backward(p[4], p[0], 100, 0, 4, 100, p[1], 0, 8, p[2], 1, 8, 8, p[3], t, p[5], p[6],
+                                          100, None) == -1
+    assert b"temperature" in lib.hess_last_error()

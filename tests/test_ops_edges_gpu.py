@@ -101,3 +101,24 @@ def test_padding_of_the_saved_pair_is_zero(dt, n):
         pre = hs.gated_ffn_forward(x, wg, wu, save=save)[1]
         assert not pre[:, f:64].any() and not pre[:, 64 + f:].any()
         assert torch.isnan(pre[7, :f]).all() and not torch.isfinite(pre[3, 64:64 + f]).any()
+
+
+def test_smallest_temperature():
+    """At 2^-126 both softmaxes are one word each: the gradient is weight / T there, with either sign."""
+    D.say("smallest temperature")
+    z, i, v, w = D.make(35, "f32", 4, 500, 20)
+    best = z.argmax(1)
+    i[:2, 3], v[:2, 3] = best[:2], 50.0     # rows 0 and 1: the teacher agrees
+    i[2:, 3], v[2:, 3] = (best[2:] + 1) % 500, 50.0
+    w[:] = 1.0
+    t = 2.0 ** -126
+    loss, grad = hs.distill_topk_step(z, i, v, weight=w, temperature=t)
+    assert not loss[:2].any() and not grad[:2].any()
+    want = torch.zeros_like(z)
+    for r in (2, 3):
+        want[r, best[r]], want[r, i[r, 3]] = 1 / t, -1 / t
+    assert torch.equal(grad, want)
+    far = (z[2:].gather(1, best[2:, None]) - z[2:].gather(1, i[2:, 3:4]))[:, 0].double() / t
+    assert torch.allclose(loss[2:].double(), far.float().double(), rtol=2.0 ** -21, atol=0.0)
+    with pytest.raises(hs.HessError, match="temperature"):
+        hs.distill_topk_step(z, i, v, weight=w, temperature=1e-40)
