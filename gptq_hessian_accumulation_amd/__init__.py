@@ -553,6 +553,7 @@ def materialize_grouped(hessians, damp_percent: float = 0.01, outs=None, neutral
 
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _PREACT_F32 = 16
+_FEW = 64  # tokens of a forward call up to which the library takes rows of any alignment
 _CODES = {torch.bfloat16: HESS_BF16, torch.float32: HESS_F32, torch.float16: HESS_F16}
 
 
@@ -615,8 +616,10 @@ def _act_mode(act: str) -> int:
     return mode
 
 
-def _ffn_args(x, w_gate, w_up):
-    """(code, n, d, f, tensors to keep, (x, stride, gate, stride, up, stride) for the library)."""
+def _ffn_args(x, w_gate, w_up, any_rows=0):
+    """(code, n, d, f, tensors to keep, (x, stride, gate, stride, up, stride) for the library).
+
+    any_rows: up to how many tokens the call reads rows of any alignment where they are."""
     code = _float_code("x", x)
     shape = w_gate.shape
     if len(shape) != 2 or shape != w_up.shape:
@@ -630,11 +633,12 @@ def _ffn_args(x, w_gate, w_up):
         raise ValueError("w_gate must have x's dtype and device")
     if w_up.dtype != dtype or w_up.get_device() != index:
         raise ValueError("w_up must have x's dtype and device")
+    x2 = x if len(given) == 2 else x.reshape(-1, d)
     # the tiles read rows of a multiple of 16 bytes where they are, if they start at 16 bytes
     step = 4 if code == HESS_F32 else 8
-    if d % step != 0:
+    if d % step != 0 or x2.shape[0] <= any_rows:
         step = 1
-    x2, xp, ldx = _rows(x if len(given) == 2 else x.reshape(-1, d), step)
+    x2, xp, ldx = _rows(x2, step)
     wg, gp, ldg = _rows(w_gate, step)
     wu, up, ldu = _rows(w_up, step)
     return code, x2.shape[0], d, f, (x2, wg, wu), (xp, ldx, gp, ldg, up, ldu)
@@ -656,7 +660,7 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
             return gated_ffn_forward(x, w_gate, w_up, act, save, out, workspace)
     lib = _load()
     mode = _act_mode(act)
-    code, n, d, f, keep, ins = _ffn_args(x, w_gate, w_up)
+    code, n, d, f, keep, ins = _ffn_args(x, w_gate, w_up, _FEW)
     h = _out("out", out, (*x.shape[:-1], f), x)
     pre = None
     if save:

@@ -10,6 +10,7 @@ import torch
 import gptq_hessian_accumulation_amd as hs
 from oracle import ops_oracle as R
 from tests import test_distill_gpu as D
+from tests import test_gated_ffn_gpu as G
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs an MI355X GPU")]
@@ -122,3 +123,25 @@ def test_smallest_temperature():
     assert torch.allclose(loss[2:].double(), far.float().double(), rtol=2.0 ** -21, atol=0.0)
     with pytest.raises(hs.HessError, match="temperature"):
         hs.distill_topk_step(z, i, v, weight=w, temperature=1e-40)
+
+
+@pytest.mark.parametrize("dt", list(D.TYPES))
+@pytest.mark.parametrize("n", [1, 24, 64])
+def test_few_tokens_copy_no_weights(n, dt):
+    """Up to 64 tokens the forward pass reads weights of any alignment where they are."""
+    D.say(f"no copies {dt} {n}")
+    d, f = 512, 2048
+    gen = torch.Generator("cuda").manual_seed(36)
+    flat = (torch.randn(2 * f * (d + 8) + 1, generator=gen, device="cuda") / 16).to(D.TYPES[dt])
+    x = torch.randn((n, d), generator=gen, device="cuda").to(D.TYPES[dt])
+    xn = D.f64(x)
+    # rows off 16 bytes; rows at an odd stride
+    for w in (flat[1:1 + 2 * f * d].view(2 * f, d), flat[:2 * f * (d + 1)].view(2 * f, d + 1)[:, :d]):
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        h = hs.gated_ffn_forward(x, w[:f], w[f:])
+        assert torch.cuda.max_memory_allocated() - before < w[:f].numel() * w.element_size() // 2
+        want, g, u = R.gated_ffn(xn, D.f64(w[:f]), D.f64(w[f:]), "silu")
+        tol = G.forward_tolerance(xn, D.f64(w[:f]), D.f64(w[f:]), g, u, "silu", dt)[0]
+        G.check("h", h, want, tol)
