@@ -1,6 +1,6 @@
 // The gated feed-forward block, forward, for few tokens (a decoding step).
 //
-// Bound by the weights' bytes.  A workgroup takes 16 to 64 features of both
+// Bound by the weights' bytes.  A workgroup takes 16 or 32 features of both
 // projections and the whole of K: its waves split K, each lane loads 16 bytes
 // of one weight row straight into the matrix instruction's operand (no LDS,
 // any alignment; 64 consecutive bytes a row and instruction), x comes from L2
@@ -30,7 +30,8 @@ template <class T> __device__ __forceinline__ u32x4 load16(const T* p) {
   if constexpr (sizeof(T) == 2) return *reinterpret_cast<const u32x4_at2*>(p);
   else return *reinterpret_cast<const u32x4_at4*>(p);
 }
-// The first `left` (< 16 / sizeof(T)) elements at p, zeros after them.
+// The first `left` elements at p, zeros after them (left: what is left of a row
+// at a lane's chunk, so any number below 64 / sizeof(T), zero and less too).
 template <class T> __device__ __forceinline__ u32x4 load_part(const T* p, int left) {
   constexpr int N = 16 / sizeof(T);
   typedef T TN __attribute__((ext_vector_type(16 / sizeof(T))));
@@ -128,16 +129,17 @@ template <int DT, int MB, int FB, int U> void launch_few(const FfnGemm& g, hipSt
   ffn_few<DT, MB, FB, 4, U><<<(unsigned)((g.N + 16 * FB - 1) / (16 * FB)), 256, 0, stream>>>(g);
 }
 
-// More features a workgroup read x less often, but need many features to have
-// a workgroup for each CU: at 4096 x 11264, fp16, 32 tokens 48.6 us with 32
-// features and 51.7 with 16, 64 tokens 61.1 with 64 and 68.6 with 16; at
-// 1001 x 2731, 24 tokens 15.2 against 11.5, 64 tokens 30.1 against 16.2.
+// 16 features a workgroup leave no second round of workgroups up to 4096
+// features; past that, 32 read x half as often.  32 tokens, 16 against 32
+// features, us: bf16 2560 x 4096 15.8 / 19.3, 2560 x 4160 23.1 / 18.6, 2560 x
+// 8192 26.2 / 21.2, 4096 x 11264 53.7 / 50.2; float32 2560 x 4096 26.5 / 40.6,
+// 2560 x 5632 50.7 / 41.2, 4096 x 11264 120 / 118.  One block of tokens gains
+// nothing (16 tokens, 4096 x 11264 40.7 / 45.5), nor do four (64 tokens, 64
+// features: 2560 x 8192 33.9 / 44.6, 4096 x 11264 69.9 / 64.7).
 template <int DT> void launch_type(const FfnGemm& g, hipStream_t stream) {
-  const bool wide = g.N >= 8192;
   if (g.M <= 16) launch_few<DT, 1, 1, 4>(g, stream);
-  else if (g.M <= 32 && wide) launch_few<DT, 2, 2, 2>(g, stream);
+  else if (g.M <= 32 && g.N > 4096) launch_few<DT, 2, 2, 2>(g, stream);
   else if (g.M <= 32) launch_few<DT, 2, 1, 4>(g, stream);
-  else if (wide) launch_few<DT, 4, 4, 1>(g, stream);
   else launch_few<DT, 4, 1, 2>(g, stream);
 }
 

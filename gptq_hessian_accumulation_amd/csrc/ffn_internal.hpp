@@ -48,6 +48,24 @@ hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int edge, int dtype, hipS
 // The forward product of at most kFfnFew tokens: operands of any alignment, no
 // workspace.
 constexpr int64_t kFfnFew = 64;
+
+// Whether up to kFfnFew tokens take that kernel also where tiles could read the
+// operands in place.  Every workgroup reads all of x, padded to 16, 32 or 64
+// tokens, so tiles, which split K over workgroups, gain as x grows; past 32
+// tokens a second round of workgroups (one for 16 features, 256 CUs) costs
+// more than they do.  Few tokens against tiles, us, weights not in any cache:
+//   bf16, 16 tokens   2560 x 2816 11.0 / 15.8   4096 x 11264 40.7 / 51.5
+//         32 tokens   2560 x 2816 15.2 / 16.5   4096 x 11264 50.2 / 54.1   8192 x 2816 40.3 / 30.8
+//         64 tokens   1024 x 2816  9.1 / 12.2   2560 x 2816 18.5 / 19.0    4096 x 2816 25.6 / 20.6
+//                     2560 x 5632 32.3 / 30.1   4096 x 11264 69.9 / 60.0
+//   float32, 32 tokens  2560 x 2816 25.0 / 28.4   4096 x 2816 34.5 / 36.5   4096 x 11264 118 / 111
+//            64 tokens  1024 x 2816 19.7 / 19.4   2560 x 2816 41.9 / 30.7   4096 x 11264 152 / 116
+// The limit's worst case is near 32 bf16 tokens at 4096 x 1024: 20.6 / 16.7.
+inline bool ffn_prefers_few(int64_t n, int64_t d, int64_t f, int64_t esize) {
+  if (n <= 16) return true;
+  if (n <= 32) return 32 * d * esize <= 320 * 1024;
+  return n <= kFfnFew && f <= 4096 && 64 * d * esize <= 320 * 1024;
+}
 hipError_t launch_ffn_few(const FfnGemm& g, int dtype, hipStream_t stream);
 
 // Copies up to three matrices of rows[m] x cols 16-bit values (row stride

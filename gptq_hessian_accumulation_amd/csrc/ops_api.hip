@@ -109,7 +109,7 @@ struct FfnWork {
 };
 FfnWork ffn_work(int64_t n, int64_t d, int64_t f, int dtype, bool backward) {
   FfnWork w{};
-  if (!backward && n <= kFfnFew) return w;
+  if (!backward && n <= kFfnFew && (packed(d, dtype) || ffn_prefers_few(n, d, f, elem_bytes(dtype)))) return w;
   w.pack = backward ? up(n * 2 * up(f, 8) * elem_bytes(dtype), 256) : 0;
   w.slots = w.pack + (packed(d, dtype) ? pack_bytes(n, d, dtype) + 2 * pack_bytes(f, d, dtype) : 0);
   w.total = w.slots + (backward ? std::max(slot_bytes(shape(n, d, f), kFfnDx, dtype),
@@ -124,12 +124,17 @@ struct FfnOperands {
   const void *x, *wg, *wu;
   int64_t ldx, ldg, ldu, d;
 };
+// Whether rows of x, gate and up start where the tiles can read them.
+bool rows_in_place(const FfnOperands& o, int64_t n, int64_t f, int dtype) {
+  const int64_t step = piece(dtype);
+  return aligned(o.x, 16) && aligned(o.wg, 16) && aligned(o.wu, 16) && (n <= 1 || o.ldx % step == 0) &&
+         (f <= 1 || (o.ldg % step == 0 && o.ldu % step == 0));
+}
 int place_operands(FfnOperands& o, char* pack, int64_t n, int64_t f, int dtype, bool want_x, bool want_w,
                    hipStream_t s) {
   const int64_t step = piece(dtype);
   if (!packed(o.d, dtype)) {
-    if (!aligned(o.x, 16) || !aligned(o.wg, 16) || !aligned(o.wu, 16) || (n > 1 && o.ldx % step != 0) ||
-        (f > 1 && (o.ldg % step != 0 || o.ldu % step != 0)))
+    if (!rows_in_place(o, n, f, dtype))
       return fail(HESS_EALIGN, "rows of x, w_gate and w_up must be 16-byte aligned where a row is a multiple of 16 bytes");
     return HESS_OK;
   }
@@ -189,14 +194,15 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
     if (int rc = check_mat(m, es)) return rc;
   if (int rc = check_mat(outs[0], es)) return rc;
   if (!aligned(preact, 16)) return fail(HESS_EALIGN, "preact not 16-byte aligned");
-  const FfnWork room = ffn_work(n, d, f, dtype, false);
+  FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
+  // few tokens whose rows the tiles cannot read where they are: no copies
+  const bool few = n <= kFfnFew && (packed(d, dtype) || ffn_prefers_few(n, d, f, es) || !rows_in_place(o, n, f, dtype));
+  const FfnWork room = few ? FfnWork{} : ffn_work(n, d, f, dtype, false);
   if (int rc = check_work(work, work_bytes, room.total)) return rc;
   if (int rc = check_outputs(outs, 2, ins, 3, es, work, room.total)) return rc;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* base = static_cast<char*>(work);
-  FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
-  const bool few = n <= kFfnFew;
   if (!few)
     if (int rc = place_operands(o, base, n, f, dtype, true, true, s)) return rc;
   FfnGemm g = shape(n, f, o.d);

@@ -65,15 +65,23 @@ int main() {
 """
 
 
-@pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include/hip"),
-                    reason="needs a host compiler and HIP's headers")
+host_compiler = pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include/hip"),
+                                   reason="needs a host compiler and HIP's headers")
+
+
+def run_host(tmp_path, source):
+    """The exit code of a program over the library's internal headers, compiled for the host."""
+    csrc = os.path.join(os.path.dirname(os.path.abspath(hs.__file__)), "csrc")
+    (tmp_path / "host.cpp").write_text(source)
+    subprocess.run(["g++", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include", "-I", csrc,
+                    str(tmp_path / "host.cpp"), "-o", str(tmp_path / "host")], check=True)
+    return subprocess.run([str(tmp_path / "host")]).returncode
+
+
+@host_compiler
 def test_rows_of_a_launch(tmp_path):
     """A grid stays below 2^32 threads, and a range of rows moves every pointer by its own stride."""
-    csrc = os.path.join(os.path.dirname(os.path.abspath(hs.__file__)), "csrc")
-    (tmp_path / "rows.cpp").write_text(ROWS)
-    subprocess.run(["g++", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include", "-I", csrc,
-                    str(tmp_path / "rows.cpp"), "-o", str(tmp_path / "rows")], check=True)
-    assert subprocess.run([str(tmp_path / "rows")]).returncode == 0
+    assert run_host(tmp_path, ROWS) == 0
 
 
 @pytest.mark.parametrize("t", [1e-40, 1.4e-45, 2.0 ** -127, 0.0, -1.0, float("inf"), float("nan")])
@@ -87,3 +95,35 @@ def test_temperatures_without_a_reciprocal(t):
     assert lib.hess_distill_topk_backward(p[4], p[0], 100, 0, 4, 100, p[1], 0, 8, p[2], 1, 8, 8, p[3], t, p[5], p[6],
                                           100, None) == -1
     assert b"temperature" in lib.hess_last_error()
+
+
+# (element bytes, tokens, d, f, us of the few-token kernel, us of the tiles), weights in no cache
+FEW_OR_TILES = [
+    (2, 8, 1024, 2816, 5.8, 11.6), (2, 16, 2560, 2816, 11.0, 15.8), (2, 16, 4096, 11264, 40.7, 51.5),
+    (2, 16, 8192, 4096, 34.8, 41.0), (2, 16, 8192, 16384, 116.3, 138.8), (2, 24, 2560, 2816, 14.5, 15.9),
+    (2, 32, 2560, 2816, 15.2, 16.5), (2, 32, 2560, 5632, 19.3, 25.2), (2, 32, 2560, 9728, 34.6, 38.6),
+    (2, 32, 4096, 5632, 25.9, 29.4), (2, 32, 4096, 11264, 50.2, 54.1), (2, 32, 5120, 13824, 70.1, 76.0),
+    (2, 32, 8192, 2816, 40.3, 30.8), (2, 32, 8192, 1024, 37.7, 18.3), (2, 32, 8192, 11264, 105.7, 97.3),
+    (2, 33, 1024, 2816, 7.9, 11.9), (2, 33, 2560, 2816, 14.8, 16.7), (2, 64, 1024, 2816, 9.1, 12.2),
+    (2, 64, 2560, 4096, 18.9, 22.2), (2, 40, 2560, 4160, 26.2, 21.8), (2, 64, 2560, 5632, 32.3, 30.1),
+    (2, 64, 4096, 5632, 47.4, 32.7), (2, 64, 4096, 2816, 25.6, 20.6), (2, 64, 8192, 1024, 45.7, 19.3),
+    (2, 48, 4096, 11264, 62.7, 57.5), (2, 64, 4096, 11264, 69.9, 60.0), (2, 64, 1024, 8192, 15.0, 12.1),
+    (4, 16, 2560, 2816, 19.1, 27.6), (4, 16, 4096, 11264, 86.2, 110.7), (4, 32, 1024, 2816, 12.7, 18.8),
+    (4, 32, 2560, 2816, 25.0, 28.4), (4, 32, 4096, 11264, 117.7, 111.3), (4, 33, 2560, 2816, 39.8, 28.9),
+    (4, 64, 2560, 4096, 43.0, 34.1), (4, 64, 4096, 2816, 64.2, 39.2), (4, 64, 4096, 11264, 151.6, 116.3)]
+
+
+@host_compiler
+def test_few_tokens_take_the_faster_kernel(tmp_path):
+    """The rule's choice where one kernel was timed at least a twentieth ahead of the other."""
+    cases = "".join(f"if (ffn_prefers_few({n}, {d}, {f}, {e}) != {int(few < tiles)}) return {i + 1};\n"
+                    for i, (e, n, d, f, few, tiles) in enumerate(FEW_OR_TILES) if max(few, tiles) > 1.05 * min(few, tiles))
+    assert run_host(tmp_path, '#include "ffn_internal.hpp"\nusing namespace hess;\nint main() {\n' + cases
+                    + "return ffn_prefers_few(65, 8, 8, 2);\n}\n") == 0
+
+
+def test_workspace_up_to_64_tokens():
+    """Where tiles take the call, their partial sums need room; rows they would have to copy stay with the other kernel."""
+    room = hs._load().hess_gated_ffn_workspace
+    assert room(64, 1024, 2816, 0, 0) == 0 and room(16, 16384, 512, 0, 0) == 0
+    assert room(64, 8192, 1024, 0, 0) > 0 and room(64, 8193, 1024, 0, 0) == 0

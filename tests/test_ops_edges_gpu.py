@@ -145,3 +145,21 @@ def test_few_tokens_copy_no_weights(n, dt):
         want, g, u = R.gated_ffn(xn, D.f64(w[:f]), D.f64(w[f:]), "silu")
         tol = G.forward_tolerance(xn, D.f64(w[:f]), D.f64(w[f:]), g, u, "silu", dt)[0]
         G.check("h", h, want, tol)
+
+
+@pytest.mark.parametrize("dt", list(D.TYPES))
+@pytest.mark.parametrize("n,d,f", [(33, 1032, 4104), (64, 264, 8200), (48, 5128, 136), (64, 5120, 4096), (31, 10248, 40)])
+def test_tokens_where_tiles_take_over(n, d, f, dt):
+    """Up to 64 tokens through the tiles, and through the other kernel where the rows do not start at 16 bytes."""
+    D.say(f"take over {dt} {n}x{d}x{f}")
+    x, xn = G.draw(41, dt, n, d)
+    w, wn = G.draw(42, dt, 2 * f, d, scale=1.5 / d ** 0.5)
+    want, g, u = R.gated_ffn(xn, wn[:f], wn[f:], "gelu")
+    tol = G.forward_tolerance(xn, wn[:f], wn[f:], g, u, "gelu", dt)[0]
+    G.check("h", hs.gated_ffn_forward(x, w[:f], w[f:], act="gelu"), want, tol)
+    off = torch.empty(2 * f * d + 1, dtype=w.dtype, device="cuda")[1:].view(2 * f, d)
+    off.copy_(w)
+    G.check("h, weights off 16 bytes", hs.gated_ffn_forward(x, off[:f], off[f:], act="gelu"), want, tol)
+    far = torch.zeros((n, d + 1), dtype=x.dtype, device="cuda")[:, :d]
+    far.copy_(x)
+    G.check("h, x at an odd stride", hs.gated_ffn_forward(far, w[:f], w[f:], act="gelu"), want, tol)
