@@ -42,6 +42,7 @@ __all__ = [
     "distill_topk_backward",
     "distill_topk_step",
     "set_tile_override",
+    "set_ffn_schedule",
     "set_staging",
     "library_path",
     "exported_symbols",
@@ -99,6 +100,7 @@ def _load():
         "hess_reset": (c_int, [vp, vp]),
         "hess_token_count": (c_int, [vp, ctypes.POINTER(i64)]),
         "hess_set_tile_override": (c_int, [c_int]),
+        "hess_set_ffn_schedule": (c_int, [c_int, c_int, c_int]),
         "hess_set_staging": (c_int, [c_int]),
         "hess_set_async_flush": (c_int, [c_int]),
         "hess_set_group_chunk": (c_int, [i64]),
@@ -231,6 +233,12 @@ def set_group_direct(enable: bool) -> None:
 def set_tile_override(edge: int) -> None:
     """Force the SYRK tile edge (0 = automatic, 64, 128 or 256); process-wide."""
     _check(_load().hess_set_tile_override(int(edge)))
+
+
+def set_ffn_schedule(edge: int = 0, whole: int = 0, parts: int = 1) -> None:
+    """Force the feed-forward block's tiles (edge 0 = automatic, 64, 128 or 256), the first ``whole`` done whole
+    and the others in ``parts`` ranges of the sum; process-wide."""
+    _check(_load().hess_set_ffn_schedule(int(edge), int(whole), int(parts)))
 
 
 class Hessian:

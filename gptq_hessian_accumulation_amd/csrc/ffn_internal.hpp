@@ -41,6 +41,14 @@ struct FfnGemm {
 // Chooses the tile's edge (returned) and fills the schedule.
 int ffn_schedule(FfnGemm& g, int mode, int dtype);
 
+// A schedule in place of the estimate's, process-wide: tiles of this edge (0:
+// the estimate's own choice), the first `whole` of them done whole and the
+// others in `parts` ranges of K.
+struct FfnForced {
+  int edge, whole, parts;
+};
+void ffn_force_schedule(FfnForced f);
+
 // One product by tiles.  Every operand row 16-byte aligned; where an operand's
 // rows run along K, K is a whole number of 16-byte pieces.
 hipError_t launch_ffn_gemm(const FfnGemm& g, int mode, int edge, int dtype, hipStream_t stream);

@@ -147,7 +147,21 @@ double schedule_for(FfnGemm& g, int mode, int edge, bool f32) {
 
 }  // namespace
 
+namespace {
+FfnForced g_forced{0, 0, 1};
+}
+void ffn_force_schedule(FfnForced f) { g_forced = f; }
+
 int ffn_schedule(FfnGemm& g, int mode, int dtype) {
+  const FfnForced forced = g_forced;
+  if (forced.edge != 0) {
+    schedule_for(g, mode, forced.edge, dtype == kInF32);
+    g.part_len = (g.niter + forced.parts - 1) / forced.parts;
+    g.parts = (g.niter + g.part_len - 1) / g.part_len;
+    // (the tiles cut along K are at most as many as the estimate would cut)
+    g.full = g.parts == 1 ? g.ntiles : std::max(std::min(forced.whole, g.ntiles), g.ntiles - 1024);
+    return forced.edge;
+  }
   int edge = 0;
   double least = 1e30;
   FfnGemm chosen{};

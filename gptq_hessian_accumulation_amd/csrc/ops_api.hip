@@ -96,6 +96,16 @@ int64_t slot_bytes(FfnGemm g, int mode, int dtype) {
   return (int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4;
 }
 
+// One product by tiles, its partial sums in `room` bytes at g.ws.  (The schedule
+// is the one the room was taken for, unless hess_set_ffn_schedule ran between.)
+int run_product(FfnGemm& g, int mode, int dtype, int64_t room, hipStream_t s, const char* what) {
+  const int edge = ffn_schedule(g, mode, dtype);
+  if ((int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4 > room)
+    return fail(HESS_EINVAL, "schedule changed during the call");
+  const hipError_t e = launch_ffn_gemm(g, mode, edge, dtype, s);
+  return e == hipSuccess ? HESS_OK : hip_fail(e, what);
+}
+
 // The tiles take 16-byte pieces of the rows of x and the weights: widths that
 // are no whole number of them are copied to padded rows in the workspace.
 int64_t piece(int dtype) { return 16 / elem_bytes(dtype); }
@@ -165,6 +175,14 @@ int place_operands(FfnOperands& o, char* pack, int64_t n, int64_t f, int dtype, 
 
 extern "C" {
 
+int hess_set_ffn_schedule(int edge, int whole, int parts) {
+  if (edge != 0 && edge != 64 && edge != 128 && edge != 256)
+    return fail(HESS_EINVAL, "tile edge must be 0, 64, 128 or 256");
+  if (whole < 0 || parts < 1 || parts > 64) return fail(HESS_EINVAL, "whole < 0, or parts outside [1, 64]");
+  ffn_force_schedule({edge, whole, parts});
+  return HESS_OK;
+}
+
 int64_t hess_gated_ffn_preact_cols(int64_t f) {
   if (f < 1 || f > kMaxWidth) {
     fail(HESS_EINVAL, "f = %lld outside [1, 2^17]", (long long)f);
@@ -221,13 +239,8 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
   g.fp = fp;
   g.act = act;
   g.pre32 = pre32;
-  hipError_t e;
-  if (few) {
-    e = launch_ffn_few(g, dtype, s);
-  } else {
-    const int edge = ffn_schedule(g, kFfnFwd, dtype);
-    e = launch_ffn_gemm(g, kFfnFwd, edge, dtype, s);
-  }
+  if (!few) return run_product(g, kFfnFwd, dtype, room.total - room.slots, s, "gated feed-forward launch");
+  const hipError_t e = launch_ffn_few(g, dtype, s);
   return e == hipSuccess ? HESS_OK : hip_fail(e, "gated feed-forward launch");
 }
 
@@ -288,9 +301,7 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
     g.ws = slots;
     g.f = f;
     g.fp = fp;
-    const int edge = ffn_schedule(g, kFfnDx, dtype);
-    e = launch_ffn_gemm(g, kFfnDx, edge, dtype, s);
-    if (e != hipSuccess) return hip_fail(e, "input gradient launch");
+    if (int rc = run_product(g, kFfnDx, dtype, room.total - room.slots, s, "input gradient launch")) return rc;
   }
   if (dw_gate) {
     FfnGemm g = shape(2 * fp, d, n);
@@ -305,9 +316,7 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
     g.ws = slots;
     g.f = f;
     g.fp = fp;
-    const int edge = ffn_schedule(g, kFfnDw, dtype);
-    e = launch_ffn_gemm(g, kFfnDw, edge, dtype, s);
-    if (e != hipSuccess) return hip_fail(e, "weight gradient launch");
+    if (int rc = run_product(g, kFfnDw, dtype, room.total - room.slots, s, "weight gradient launch")) return rc;
   }
   return HESS_OK;
 }

@@ -584,6 +584,14 @@ int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int
  * fp .. fp + f - 1); -1 for bad f. */
 int64_t hess_gated_ffn_preact_cols(int64_t f);
 
+/* Tuning and test hook, process-wide: the tiles of the block's products (calls
+ * of the few-token kernel excepted).  edge 64, 128 or 256: tiles of that edge,
+ * the first `whole` of them (and all but the last 1,024) done whole, the others
+ * in `parts` (1 .. 64) ranges of K added by a second launch.  edge 0: the
+ * choice per call, an estimate of the time.  Workspaces are sized for the
+ * schedule in force.  EINVAL for other values. */
+int hess_set_ffn_schedule(int edge, int whole, int parts);
+
 /*
  * hess_gated_ffn_forward -- h from x, w_gate and w_up.
  *   preact    device, n x hess_gated_ffn_preact_cols(f) of dtype (or float32,

@@ -127,3 +127,24 @@ def test_workspace_up_to_64_tokens():
     room = hs._load().hess_gated_ffn_workspace
     assert room(64, 1024, 2816, 0, 0) == 0 and room(16, 16384, 512, 0, 0) == 0
     assert room(64, 8192, 1024, 0, 0) > 0 and room(64, 8193, 1024, 0, 0) == 0
+
+
+def test_forced_schedules():
+    """The hook's checks, and the workspace of the schedule it sets."""
+    lib = hs._load()
+    for bad in ((32, 0, 1), (-64, 0, 1), (64, -1, 1), (64, 0, 0), (64, 0, 65)):
+        assert lib.hess_set_ffn_schedule(*bad) == -1
+    room = lib.hess_gated_ffn_workspace
+    natural = [room(300, 456, 152, t, b) for t in range(3) for b in (0, 1)]
+    try:
+        # 300 x 152 features: 2 x 2 tiles of 256 x 128, 5 x 5 of 64 x 32; K of 456: 15 stages in 2 bytes, 29 in 4
+        assert lib.hess_set_ffn_schedule(256, 0, 1) == 0 and room(300, 456, 152, 0, 0) == 0
+        assert lib.hess_set_ffn_schedule(256, 0, 3) == 0 and room(300, 456, 152, 0, 0) == 4 * 3 * 256 * 256 * 4
+        assert lib.hess_set_ffn_schedule(256, 1, 3) == 0 and room(300, 456, 152, 1, 0) == 3 * 3 * 256 * 256 * 4
+        assert lib.hess_set_ffn_schedule(64, 20, 4) == 0 and room(300, 456, 152, 2, 0) == 5 * 4 * 64 * 64 * 4
+        # no more parts than stages; every tile whole
+        assert lib.hess_set_ffn_schedule(64, 0, 64) == 0 and room(300, 456, 152, 0, 0) == 25 * 15 * 64 * 64 * 4
+        assert lib.hess_set_ffn_schedule(128, 99, 2) == 0 and room(300, 456, 152, 0, 0) == 0
+    finally:
+        assert lib.hess_set_ffn_schedule(0, 0, 1) == 0
+    assert natural == [room(300, 456, 152, t, b) for t in range(3) for b in (0, 1)]
