@@ -31,8 +31,10 @@ constexpr float kLog2eHalfLow = -9.62981495e-09f;
 // exp(-z^2) erfcx(z) / 2 with z = |g| / sqrt 2, and erfcx(z) a polynomial in
 // t = 1 / (1 + 0.3 z) times t, fitted here for the least relative error on
 // 0 <= z <= 14 (4e-8).  The exponent -g^2 log2(e) / 2 is formed in two parts,
-// so that the far tail is as accurate (2e-7).  |g| past 20 counts as 20, where
-// the tail is below float32's range.
+// so that the far tail is as accurate as the middle.  In float32 g times it is
+// off by up to 5.4e-7 (measured at 6 million g in [-13, 13]: 4.2e-7 below -3,
+// 5.0e-7 to -0.1, 5.4e-7 around 0, 1.3e-7 above 1).  |g| past 20 counts as 20,
+// where the tail is below float32's range.
 __device__ __forceinline__ float normal_cdf(float g, float& e) {
   const float s = fminf(fabsf(g), 20.0f);
   const float t = __builtin_amdgcn_rcpf(fmaf(0.3f * 0.70710678118654752f, s, 1.0f));

@@ -163,3 +163,18 @@ def test_tokens_where_tiles_take_over(n, d, f, dt):
     far = torch.zeros((n, d + 1), dtype=x.dtype, device="cuda")[:, :d]
     far.copy_(x)
     G.check("h, x at an odd stride", hs.gated_ffn_forward(far, w[:f], w[f:], act="gelu"), want, tol)
+
+
+def test_gelu_relative_accuracy():
+    """float32 gelu over the whole range.  In units u = 2^-24, relative: the fit 1; the hardware exponential 2; t's
+    argument 1 and reciprocal 2, times the slope of t q(t), 1 + t q' / q, which is largest at t = 1: 3.8, so 12; the
+    polynomial's eight steps, damped by t < 1, 3; the exponent's low part 1; the products e t q 2; 1 - tail 1; g times
+    it 1: 23 in all."""
+    D.say("gelu accuracy")
+    g = np.concatenate([np.linspace(-12.9, 12.9, 400001), -np.logspace(-30, 1.1, 100001), np.logspace(-30, 1.1, 100001)])
+    g = g.astype(np.float32)
+    x = torch.from_numpy(np.stack([g, np.ones_like(g)], 1)).cuda()
+    gate, up = torch.tensor([[1.0, 0.0]], device="cuda"), torch.tensor([[0.0, 1.0]], device="cuda")
+    h = hs.gated_ffn_forward(x, gate, up, act="gelu")[:, 0].double().cpu().numpy()
+    want = R.act_and_slope(g.astype(np.float64), "gelu")[0]
+    assert (np.abs(h - want) <= 23 * G.U * np.abs(want) + 2.0 ** -126).all()
