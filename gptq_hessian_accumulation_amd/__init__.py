@@ -692,7 +692,12 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
 def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
                        preact: torch.Tensor, act: str = "silu", need_x: bool = True, need_w: bool = True,
                        workspace: torch.Tensor | None = None, stream=None):
-    """``(dx, dw_gate, dw_up)`` for the gradient dh of gated_ffn_forward's h (entries not needed are None)."""
+    """``(dx, dw_gate, dw_up)`` for the gradient dh of gated_ffn_forward's h (entries not needed are None).
+
+    Sums are float32.  For 16-bit types the gradients of the two pre-activations are rounded to that type
+    before the products, which leaves the results about 1.4 times as far off as their own last rounding;
+    float32 inputs have no such rounding.
+    """
     if stream is not None:  # the call, its temporaries and its outputs belong to it
         with torch.cuda.stream(stream):
             return gated_ffn_backward(dh, x, w_gate, w_up, preact, act, need_x, need_w, workspace)

@@ -15,7 +15,7 @@
 // Longer rows take the second and the third for loss and gradient.
 //
 // Measured (a large copy reaches 4.8 TB/s, a read 5.6): 8192 x 131072 bf16,
-// loss and gradient, 0.86 ms, 5.0 TB/s; 1024 x 65537 float32, loss alone, 51
+// loss and gradient, 0.87 ms, 4.9 TB/s; 1024 x 65537 float32, loss alone, 51
 // us, 5.2 TB/s; 2047 x 50001 bf16 with a quarter of the rows masked, 93 us, 3.8
 // TB/s.  Few rows and short rows are bound by one row's chain of loads, joins
 // and float64 logarithms, about 8 us.  A second pass over the row instead of

@@ -6,8 +6,9 @@
 // any alignment; 64 consecutive bytes a row and instruction), x comes from L2
 // the same way, and the waves' sums meet in LDS before the activation.  One
 // launch, no workspace, every weight byte read once.  One bf16 token at 4096 x
-// 11264: 32.5 us, 5.7 TB/s (a large read reaches 5.6; the last-level cache
-// holds some of the weights); 24 fp16 tokens at 2560 x 9728: 31 us, 3.2 TB/s,
+// 11264: 32.9 us, 5.6 TB/s, where the last-level cache holds some of the
+// weights, and 35.2 us, 5.2 TB/s, where it holds none (a large read reaches
+// 5.6); 24 fp16 tokens at 2560 x 9728: 31 us, 3.2 TB/s,
 // where x, read again for every 32 features, costs about as much as a third of
 // the weights.
 //

@@ -1,12 +1,13 @@
-// The gated feed-forward block's products: tiles of edge 256 or 128 with
+// The gated feed-forward block's products: tiles of edge 256, 128 or 64 with
 // float32 accumulators, on v_mfma_f32_16x16x32 (bf16 or fp16) or, for float32
 // operands, v_mfma_f32_16x16x4_f32.  A stage is 64 bytes of K: 32 values of a
 // 16-bit type, 16 of float32.
 //
-//  * 8 waves of 128 x 64 (edge 256) or 4 of 64 x 64 (edge 128), one matrix
-//    instruction (float32: four) per 16 x 16 accumulator and stage.  Two
-//    waves share each SIMD (edge 128: two workgroups a CU), so that one's
-//    waits are covered by the other's matrix instructions.  The B
+//  * 8 waves of 128 x 64 (edge 256) or 4 of 64 x 64 (edge 128) or 32 x 32
+//    (edge 64, for small products), one matrix instruction (float32: four)
+//    per 16 x 16 accumulator and stage.  Two waves share each SIMD (edge 128:
+//    two workgroups a CU; edge 64: four), so that one's waits are covered by
+//    the other's matrix instructions.  The B
 //    operand goes first, so that a lane holds four consecutive columns; two
 //    neighbouring blocks are exchanged between lane rows before they are
 //    stored, which makes eight (one 16-byte store).
@@ -25,11 +26,13 @@
 //    workgroup was given lies outside the descriptor (or its chunk's offset
 //    does), and all of these read as zeros.
 //
-// Measured (bf16 unless said): forward of 16384 tokens at 4096 x 11264 2.33 ms,
-// 1.30 PFLOP/s, with the activation (a library product of the same size alone:
-// 1.44); 8192 tokens, dx 1.33 ms and dW 1.29 ms, 1.14 and 1.17 PFLOP/s (library
-// products 1.19 and 0.98); float32, 2000 x 2560 x 4000, 136 TFLOP/s of the 137
-// a large library product reaches.  16-bit products are bound by the card's
+// Measured (bf16 unless said; the card's clock, and with it every long product,
+// varies by a tenth from card to card and over the first passes): forward of
+// 16384 tokens at 4096 x 11264 2.34 to 2.43 ms, 1.24 to 1.29 PFLOP/s, with the
+// activation (a library product of the same size alone: 1.44); 8192 tokens, dx
+// 1.17 to 1.26 ms and dW 1.12 to 1.21 ms (library products 1.27 and 1.54);
+// float32, 2000 x 2560 x 4000, 136 TFLOP/s of the 137 a large library product
+// reaches.  16-bit products are bound by the card's
 // power and the meetings of the waves: the matrix cores are busy in 64% of the
 // cycles, at a clock that falls to 1.6 GHz; LDS is free of bank conflicts and
 // busy in a quarter of them.  Small products are bound by a launch's fixed 4 to

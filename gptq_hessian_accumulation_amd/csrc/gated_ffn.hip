@@ -99,8 +99,9 @@ int slots_of(int edge) { return edge == 256 ? 256 : edge == 128 ? 512 : 1024; }
 // the matrix cores; 16-bit products of edge 256 are slowed by the card's power
 // as it fills (0.50 us alone, 0.83 us on all CUs), and smaller edges reach
 // 0.7 (128) and 0.4 (64) of its rate, but divide the work more evenly over the
-// CUs: 300 tokens at 704 x 1000, bf16, take 7.7 us with edge 64, 11.6 with 128
-// and 24 with 256; 1999 at 2560 x 9728 take 400, 260 and 213.
+// CUs: 300 tokens at 704 x 1000, bf16, take 7.7 us with edge 64, 11.5 with 128
+// and 23 with 256; 1999 at 2560 x 9728 take 395, 232 and 187 (operands in the
+// last-level cache; 209 with cold ones).
 double stage_us(int edge, int groups, bool f32, int mode) {
   const int each = (groups + 255) / 256;  // on the busiest CU
   if (edge == 256) return f32 ? 3.7 : 0.50 + 0.33 * groups / 256;

@@ -558,7 +558,8 @@ int hess_imatrix_destroy(hess_imx_t m);
  *
  * Alignment: h, dh, dx and the weight gradients take any element alignment
  * and stride.  Forward calls of up to 64 tokens take any for x and the weights
- * too.  All others read x and the weights in 16-byte pieces: where a row (d
+ * too, without copies (a kernel of their own, which also takes most aligned
+ * ones).  All others read x and the weights in 16-byte pieces: where a row (d
  * elements) is a whole number of them, every row must start at 16 bytes
  * (EALIGN otherwise); where it is not, the rows are first copied to padded
  * ones in the workspace.
@@ -642,8 +643,9 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
  *             value and whether or not the row has other entries.  Repeated
  *             ids add their probabilities.
  *   values    n x k teacher logits (or log-probabilities) of values_dtype,
- *             row stride ldv; not read where the entry is absent.  A value
- *             of -infinity makes the entry absent too.
+ *             row stride ldv; ignored where the id is negative.  A value of
+ *             -infinity makes the entry absent too.  A NaN makes the row's
+ *             loss, and the gradient at its entries, NaN.
  *   weight    n floats, or NULL for ones.  A row of weight 0, or one whose
  *             entries are all absent, has loss 0 and a zero gradient whatever
  *             its logits hold.
