@@ -6,7 +6,8 @@ package makes.  ``exact`` gives the same outputs from the definitions in float64
 
 Codes, whole numbers to nearest, ties to even.  A row with a scale of its own: with a its largest magnitude,
 a value x is held as 127 x / a and stands for that times a / 127.  In blocks of 32 columns: x is held as x / s and
-stands for that times s, s the smallest power of two with a / s < 127.5 for the block's largest magnitude a.
+stands for that times s, s the power of two with 64 <= a / s < 128 for the block's largest magnitude a, and
+none past 127 in magnitude.
 """
 
 import math
@@ -132,8 +133,8 @@ def _hold(x, block):
     top = xb.abs().amax(2, keepdim=True)
     top = torch.where(top > 0.0, top, 1.0)
     part = torch.frexp(top)[0]  # top / part is a power of two, and the quotient exact
-    step = top / part * torch.where(part < 127.5 / 128.0, 1.0 / 128.0, 1.0 / 64.0)
-    q, step = torch.round(xb / step), step.expand(-1, -1, block)
+    step = top / part / 128.0
+    q, step = torch.round(xb / step).clamp(-127.0, 127.0), step.expand(-1, -1, block)
     return q.view(n, groups * block)[:, :d], step.reshape(n, groups * block)[:, :d]
 
 
@@ -233,11 +234,9 @@ def exact(case, seed):
                 continue
             part = v[:, lo:hi].reshape(n, -1, width)
             big = torch.linalg.vector_norm(part, ord=math.inf, dim=2, keepdim=True)
-            # big = 2^e (1 + m / 2^52): a step of 2^(e - 6), or twice that from 127.5 / 64 = 1.9921875 on
-            bits = big.view(torch.int64)
-            e = (bits >> 52) - 1023 + ((bits & ((1 << 52) - 1)) >= 127 << 45).long()
-            unit = ((e - 6 + 1023).clamp(min=1) << 52).view(torch.float64)
-            out[:, lo:hi] = torch.where(big > 0.0, (part / unit).round() * unit, torch.zeros_like(part)).reshape(n, -1)
+            # the power of two in big's exponent bits, less 6
+            unit = (((big.view(torch.int64) >> 52) - 6).clamp(min=1) << 52).view(torch.float64)
+            out[:, lo:hi] = torch.where(big > 0.0, (part / unit).round().clamp(-127.0, 127.0) * unit, torch.zeros_like(part)).reshape(n, -1)
         return out
 
     if case["op"] == "store":
