@@ -21,6 +21,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from typing import NamedTuple
 
 import torch
 import torch.autograd.forward_ad as _forward_ad
@@ -41,6 +42,13 @@ __all__ = [
     "distill_topk_forward",
     "distill_topk_backward",
     "distill_topk_step",
+    "Int8Rows",
+    "quantize_int8",
+    "dequantize_int8",
+    "int8_matmul",
+    "int8_linear",
+    "int8_linear_forward",
+    "int8_linear_backward",
     "set_tile_override",
     "set_ffn_schedule",
     "set_staging",
@@ -135,6 +143,16 @@ def _load():
                                       ctypes.c_float, vp, vp, vp, i64, vp, i64, vp]),
         "hess_distill_topk_backward": (c_int, [vp, vp, i64, c_int, i64, i64, vp, c_int, i64, vp, c_int, i64, c_int,
                                                vp, ctypes.c_float, vp, vp, i64, vp]),
+        "hess_gated_ffn_preact_i8_cols": (i64, [i64]),
+        "hess_int8_quantize": (c_int, [vp, i64, c_int, i64, i64, c_int, vp, i64, i64, vp, vp]),
+        "hess_int8_dequantize": (c_int, [vp, i64, vp, i64, i64, c_int, vp, i64, c_int, vp]),
+        "hess_int8_matmul_workspace": (i64, [i64, i64, i64]),
+        "hess_int8_matmul": (c_int, [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, i64, c_int, vp, i64, vp]),
+        "hess_int8_linear_workspace": (i64, [i64, i64, i64, c_int, c_int]),
+        "hess_int8_linear_forward": (c_int, [vp, i64, c_int, vp, i64, vp, i64, i64, i64, vp, i64, vp, i64, vp, vp, i64,
+                                             vp]),
+        "hess_int8_linear_backward": (c_int, [vp, i64, c_int, vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, i64, vp,
+                                              i64, vp, i64, vp]),
         "hess_imatrix_create": (vp, [i64, c_int]),
         "hess_imatrix_destroy": (c_int, [vp]),
         "hess_imatrix_add_batch": (c_int, [vp, vp, i64, i64, vp]),
@@ -561,6 +579,7 @@ def materialize_grouped(hessians, damp_percent: float = 0.01, outs=None, neutral
 
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _PREACT_F32 = 16
+_PREACT_I8 = 64
 _FEW = 64  # tokens of a forward call up to which the library takes rows of any alignment
 _CODES = {torch.bfloat16: HESS_BF16, torch.float32: HESS_F32, torch.float16: HESS_F16}
 
@@ -661,26 +680,32 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     With ``save`` returns ``(h, preact)``, preact being what gated_ffn_backward needs: the
     (tokens, 2 f') pair of pre-activations, f' = f rounded up to a multiple of 8, in float32
     (``save=True``) or in the dtype given: float32 or x's, which takes half the memory and leaves
-    16-bit gradients about 1.3 times as far off.
+    16-bit gradients about 1.3 times as far off.  ``save=torch.int8`` keeps an 8-bit checkpoint, a
+    quarter of the memory: codes in blocks of 32 features with a step each, as quantize_int8 with
+    ``block=32`` makes them, in one int8 tensor (h of up to 64 tokens may then differ in its last bit).
     """
     if stream is not None:  # the call, its temporaries and its outputs belong to it
         with torch.cuda.stream(stream):
             return gated_ffn_forward(x, w_gate, w_up, act, save, out, workspace)
     lib = _load()
     mode = _act_mode(act)
-    code, n, d, f, keep, ins = _ffn_args(x, w_gate, w_up, _FEW)
+    in8 = save is torch.int8
+    code, n, d, f, keep, ins = _ffn_args(x, w_gate, w_up, 0 if in8 else _FEW)
     h = _out("out", out, (*x.shape[:-1], f), x)
     pre = None
-    if save:
+    if in8:
+        pre = x.new_empty((n, lib.hess_gated_ffn_preact_i8_cols(f)), dtype=torch.int8)
+        mode |= _PREACT_I8
+    elif save:
         kept = torch.float32 if save is True else save
         if kept not in (torch.float32, x.dtype):
-            raise ValueError(f"save must be a bool, torch.float32 or the dtype of x, not {save}")
+            raise ValueError(f"save must be a bool, torch.float32, torch.int8 or the dtype of x, not {save}")
         pre = x.new_empty((n, 2 * (-(-f // 8) * 8)), dtype=kept)
         if kept == torch.float32:
             mode |= _PREACT_F32
     if n > 0:
         ldh = h.stride(0) if out is not None and h.dim() == 2 and n > 1 else f
-        need = lib.hess_gated_ffn_workspace(n, d, f, code, 0)
+        need = lib.hess_gated_ffn_workspace(n, d, f, code, 2 if in8 else 0)
         wp, wb, work = _workspace(workspace, need, x) if need else (None, 0, None)
         rc = lib.hess_gated_ffn_forward(*ins, code, mode, n, d, f, h.data_ptr(), ldh,
                                         pre.data_ptr() if save else None, wp, wb, _stream(None, x.get_device()))
@@ -696,21 +721,37 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
 
     Sums are float32.  For 16-bit types the gradients of the two pre-activations are rounded to that type
     before the products, which leaves the results about 1.4 times as far off as their own last rounding;
-    float32 inputs have no such rounding.
+    float32 inputs have no such rounding.  ``preact`` from ``save=torch.int8`` gives the derivatives at
+    what its codes stand for.  ``x`` may be an 8-bit checkpoint too (Int8Rows, from quantize_int8), which
+    dw_gate and dw_up then take, or None where they are not needed.
     """
     if stream is not None:  # the call, its temporaries and its outputs belong to it
         with torch.cuda.stream(stream):
             return gated_ffn_backward(dh, x, w_gate, w_up, preact, act, need_x, need_w, workspace)
     lib = _load()
     mode = _act_mode(act)
-    code, n, d, f, keep, (xp, ldx, gp, ldg, up, ldu) = _ffn_args(x, w_gate, w_up)
+    if isinstance(x, Int8Rows):
+        _int8_args("x", x)
+        if tuple(x.codes.shape) != (*dh.shape[:-1], w_gate.shape[-1]):
+            raise ValueError(f"x must hold {(*dh.shape[:-1], w_gate.shape[-1])} codes")
+        x = dequantize_int8(x, dtype=dh.dtype) if need_w else None
+    elif x is None and need_w:
+        raise ValueError("dw_gate and dw_up need x")
+    if x is None:  # only its shape matters
+        code, n, d, f, keep, (_, _, gp, ldg, up, ldu) = _ffn_args(dh.new_empty((0, w_gate.shape[-1])), w_gate, w_up)
+        x, xp, ldx, n = dh.new_empty(1).expand(*dh.shape[:-1], d), None, d, dh.shape[:-1].numel()
+    else:
+        code, n, d, f, keep, (xp, ldx, gp, ldg, up, ldu) = _ffn_args(x, w_gate, w_up)
     if tuple(dh.shape) != (*x.shape[:-1], f) or dh.dtype != x.dtype or dh.device != x.device:
         raise ValueError(f"dh must be a {x.dtype} {(*x.shape[:-1], f)} tensor on {x.device}")
-    cols = 2 * (-(-f // 8) * 8)
-    if tuple(preact.shape) != (n, cols) or preact.dtype not in (torch.float32, x.dtype) \
+    in8 = preact.dtype == torch.int8
+    cols = lib.hess_gated_ffn_preact_i8_cols(f) if in8 else 2 * (-(-f // 8) * 8)
+    if tuple(preact.shape) != (n, cols) or not (in8 or preact.dtype in (torch.float32, x.dtype)) \
             or preact.device != x.device or not preact.is_contiguous():
         raise ValueError(f"preact must be the contiguous ({n}, {cols}) tensor gated_ffn_forward saved")
-    if preact.dtype == torch.float32:
+    if in8:
+        mode |= _PREACT_I8
+    elif preact.dtype == torch.float32:
         mode |= _PREACT_F32
     dh2, dhp, lddh = _rows(dh.reshape(-1, f) if dh.dim() != 2 else dh)
     dx = x.new_empty(x.shape) if need_x else None
@@ -740,15 +781,23 @@ class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, act, save):
         h, preact = gated_ffn_forward(x, w_gate, w_up, act=act, save=save)
-        ctx.save_for_backward(x, w_gate, w_up, preact)
-        ctx.act = act
+        ctx.act, ctx.block = act, None
+        if save is torch.int8:
+            need = ctx.needs_input_grad
+            kept = quantize_int8(x, block=32) if need[1] or need[2] else Int8Rows(None, None, 32)
+            ctx.block = 32
+            ctx.save_for_backward(kept.codes, w_gate, w_up, preact, kept.scale)
+        else:
+            ctx.save_for_backward(x, w_gate, w_up, preact)
         return h
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh):
-        x, w_gate, w_up, preact = ctx.saved_tensors
+        x, w_gate, w_up, preact, *scale = ctx.saved_tensors
         need = ctx.needs_input_grad
+        if ctx.block is not None and x is not None:
+            x = Int8Rows(x, scale[0], ctx.block)
         dx, dwg, dwu = gated_ffn_backward(dh, x, w_gate, w_up, preact, act=ctx.act, need_x=need[0],
                                           need_w=need[1] or need[2])
         return dx, (dwg if need[1] else None), (dwu if need[2] else None), None, None
@@ -758,7 +807,9 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: st
               save: bool | torch.dtype = True) -> torch.Tensor:
     """gated_ffn_forward under autograd: the backward pass is gated_ffn_backward (once differentiable).
 
-    ``save``: in which type the pre-activations are kept for it, as for gated_ffn_forward.  Reverse mode
+    ``save``: in which type the pre-activations are kept for it, as for gated_ffn_forward; with torch.int8
+    x is kept in 8 bits too (in blocks of 32 columns), and not at all where no weight needs a gradient:
+    the gradients are those at the values so held.  Reverse mode
     only: dual tensors of forward mode raise NotImplementedError.
     """
     _refuse_forward_mode("gated_ffn", x, w_gate, w_up)
@@ -911,3 +962,255 @@ def distill_topk(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, 
         if logits.requires_grad:
             return _DistillTopk.apply(logits, ids, values, weight, float(temperature))
     return distill_topk_forward(logits, ids, values, weight=weight, temperature=temperature)[0]
+
+
+# -- 8-bit integers: rows as codes with scales, their product, a linear layer ---------------------
+
+_E8 = torch.float8_e8m0fnu  # powers of two by their exponent byte, as the library's block 32 has them
+
+
+class Int8Rows(NamedTuple):
+    """Rows held as int8 ``codes`` (..., d) with their ``scale``: float32 (...) for ``block`` 0 (one a row),
+    or for ``block`` 32 powers of two, torch.float8_e8m0fnu (..., ceil(d / 32)), for each 32 columns."""
+
+    codes: torch.Tensor
+    scale: torch.Tensor
+    block: int = 0
+
+
+def _int8_args(name: str, rows: Int8Rows, block=None):
+    """(tensors to keep, leading shape, n, d, code pointer, row stride, scale pointer) of checked rows."""
+    codes, scale, b = rows
+    index = codes.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be on the GPU")
+    if index != _current_device():
+        raise ValueError(f"{name} is on {codes.device}, not on the current device")
+    if codes.dtype != torch.int8:
+        raise TypeError(f"codes of {name} must be int8, not {codes.dtype}")
+    if b != 0 and b != 32:
+        raise ValueError(f"block of {name} must be 0 or 32, not {b}")
+    if block is not None and b != block:
+        raise ValueError(f"{name} must have a scale a row (block 0)")
+    shape = codes.shape
+    if len(shape) < 1:
+        raise ValueError(f"codes of {name} must be (..., d)")
+    lead, d = shape[:-1], shape[-1]
+    if scale.dtype != (torch.float32 if b == 0 else _E8) or scale.get_device() != index \
+            or scale.shape != (lead if b == 0 else (*lead, -(-d // 32))):
+        raise ValueError(f"scale of {name} must be a {'float32' if b == 0 else 'float8_e8m0fnu'} "
+                         f"{tuple(lead) if b == 0 else (*lead, -(-d // 32))} tensor on {codes.device}")
+    if not scale.is_contiguous():
+        scale = scale.contiguous()
+    c2, cp, ldc = _rows(codes if len(shape) == 2 else codes.reshape(-1, d))
+    return (c2, scale), lead, c2.shape[0], d, cp, ldc, scale.data_ptr()
+
+
+def _new_codes(lead, d: int, like: torch.Tensor):
+    """(codes, row stride): int8 (*lead, d), rows of a multiple of 16 bytes apart."""
+    pad = -(-d // 16) * 16
+    codes = like.new_empty((*lead, pad), dtype=torch.int8)
+    return (codes if pad == d else codes[..., :d]), pad
+
+
+def quantize_int8(x: torch.Tensor, block: int = 0, stream=None) -> Int8Rows:
+    """x (..., d) bfloat16, float16 or float32 as 8-bit codes; not recorded by autograd.
+
+    ``block=0``: a scale a row, max |x| / 127, and codes rint(127 x / max |x|): the operands of
+    int8_matmul, tokens or a weight's output channels.  ``block=32``: a power of two for each 32
+    columns, s with 64 <= max |x| / s < 128: checkpoints of activations (33 / 32 bytes a value; half a
+    step off, at most 1 / 128 of the block's largest magnitude, and less than a step past 127.5 of them).  A row (block) with an infinity or NaN
+    stands for NaN.
+    """
+    if stream is not None:  # the call, its temporaries and its outputs belong to it
+        with torch.cuda.stream(stream):
+            return quantize_int8(x, block)
+    lib = _load()
+    code = _float_code("x", x)
+    if block != 0 and block != 32:
+        raise ValueError(f"block must be 0 or 32, not {block}")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be (..., d) with d >= 1")
+    lead, d = x.shape[:-1], x.shape[-1]
+    x2, xp, ldx = _rows(x if x.dim() == 2 else x.reshape(-1, d))
+    codes, pad = _new_codes(lead, d, x)
+    scale = x.new_empty(lead, dtype=torch.float32) if block == 0 else x.new_empty((*lead, -(-d // 32)), dtype=_E8)
+    rc = lib.hess_int8_quantize(xp, ldx, code, x2.shape[0], d, block, codes.data_ptr(), pad, pad, scale.data_ptr(),
+                                _stream(None, x.get_device()))
+    if rc != 0:
+        _check(rc)
+    return Int8Rows(codes, scale, block)
+
+
+def dequantize_int8(rows: Int8Rows, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """What the codes stand for, rounded once to ``dtype`` (exact in bfloat16 and float32 for block 32)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dequantize_int8(rows, dtype, out)
+    lib = _load()
+    keep, lead, n, d, cp, ldc, sp = _int8_args("rows", rows)
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; use torch.bfloat16, torch.float16 or torch.float32")
+    x = _out("out", out, (*lead, d), keep[0].new_empty(0, dtype=dtype)) if out is not None \
+        else keep[0].new_empty((*lead, d), dtype=dtype)
+    ldx = x.stride(0) if x.dim() == 2 and n > 1 else d
+    rc = lib.hess_int8_dequantize(cp, ldc, sp, n, d, rows.block, x.data_ptr(), ldx, code,
+                                  _stream(None, x.get_device()))
+    if rc != 0:
+        _check(rc)
+    return x
+
+
+def int8_matmul(a: Int8Rows, b: Int8Rows, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``y = a b^T`` (..., f) of dtype for rows of codes a (..., d) and b (f, d) with a scale a row.
+
+    Sums are int32 and exact (d < 2^17); not recorded by autograd.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return int8_matmul(a, b, dtype, out, workspace)
+    lib = _load()
+    keep, lead, n, d, ap, lda, asp = _int8_args("a", a, 0)
+    keep_b, lead_b, f, db, bp, ldb, bsp = _int8_args("b", b, 0)
+    if len(lead_b) != 1 or db != d:
+        raise ValueError(f"b must hold (f, {d}) codes, not {tuple(b.codes.shape)}")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; use torch.bfloat16, torch.float16 or torch.float32")
+    like = keep[0].new_empty(0, dtype=dtype)
+    y = _out("out", out, (*lead, f), like)
+    ldy = y.stride(0) if out is not None and y.dim() == 2 and n > 1 else f
+    wp, wb, work = _workspace(workspace, lib.hess_int8_matmul_workspace(n, d, f), like)
+    rc = lib.hess_int8_matmul(ap, lda, asp, bp, ldb, bsp, n, d, f, y.data_ptr(), ldy, code, wp, wb,
+                              _stream(None, like.get_device()))
+    if rc != 0:
+        _check(rc)
+    return y
+
+
+def int8_linear_forward(x: torch.Tensor, w: Int8Rows, save: bool = False, out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """``y = xq w^T`` (..., f) of x's dtype: x (..., d) as quantize_int8 holds its rows, times weights held as codes
+    (f, d) with a scale for each output channel; not recorded by autograd.
+
+    ``w``: quantize_int8 of a float weight, or what gptq_quantize left with whole rows
+    (``Int8Rows((codes.to(torch.int8) - 8), scales[:, 0])``).  With ``save`` returns ``(y, xq)``, the 8-bit
+    checkpoint that int8_linear_backward takes.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return int8_linear_forward(x, w, save, out, workspace)
+    lib = _load()
+    code = _float_code("x", x)
+    keep, lead_w, f, d, wp8, ldw, wsp = _int8_args("w", w, 0)
+    if len(lead_w) != 1 or x.dim() < 1 or x.shape[-1] != d:
+        raise ValueError(f"w must hold (f, d) codes and x be (..., d), not {tuple(w.codes.shape)} and {tuple(x.shape)}")
+    lead = x.shape[:-1]
+    x2, xp, ldx = _rows(x if len(lead) == 1 else x.reshape(-1, d))
+    n = x2.shape[0]
+    y = _out("out", out, (*lead, f), x)
+    ldy = y.stride(0) if out is not None and y.dim() == 2 and n > 1 else f
+    codes = scale = None
+    ldc = 0
+    if save:
+        codes, ldc = _new_codes(lead, d, x)
+        scale = x.new_empty(lead, dtype=torch.float32)
+    wp, wb, work = _workspace(workspace, lib.hess_int8_linear_workspace(n, d, f, code, 0), x)
+    rc = lib.hess_int8_linear_forward(xp, ldx, code, wp8, ldw, wsp, n, d, f, y.data_ptr(), ldy,
+                                      codes.data_ptr() if save and n > 0 else None, ldc,
+                                      scale.data_ptr() if save and n > 0 else None, wp, wb,
+                                      _stream(None, x.get_device()))
+    if rc != 0:
+        _check(rc)
+    return (y, Int8Rows(codes, scale)) if save else y
+
+
+def int8_linear_backward(dy: torch.Tensor, x: Int8Rows | None, w: Int8Rows | None, need_x: bool = True,
+                         need_w: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """``(dx, dw)`` for the gradient dy (..., f) of int8_linear_forward's y, straight through the rounding:
+    dx = dy wq, dw = dy^T xq (entries not needed are None), of dy's dtype.
+
+    ``x``: the checkpoint that the forward call saved (None if dw is not needed); ``w``: its weights (None
+    if dx is not needed).  For 16-bit types xq and wq are rounded to that type before the products, which
+    leaves the results about 1.4 times as far off as their own last rounding; sums are float32.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return int8_linear_backward(dy, x, w, need_x, need_w, workspace)
+    lib = _load()
+    code = _float_code("dy", dy)
+    if dy.dim() < 1 or (need_x and w is None) or (need_w and x is None):
+        raise ValueError("dy must be (..., f); dx needs w and dw needs x")
+    if x is None and w is None:
+        return None, None
+    lead, f = dy.shape[:-1], dy.shape[-1]
+    d = (w if x is None else x).codes.shape[-1]
+    cp = ldc = sp = wp8 = ldw = wsp = None
+    if need_w:
+        keep_x, lead_x, _, dx_, cp, ldc, sp = _int8_args("x", x, 0)
+        if lead_x != lead or dx_ != d:
+            raise ValueError(f"x must hold {(*lead, d)} codes, not {tuple(x.codes.shape)}")
+    if need_x:
+        keep_w, lead_w, fw, dw_, wp8, ldw, wsp = _int8_args("w", w, 0)
+        if len(lead_w) != 1 or fw != f or dw_ != d:
+            raise ValueError(f"w must hold {(f, d)} codes, not {tuple(w.codes.shape)}")
+    if not need_x and not need_w:
+        return None, None
+    step = 4 if code == HESS_F32 else 8
+    dy2, dyp, lddy = _rows(dy if len(lead) == 1 else dy.reshape(-1, f), step if f % step == 0 else 1)
+    n = dy2.shape[0]
+    dx = dy.new_empty((*lead, d)) if need_x else None
+    dw = dy.new_empty((f, d)) if need_w else None
+    need = lib.hess_int8_linear_workspace(n, d, f, code, (1 if need_x else 0) + (2 if need_w else 0))
+    wp, wb, work = _workspace(workspace, need, dy)
+    rc = lib.hess_int8_linear_backward(dyp, lddy, code, cp, ldc or 0, sp, wp8, ldw or 0, wsp, n, d, f,
+                                       dx.data_ptr() if need_x and n > 0 else None, d,
+                                       dw.data_ptr() if need_w else None, d, wp, wb, _stream(None, dy.get_device()))
+    if rc != 0:
+        _check(rc)
+    return dx, dw
+
+
+class _Int8Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, codes, scale):
+        w = Int8Rows(codes, scale) if weight is None else quantize_int8(weight)
+        need = ctx.needs_input_grad
+        y, kept = int8_linear_forward(x, w, save=True) if need[1] else (int8_linear_forward(x, w), Int8Rows(None, None))
+        # (each side only where a gradient will read it)
+        ctx.save_for_backward(kept.codes, kept.scale, *((w.codes, w.scale) if need[0] else (None, None)))
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        xc, xs, wc, ws = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw = int8_linear_backward(dy, Int8Rows(xc, xs) if need[1] else None, Int8Rows(wc, ws) if need[0] else None,
+                                      need_x=need[0], need_w=need[1])
+        return dx, dw, None, None
+
+
+def int8_linear(x: torch.Tensor, w: torch.Tensor | Int8Rows) -> torch.Tensor:
+    """A linear layer that computes in 8-bit integers, under autograd: int8_linear_forward and int8_linear_backward.
+
+    ``w``: Int8Rows, weights already quantized, which take no gradient; or a float (f, d) tensor of x's dtype,
+    quantized by output channel in every call, with a gradient straight through the rounding.  What is kept for
+    the backward pass is in 8 bits.  Once differentiable, reverse mode only.
+    """
+    if isinstance(w, Int8Rows):
+        _refuse_forward_mode("int8_linear", x, w.scale)
+        if w.scale.requires_grad:
+            raise ValueError("the scales are constants of the layer: detach them")
+        if torch.is_grad_enabled() and x.requires_grad:
+            return _Int8Linear.apply(x, None, w.codes, w.scale)
+        return int8_linear_forward(x, w)
+    _refuse_forward_mode("int8_linear", x, w)
+    if w.dim() != 2 or w.dtype != x.dtype or w.get_device() != x.get_device():
+        raise ValueError("w must be Int8Rows, or an (f, d) tensor of x's dtype and device")
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+        return _Int8Linear.apply(x, w, None, None)
+    return int8_linear_forward(x, quantize_int8(w))

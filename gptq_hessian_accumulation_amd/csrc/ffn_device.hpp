@@ -5,6 +5,7 @@
 #include "elem.hpp"
 #include "ffn_internal.hpp"
 #include "hess_device.hpp"
+#include "int8_device.hpp"
 #include "../../include/hess.h"
 
 namespace hess {
@@ -145,6 +146,41 @@ __device__ __forceinline__ void put_preact(const FfnGemm& P, int64_t r, int64_t 
   }
 }
 
+// Features c .. c + N - 1 of row r of the pair as 8-bit codes; top: the bits of
+// the largest magnitudes in the blocks of 32 that c lies in.  One lane of each
+// block passes `first`.
+template <int N>
+__device__ __forceinline__ void put_pair8(const FfnGemm& P, int64_t r, int64_t c, const float (&g)[N],
+                                          const float (&u)[N], uint32_t top_g, uint32_t top_u, bool first) {
+  const int64_t fq = (P.f + 31) / 32 * 32;
+  if (r >= P.M || c >= fq) return;
+  char* row = static_cast<char*>(P.o1) + r * P.ldo1;
+  const uint32_t bg = block_exponent(top_g), bu = block_exponent(top_u);
+  const float ig = block_inverse(bg), iu = block_inverse(bu);
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    *reinterpret_cast<uint32_t*>(row + c + j) =
+        pack4(block_code(g[j], ig), block_code(g[j + 1], ig), block_code(g[j + 2], ig), block_code(g[j + 3], ig));
+    *reinterpret_cast<uint32_t*>(row + fq + c + j) =
+        pack4(block_code(u[j], iu), block_code(u[j + 1], iu), block_code(u[j + 2], iu), block_code(u[j + 3], iu));
+  }
+  if (first) {
+    row[2 * fq + c / 32] = (char)bg;
+    row[2 * fq + fq / 32 + c / 32] = (char)bu;
+  }
+}
+// Columns past f are zeros (absent weight rows read as zeros, but times an
+// infinite x they are none).
+template <int N> __device__ __forceinline__ uint32_t top_inside(const FfnGemm& P, int64_t c, float (&v)[N]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    v[j] = c + j < P.f ? v[j] : 0.0f;
+    m = max(m, abs_bits(v[j]));
+  }
+  return m;
+}
+
 // Outputs of row r, features c .. c + N - 1 of the forward pass.
 template <int DT, int N>
 __device__ __forceinline__ void put_fwd(const FfnGemm& P, int64_t r, int64_t c, const float (&g)[N],
@@ -155,7 +191,7 @@ __device__ __forceinline__ void put_fwd(const FfnGemm& P, int64_t r, int64_t c, 
 #pragma unroll
   for (int j = 0; j < N; ++j) h[j] = act_value<DT == kInF32>(g[j], P.act) * u[j];
   if (c < P.N) store_n(static_cast<T*>(P.o0) + r * P.ldo0 + c, h, (int)min((int64_t)N, P.N - c));
-  if (!P.o1) return;
+  if (!P.o1 || P.pre8) return;
   // columns f .. fp - 1 are zeros: absent weight rows read as zeros, but times
   // an infinite x they are none
   float gz[N], uz[N];

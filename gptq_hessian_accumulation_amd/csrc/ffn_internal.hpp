@@ -9,7 +9,7 @@ namespace hess {
 
 enum FfnMode {
   kFfnFwd = 0,  // h = act(x Wg^T) * (x Wu^T)          M = n, N = f (half a tile's columns each), K = d
-  kFfnDx = 1,   // dx = dg Wg + du Wu                   M = n, N = d, K = f, two segments
+  kFfnDx = 1,   // dx = dg Wg + du Wu                   M = n, N = d, K = f, two segments (or one: dy W)
   kFfnDw = 2,   // [dWg; dWu] = [dg du]^T x             M = 2 fp, N = d, K = n
 };
 
@@ -32,6 +32,8 @@ struct FfnGemm {
   int64_t f, fp;
   int act;
   int pre32;       // fwd: o1 is float32 whatever the type
+  int pre8;        // fwd: o1 is the pair as int8 codes in blocks of 32 (see pair8_cols)
+  int segs;        // dx: segments of K
   // schedule: tiles 0 .. full - 1 of the blocked order are done whole; each of
   // the others is cut into `parts` ranges of part_len K-iterations, whose
   // partial sums go to workspace slot part * (ntiles - full) + (tile - full)
@@ -86,8 +88,19 @@ struct PackRows {
 };
 hipError_t launch_pack_rows16(const PackRows& p, hipStream_t stream);
 
+// The pair in 8 bits: rows of pair8_cols(f) bytes, fq = f rounded up to 32: the
+// codes of g in the first fq, those of u in the next, then an exponent byte for
+// each block of 32 of g and of u.
+inline int64_t pair8_cols(int64_t f) {
+  const int64_t fq = (f + 31) / 32 * 32;
+  return (2 * fq + fq / 16 + 15) / 16 * 16;
+}
+
+// In what type the pair is kept.
+enum PairType { kPairSame = 0, kPairF32 = 1, kPairI8 = 2 };
+
 // dg = dh u act'(g), du = dh act(g) into the n x 2 fp pair dgu (columns past f zero).
-hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, bool pre32, void* dgu, int64_t n,
+hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, PairType pair, void* dgu, int64_t n,
                           int64_t f, int64_t fp, int act, int dtype, hipStream_t stream);
 
 // Zeros rows x cols elements of esize bytes at p (row stride ld elements).

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) f
   tile_coords<Mode>(P, t, I, J);
   const int64_t i0 = (int64_t)I * Edge;
   const int64_t j0 = (int64_t)J * (Mode == kFfnFwd ? Edge / 2 : Edge);
-  const int per_seg = Mode == kFfnDx ? P.niter / 2 : P.niter;
+  const int per_seg = Mode == kFfnDx ? P.niter / P.segs : P.niter;
   const int64_t rowA = P.lda * kSize, rowB = P.ldb0 * kSize;
 
   // Offsets of this wave's loads.  Along K: load i holds 16 rows, lane l row
@@ -306,15 +306,36 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) f
       }
     };
     // features of one row, forward
-    auto put_features = [&](int64_t r, int64_t col, const float (&g)[8], const float (&u)[8]) {
+    auto put_features = [&](int64_t r, int64_t col, float (&g)[8], float (&u)[8]) {
       if constexpr (In) {
         float h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = act_value<DT == kInF32>(g[e], P.act) * u[e];
         store_n(static_cast<T*>(P.o0) + r * P.ldo0 + col, h, 8);
-        if (P.o1) put_preact<T>(P, r, col, g, u);
+        if (P.o1 && !P.pre8) put_preact<T>(P, r, col, g, u);
       } else {
         put_fwd<DT>(P, r, col, g, u);
+      }
+      if (P.pre8) {
+        // a block's 32 features are in the four lanes of one row (edge 64: in
+        // two of this wave and two of the next, which meet in LDS)
+        uint32_t tg = top_inside(P, col, g), tu = top_inside(P, col, u);
+        tg = max(tg, (uint32_t)__shfl_xor((int)tg, 32));
+        tu = max(tu, (uint32_t)__shfl_xor((int)tu, 32));
+        if constexpr (Edge == 64) {
+          uint2* tops = reinterpret_cast<uint2*>(lds);
+          const int at = (int)(r - i0);
+          __syncthreads();  // (nobody reads the stages any more)
+          tops[wc * Edge + at] = uint2{tg, tu};
+          __syncthreads();
+          const uint2 o = tops[(wc ^ 1) * Edge + at];
+          tg = max(tg, o.x);
+          tu = max(tu, o.y);
+        } else {
+          tg = max(tg, (uint32_t)__shfl_xor((int)tg, 16));
+          tu = max(tu, (uint32_t)__shfl_xor((int)tu, 16));
+        }
+        put_pair8(P, r, col, g, u, tg, tu, (col & 31) == 0);
       }
     };
     if constexpr (Mode == kFfnFwd && kBn == 2) {
@@ -383,7 +404,18 @@ template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn
       g[0] += a.x, g[1] += a.y, g[2] += a.z, g[3] += a.w;
       u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
     }
-    put_fwd<DT>(P, (int64_t)I * Edge + row, (int64_t)J * (Edge / 2) + w * (cols / 2) + 4 * q, g, u);
+    const int64_t r = (int64_t)I * Edge + row, c = (int64_t)J * (Edge / 2) + w * (cols / 2) + 4 * q;
+    put_fwd<DT>(P, r, c, g, u);
+    if (P.pre8) {
+      // eight neighbouring lanes hold a block's 32 features
+      uint32_t tg = top_inside(P, c, g), tu = top_inside(P, c, u);
+#pragma unroll
+      for (int o = 1; o < 8; o *= 2) {
+        tg = max(tg, (uint32_t)__shfl_xor((int)tg, o));
+        tu = max(tu, (uint32_t)__shfl_xor((int)tu, o));
+      }
+      put_pair8(P, r, c, g, u, tg, tu, (c & 31) == 0);
+    }
   } else {
     float v[4] = {};
     for (int p = 0; p < P.parts; ++p) {

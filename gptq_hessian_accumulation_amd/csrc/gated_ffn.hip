@@ -66,6 +66,43 @@ __global__ void __launch_bounds__(256) ffn_dgu(const typename Elem<DT>::type* dh
   *reinterpret_cast<T8*>(o + fp) = du;
 }
 
+// The same from the pair in 8 bits (rows of pair8_cols(f) bytes).
+template <int DT>
+__global__ void __launch_bounds__(256) ffn_dgu8(const typename Elem<DT>::type* dh, int64_t lddh, const char* pre,
+                                                int64_t ldp, typename Elem<DT>::type* out, int64_t f, int64_t fp,
+                                                int act) {
+  typedef typename Elem<DT>::type T;
+  typedef T T8 __attribute__((ext_vector_type(8)));
+  typedef T8 T8u __attribute__((aligned(sizeof(T))));
+  const int64_t row = blockIdx.y;
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (c >= fp) return;
+  const int64_t fq = (f + 31) / 32 * 32;
+  const char* q = pre + row * ldp;
+  const uint2 g8 = *reinterpret_cast<const uint2*>(q + c), u8 = *reinterpret_cast<const uint2*>(q + fq + c);
+  const float sg = block_step((uint8_t)q[2 * fq + c / 32]), su = block_step((uint8_t)q[2 * fq + fq / 32 + c / 32]);
+  T8 h8;
+  const T* hp = dh + row * lddh + c;
+  if (c + 8 <= f) {
+    h8 = *reinterpret_cast<const T8u*>(hp);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h8[j] = c + j < f ? hp[j] : (T)0.0f;
+  }
+  T8 dg, du;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float a, da;
+    act_both<DT == kInF32>(unpack(j < 4 ? g8.x : g8.y, j & 3) * sg, act, a, da);
+    const float h = to_f32(h8[j]);
+    dg[j] = c + j < f ? from_f32<T>(h * (unpack(j < 4 ? u8.x : u8.y, j & 3) * su) * da) : (T)0.0f;
+    du[j] = c + j < f ? from_f32<T>(h * a) : (T)0.0f;
+  }
+  T* o = out + row * 2 * fp + c;
+  *reinterpret_cast<T8*>(o) = dg;
+  *reinterpret_cast<T8*>(o + fp) = du;
+}
+
 template <class T> __global__ void __launch_bounds__(256) zero_rows(T* p, int64_t ld, int64_t cols, int64_t total) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256)
     p[i / cols * ld + i % cols] = T(0);
@@ -82,6 +119,21 @@ hipError_t launch_dgu(const void* dh, int64_t lddh, const void* preact, void* dg
     ffn_dgu<DT, PT><<<dim3(gx, rows), 256, 0, stream>>>(static_cast<const T*>(dh) + r0 * lddh, lddh,
                                                         static_cast<const PT*>(preact) + r0 * 2 * fp,
                                                         static_cast<T*>(dgu) + r0 * 2 * fp, f, fp, act);
+  }
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_dgu8(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f, int64_t fp,
+                       int act, hipStream_t stream) {
+  typedef typename Elem<DT>::type T;
+  const unsigned gx = (unsigned)((fp / 8 + 255) / 256);
+  const int64_t ldp = pair8_cols(f);
+  for (int64_t r0 = 0; r0 < n; r0 += 65535) {
+    const unsigned rows = (unsigned)std::min<int64_t>(65535, n - r0);
+    ffn_dgu8<DT><<<dim3(gx, rows), 256, 0, stream>>>(static_cast<const T*>(dh) + r0 * lddh, lddh,
+                                                     static_cast<const char*>(preact) + r0 * ldp, ldp,
+                                                     static_cast<T*>(dgu) + r0 * 2 * fp, f, fp, act);
   }
   return hipGetLastError();
 }
@@ -117,7 +169,7 @@ double schedule_for(FfnGemm& g, int mode, int edge, bool f32) {
   g.tn = (int)((g.N + cols - 1) / cols);
   g.ntiles = g.tm * g.tn;
   const int per_seg = (int)((g.K + step - 1) / step);
-  g.niter = mode == kFfnDx ? 2 * per_seg : per_seg;
+  g.niter = mode == kFfnDx ? g.segs * per_seg : per_seg;
   g.full = g.ntiles;
   g.parts = 1;
   g.part_len = g.niter;
@@ -178,8 +230,14 @@ int ffn_schedule(FfnGemm& g, int mode, int dtype) {
   return edge;
 }
 
-hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, bool pre32, void* dgu, int64_t n,
+hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, PairType pair, void* dgu, int64_t n,
                           int64_t f, int64_t fp, int act, int dtype, hipStream_t stream) {
+  if (pair == kPairI8) {
+    if (dtype == kInF32) return launch_dgu8<kInF32>(dh, lddh, preact, dgu, n, f, fp, act, stream);
+    if (dtype == kInBF16) return launch_dgu8<kInBF16>(dh, lddh, preact, dgu, n, f, fp, act, stream);
+    return launch_dgu8<kInF16>(dh, lddh, preact, dgu, n, f, fp, act, stream);
+  }
+  const bool pre32 = pair == kPairF32;
   if (dtype == kInF32) return launch_dgu<kInF32, float>(dh, lddh, preact, dgu, n, f, fp, act, stream);
   if (dtype == kInBF16)
     return pre32 ? launch_dgu<kInBF16, float>(dh, lddh, preact, dgu, n, f, fp, act, stream)

@@ -1,0 +1,259 @@
+// C ABI of the 8-bit integer operators (declared in include/hess.h): argument
+// checks, workspace layout, dispatch.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/hess.h"
+#include "ffn_internal.hpp"
+#include "hess_internal.hpp"
+#include "int8_internal.hpp"
+#include "ops_checks.hpp"
+
+using namespace hess;
+
+namespace {
+
+int check_codes(const char* name, const void* p, int64_t ld, int64_t cols) { return check_mat({name, p, ld, 0, cols}, 1); }
+
+int check_scale(const char* name, const void* p) {
+  if (!p) return fail(HESS_EINVAL, "null %s", name);
+  if (!aligned(p, 4)) return fail(HESS_EALIGN, "%s not float-aligned", name);
+  return HESS_OK;
+}
+
+// Checks of a set of rows held as codes; bytes of its scales.
+int check_rows(int64_t n, int64_t d, int block, int dtype, const void* x, int64_t ldx, const void* codes, int64_t ldc,
+               const void* scale, const char* values) {
+  if (int rc = check_ffn_sizes(n, d, 1, dtype)) return rc;
+  if (block != 0 && block != 32) return fail(HESS_EINVAL, "block %d is neither 0 nor 32", block);
+  if (n == 0) return HESS_OK;
+  if (int rc = check_mat({values, x, ldx, n, d}, elem_bytes(dtype))) return rc;
+  if (int rc = check_codes("codes", codes, ldc, d)) return rc;
+  if (block == 0) return check_scale("scale", scale);
+  return scale ? HESS_OK : fail(HESS_EINVAL, "null scale");
+}
+int64_t scale_bytes(int64_t n, int64_t d, int block) { return block == 0 ? 4 * n : n * ((d + 31) / 32); }
+
+int check_product(int64_t n, int64_t d, int64_t f, int dtype) {
+  if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
+  // (int32 sums of products of up to 2^14)
+  return d < kMaxWidth ? HESS_OK : fail(HESS_EINVAL, "d = %lld: sums of 2^17 products pass 32 bits", (long long)d);
+}
+
+// Codes as the product's tiles take them: rows of a multiple of 16 bytes.
+int64_t code_stride(int64_t d) { return up(d, 16); }
+
+// Forward workspace of a linear layer: codes and scales of x.
+struct LinearWork {
+  int64_t scale, total;
+};
+LinearWork linear_work(int64_t n, int64_t d) {
+  LinearWork w{};
+  w.scale = up(n * code_stride(d), 256);
+  w.total = w.scale + up(4 * n, 256);
+  return w;
+}
+
+int run_int8(const Int8Gemm& g, int dtype, hipStream_t s) {
+  const hipError_t e = launch_int8_few(g, dtype, s);
+  return e == hipSuccess ? HESS_OK : hip_fail(e, "8-bit product launch");
+}
+
+// Backward workspace: dy with padded rows | weights | x, both in the
+// gradients' type | partial tiles.
+struct LinearGradWork {
+  int64_t w, x, slots, total;
+};
+int64_t piece(int dtype) { return 16 / elem_bytes(dtype); }
+LinearGradWork grad_work(int64_t n, int64_t d, int64_t f, int dtype, bool want_x, bool want_w) {
+  const int64_t es = elem_bytes(dtype), dp = up(d, piece(dtype)), fp = up(f, piece(dtype));
+  LinearGradWork r{};
+  r.w = f == fp ? 0 : up(n * fp * es, 256);
+  r.x = r.w + (want_x ? up(f * dp * es, 256) : 0);
+  r.slots = r.x + (want_w ? up(n * dp * es, 256) : 0);
+  FfnGemm gx = shape(n, d, f), gw = shape(fp, d, n);
+  gx.segs = 1;
+  r.total = r.slots + std::max(want_x ? slot_bytes(gx, kFfnDx, dtype) : 0, want_w ? slot_bytes(gw, kFfnDw, dtype) : 0);
+  return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hess_int8_quantize(const void* x, int64_t ldx, int dtype, int64_t n, int64_t d, int block, int8_t* codes,
+                       int64_t ldc, int64_t pad, void* scale, hess_stream_t stream) {
+  if (int rc = check_rows(n, d, block, dtype, x, ldx, codes, ldc, scale, "x")) return rc;
+  if (n == 0) return HESS_OK;
+  if (pad < d || pad > ldc) return fail(HESS_EINVAL, "pad = %lld outside [d, ldc]", (long long)pad);
+  const Mat in{"x", x, ldx, n, d};
+  const Mat outs[2] = {{"codes", codes, ldc, n, pad, 1}, {"scale", scale, scale_bytes(n, d, block), 1, scale_bytes(n, d, block), 1}};
+  if (int rc = check_outputs(outs, 2, &in, 1, elem_bytes(dtype), nullptr, 0)) return rc;
+  const Int8Rows r{x, ldx, codes, ldc, scale, n, d, pad};
+  const hipError_t e = launch_int8_quantize(r, block, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HESS_OK : hip_fail(e, "quantize launch");
+}
+
+int hess_int8_dequantize(const int8_t* codes, int64_t ldc, const void* scale, int64_t n, int64_t d, int block,
+                         void* x, int64_t ldx, int dtype, hess_stream_t stream) {
+  if (int rc = check_rows(n, d, block, dtype, x, ldx, codes, ldc, scale, "x")) return rc;
+  if (n == 0) return HESS_OK;
+  const Mat out{"x", x, ldx, n, d};
+  const Mat ins[2] = {{"codes", codes, ldc, n, d, 1}, {"scale", scale, scale_bytes(n, d, block), 1, scale_bytes(n, d, block), 1}};
+  if (int rc = check_outputs(&out, 1, ins, 2, elem_bytes(dtype), nullptr, 0)) return rc;
+  const Int8Rows r{x, ldx, const_cast<int8_t*>(codes), ldc, const_cast<void*>(scale), n, d, d};
+  const hipError_t e = launch_int8_dequantize(r, block, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HESS_OK : hip_fail(e, "dequantize launch");
+}
+
+int64_t hess_int8_matmul_workspace(int64_t n, int64_t d, int64_t f) {
+  if (check_product(n, d, f, HESS_BF16) != HESS_OK) return -1;
+  return 0;
+}
+
+int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
+                     const float* b_scale, int64_t n, int64_t d, int64_t f, void* y, int64_t ldy, int dtype, void* work,
+                     int64_t work_bytes, hess_stream_t stream) {
+  if (int rc = check_product(n, d, f, dtype)) return rc;
+  if (n == 0) return HESS_OK;
+  if (int rc = check_codes("a", a, lda, d)) return rc;
+  if (int rc = check_codes("b", b, ldb, d)) return rc;
+  if (int rc = check_scale("a_scale", a_scale)) return rc;
+  if (int rc = check_scale("b_scale", b_scale)) return rc;
+  const int64_t es = elem_bytes(dtype);
+  const Mat out{"y", y, ldy, n, f};
+  if (int rc = check_mat(out, es)) return rc;
+  const Mat ins[4] = {{"a", a, lda, n, d, 1}, {"b", b, ldb, f, d, 1}, {"a_scale", a_scale, n, 1, n, 4}, {"b_scale", b_scale, f, 1, f, 4}};
+  const int64_t need = hess_int8_matmul_workspace(n, d, f);
+  if (int rc = check_work(work, work_bytes, need)) return rc;
+  if (int rc = check_outputs(&out, 1, ins, 4, es, work, need)) return rc;
+  const Int8Gemm g{a, lda, a_scale, b, ldb, b_scale, y, ldy, n, f, d};
+  return run_int8(g, dtype, static_cast<hipStream_t>(stream));
+}
+
+int64_t hess_int8_linear_workspace(int64_t n, int64_t d, int64_t f, int dtype, int pass) {
+  if (check_product(n, d, f, dtype) != HESS_OK) return -1;
+  if (pass < 0 || pass > 3) {
+    fail(HESS_EINVAL, "pass %d outside [0, 3]", pass);
+    return -1;
+  }
+  if (n == 0) return 0;
+  return pass == 0 ? linear_work(n, d).total : grad_work(n, d, f, dtype, pass & 1, pass & 2).total;
+}
+
+int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t* w, int64_t ldw, const float* w_scale,
+                             int64_t n, int64_t d, int64_t f, void* y, int64_t ldy, int8_t* x_codes, int64_t ldc,
+                             float* x_scale, void* work, int64_t work_bytes, hess_stream_t stream) {
+  if (int rc = check_product(n, d, f, dtype)) return rc;
+  if (!x_codes != !x_scale) return fail(HESS_EINVAL, "x_codes and x_scale: both or neither");
+  if (n == 0) return HESS_OK;
+  const int64_t es = elem_bytes(dtype);
+  const Mat ins[3] = {{"x", x, ldx, n, d}, {"w", w, ldw, f, d, 1}, {"w_scale", w_scale, f, 1, f, 4}};
+  if (int rc = check_mat(ins[0], es)) return rc;
+  if (int rc = check_codes("w", w, ldw, d)) return rc;
+  if (int rc = check_scale("w_scale", w_scale)) return rc;
+  const Mat outs[3] = {{"y", y, ldy, n, f}, {"x_codes", x_codes, ldc, n, code_stride(d), 1}, {"x_scale", x_scale, n, 1, n, 4}};
+  if (int rc = check_mat(outs[0], es)) return rc;
+  if (x_codes) {
+    if (int rc = check_codes("x_codes", x_codes, ldc, code_stride(d))) return rc;
+    if (!aligned(x_codes, 16) || ldc % 16 != 0) return fail(HESS_EALIGN, "rows of x_codes not 16-byte aligned");
+    if (int rc = check_scale("x_scale", x_scale)) return rc;
+  }
+  const LinearWork room = linear_work(n, d);
+  if (int rc = check_work(work, work_bytes, room.total)) return rc;
+  if (int rc = check_outputs(outs, 3, ins, 3, es, work, room.total)) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* base = static_cast<char*>(work);
+  if (!x_codes) {
+    x_codes = reinterpret_cast<int8_t*>(base);
+    ldc = code_stride(d);
+    x_scale = reinterpret_cast<float*>(base + room.scale);
+  }
+  const Int8Rows r{x, ldx, x_codes, ldc, x_scale, n, d, code_stride(d)};
+  const hipError_t e = launch_int8_quantize(r, 0, dtype, s);
+  if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  const Int8Gemm g{x_codes, ldc, x_scale, w, ldw, w_scale, y, ldy, n, f, d};
+  return run_int8(g, dtype, s);
+}
+
+int hess_int8_linear_backward(const void* dy, int64_t lddy, int dtype, const int8_t* x_codes, int64_t ldc,
+                              const float* x_scale, const int8_t* w, int64_t ldw, const float* w_scale, int64_t n,
+                              int64_t d, int64_t f, void* dx, int64_t lddx, void* dw, int64_t lddw, void* work,
+                              int64_t work_bytes, hess_stream_t stream) {
+  if (int rc = check_product(n, d, f, dtype)) return rc;
+  const int64_t es = elem_bytes(dtype), dp = up(d, piece(dtype)), fp = up(f, piece(dtype));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Mat outs[2] = {{"dx", dx, lddx, n, d}, {"dw", dw, lddw, f, d}};
+  for (const Mat& m : outs)
+    if (m.p && m.rows > 0)
+      if (int rc = check_mat(m, es)) return rc;
+  if (n == 0) {
+    if (!dw) return HESS_OK;
+    const hipError_t e = launch_zero_rows(dw, lddw, f, d, (int)es, s);
+    return e == hipSuccess ? HESS_OK : hip_fail(e, "gradient clear launch");
+  }
+  if (!dx && !dw) return HESS_OK;
+  const Mat ins[5] = {{"dy", dy, lddy, n, f},
+                      {"x_codes", dw ? x_codes : nullptr, ldc, n, d, 1},
+                      {"x_scale", dw ? x_scale : nullptr, n, 1, n, 4},
+                      {"w", dx ? w : nullptr, ldw, f, d, 1},
+                      {"w_scale", dx ? w_scale : nullptr, f, 1, f, 4}};
+  if (int rc = check_mat(ins[0], es)) return rc;
+  if (f == fp && (!aligned(dy, 16) || (n > 1 && lddy % piece(dtype) != 0)))
+    return fail(HESS_EALIGN, "rows of dy must be 16-byte aligned where a row is a multiple of 16 bytes");
+  if (dw) {
+    if (int rc = check_codes("x_codes", x_codes, ldc, d)) return rc;
+    if (int rc = check_scale("x_scale", x_scale)) return rc;
+  }
+  if (dx) {
+    if (int rc = check_codes("w", w, ldw, d)) return rc;
+    if (int rc = check_scale("w_scale", w_scale)) return rc;
+  }
+  const LinearGradWork room = grad_work(n, d, f, dtype, dx != nullptr, dw != nullptr);
+  if (int rc = check_work(work, work_bytes, room.total)) return rc;
+  if (int rc = check_outputs(outs, 2, ins, 5, es, work, room.total)) return rc;
+
+  char* base = static_cast<char*>(work);
+  if (f != fp) {
+    const int64_t half = es / 2;  // a float32 moves as two 16-bit halves
+    PackRows p{};
+    p.src[0] = dy, p.dst[0] = base, p.ld[0] = lddy * half, p.rows[0] = n;
+    p.count = 1, p.cols = (int)(f * half), p.pad = (int)(fp * half);
+    const hipError_t e = launch_pack_rows16(p, s);
+    if (e != hipSuccess) return hip_fail(e, "operand copy launch");
+    dy = base;
+    lddy = fp;
+  }
+  float* slots = reinterpret_cast<float*>(base + room.slots);
+  if (dx) {
+    const Int8Rows r{base + room.w, dp, const_cast<int8_t*>(w), ldw, const_cast<float*>(w_scale), f, d, dp};
+    const hipError_t e = launch_int8_dequantize(r, 0, dtype, s);
+    if (e != hipSuccess) return hip_fail(e, "dequantize launch");
+    FfnGemm g = shape(n, d, f);
+    g.segs = 1;
+    g.a = dy, g.lda = lddy;
+    g.b0 = base + room.w, g.ldb0 = dp;
+    g.b1 = g.b0, g.ldb1 = dp;
+    g.o0 = dx, g.ldo0 = lddx;
+    g.ws = slots;
+    g.f = f, g.fp = fp;
+    if (int rc = run_product(g, kFfnDx, dtype, room.total - room.slots, s, "input gradient launch")) return rc;
+  }
+  if (dw) {
+    const Int8Rows r{base + room.x, dp, const_cast<int8_t*>(x_codes), ldc, const_cast<float*>(x_scale), n, d, dp};
+    const hipError_t e = launch_int8_dequantize(r, 0, dtype, s);
+    if (e != hipSuccess) return hip_fail(e, "dequantize launch");
+    FfnGemm g = shape(fp, d, n);
+    g.a = dy, g.lda = lddy;
+    g.b0 = base + room.x, g.ldb0 = dp;
+    g.o0 = dw, g.ldo0 = lddw;
+    g.ws = slots;
+    g.f = f, g.fp = fp;
+    if (int rc = run_product(g, kFfnDw, dtype, room.total - room.slots, s, "weight gradient launch")) return rc;
+  }
+  return HESS_OK;
+}
+
+}  // extern "C"

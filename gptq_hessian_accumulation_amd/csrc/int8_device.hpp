@@ -1,0 +1,47 @@
+// Device code shared by the 8-bit integer operators and the 8-bit activation
+// checkpoints: blocks of 32 columns with a power-of-two step.
+#pragma once
+
+#include "elem.hpp"
+#include "hess_device.hpp"
+
+namespace hess {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_at1 __attribute__((aligned(1)));
+typedef uint2 uint2_at1 __attribute__((aligned(1)));
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// The exponent byte b of a block whose largest magnitude has these bits: the
+// step 2^(b - 127) is the power of two with 64 <= top / step < 128, at least
+// 2^-126, so that what codes stand for is no subnormal number; 255 where a value
+// of the block is not finite.
+__device__ __forceinline__ uint32_t block_exponent(uint32_t top) {
+  if (top >= kInfBits) return 255u;
+  return (uint32_t)max((int)(top >> 23) - 6, 1);
+}
+// 2^(127 - b), what the block's values are multiplied by (0 for 255: codes 0)
+__device__ __forceinline__ float block_inverse(uint32_t b) { return __uint_as_float(b == 255u ? 0u : (254u - b) << 23); }
+// 2^(b - 127), or NaN for 255
+__device__ __forceinline__ float block_step(uint32_t b) {
+  return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7fc00000u : b << 23);
+}
+
+// The nearest whole number, ties to even, of magnitude up to 127 (values past
+// 127.5 steps are less than a step off; 0 for what a block that is not finite holds).
+__device__ __forceinline__ int block_code(float v, float inverse) {
+  const float t = v * inverse;
+  return inverse == 0.0f ? 0 : (int)rintf(fminf(fmaxf(t, -127.0f), 127.0f));
+}
+
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+}
+
+// Code j of a packed word, as a float.
+__device__ __forceinline__ float unpack(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
+
+}  // namespace hess

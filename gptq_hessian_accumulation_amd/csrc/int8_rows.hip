@@ -1,0 +1,243 @@
+// Rows of activations or weights as int8 codes, and back, on gfx950.
+//
+// A scale a row (the operands of the 8-bit product): with a = max |x| of the
+// row, code = rint(127 x / a), ties to even, scale = a / 127 in float32.  The
+// code is the one exact arithmetic gives: for 16-bit types 127 x / a is formed
+// in float32 (off by less than 3 units of its last place) and rounded to 2^-21
+// relative first, which makes every tie exact, and other quotients of 11-bit
+// numbers are at least 2^-19 from one; for float32 it is formed in float64 and
+// rounded to 2^-40 (others are at least 2^-33 away).
+// Blocks of 32 columns (checkpoints): steps are powers of two, so that codes
+// take one exact multiplication and what they stand for is exact in bf16 and
+// fp16.
+// A row or block with an infinity or NaN has a NaN scale and codes 0.
+
+#include <algorithm>
+
+#include "int8_device.hpp"
+#include "int8_internal.hpp"
+
+namespace hess {
+
+namespace {
+
+// 8 values at p (any element alignment), the first `left` of them inside the row.
+template <class T> __device__ __forceinline__ void load8(const T* p, int64_t left, float (&v)[8]) {
+  if (left >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      typedef T T8 __attribute__((ext_vector_type(8)));
+      typedef T8 T8u __attribute__((aligned(sizeof(T))));
+      const T8 t = *reinterpret_cast<const T8u*>(p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = to_f32(t[j]);
+    } else {
+      typedef float F4u __attribute__((ext_vector_type(4), aligned(4)));
+      const F4u a = *reinterpret_cast<const F4u*>(p), b = *reinterpret_cast<const F4u*>(p + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < left ? to_f32(p[j]) : 0.0f;
+  }
+}
+
+// 8 codes to p (any alignment), the first `left` of them inside what is written.
+__device__ __forceinline__ void store8(int8_t* p, int64_t left, const int (&q)[8]) {
+  if (left >= 8) {
+    *reinterpret_cast<uint2_at1*>(p) = uint2{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) p[j] = (int8_t)q[j];
+  }
+}
+
+__device__ __forceinline__ uint32_t top_of(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+  return m;
+}
+
+// What turns a row's values into codes, from the bits of its largest magnitude.
+template <class T> struct RowCode {
+  float lift, inverse;
+  double inverse64;
+  bool zero;
+  __device__ __forceinline__ explicit RowCode(uint32_t top) {
+    const float a = __uint_as_float(top);
+    zero = top == 0u || top >= kInfBits;
+    if constexpr (sizeof(T) == 2) {
+      // (rows of tiny values are lifted by a power of two first)
+      lift = a < 1e-30f ? 0x1p96f : 1.0f;
+      inverse = zero ? 0.0f : 127.0f / (a * lift);
+    } else {
+      inverse64 = zero ? 0.0 : 127.0 / (double)a;
+    }
+  }
+  __device__ __forceinline__ int operator()(float v) const {
+    if (zero) return 0;
+    if constexpr (sizeof(T) == 2) {
+      const float t = v * lift * inverse;
+      return (int)rintf(__uint_as_float((__float_as_uint(t) + 4u) & ~7u));
+    } else {
+      const double t = (double)v * inverse64;
+      return (int)rint((t + 6144.0) - 6144.0);
+    }
+  }
+};
+__device__ __forceinline__ float row_scale(uint32_t top) {
+  return top >= kInfBits ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
+}
+
+// A row a workgroup of T threads, P pieces of 8 values a thread in registers
+// (rows longer than that are read twice).
+template <int DT, int T, int P> __global__ void __launch_bounds__(T) quantize_rows(Int8Rows R) {
+  typedef typename Elem<DT>::type E;
+  __shared__ uint32_t part[T / 64];
+  const int64_t row = blockIdx.x;
+  const E* x = static_cast<const E*>(R.x) + row * R.ldx;
+  int8_t* c = R.codes + row * R.ldc;
+  float v[P][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int64_t at = (int64_t)(i * T + threadIdx.x) * 8;
+    if (at < R.d) load8(x + at, R.d - at, v[i]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    top = max(top, top_of(v[i]));
+  }
+  for (int64_t at = (int64_t)(P * T + threadIdx.x) * 8; at < R.d; at += T * 8) {
+    float w[8];
+    load8(x + at, R.d - at, w);
+    top = max(top, top_of(w));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < T / 64; ++w) top = max(top, part[w]);
+  }
+  const RowCode<E> code(top);
+  if (threadIdx.x == 0) static_cast<float*>(R.scale)[row] = row_scale(top);
+  auto put = [&](int64_t at, const float (&w)[8]) {
+    int q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = code(w[j]);
+    store8(c + at, R.pad - at, q);
+  };
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int64_t at = (int64_t)(i * T + threadIdx.x) * 8;
+    if (at < R.pad) put(at, v[i]);
+  }
+  for (int64_t at = (int64_t)(P * T + threadIdx.x) * 8; at < R.pad; at += T * 8) {
+    float w[8] = {};
+    if (at < R.d) load8(x + at, R.d - at, w);
+    put(at, w);
+  }
+}
+
+// Blocks of 32 columns: 8 values a thread, four neighbouring lanes a block.
+template <int DT> __global__ void __launch_bounds__(256) quantize_blocks(Int8Rows R, int64_t groups, int64_t total) {
+  typedef typename Elem<DT>::type E;
+  // (whole waves run: total is a whole number of groups of four lanes)
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / (groups * 4);
+    const int64_t at = (i - row * groups * 4) * 8;
+    float v[8] = {};
+    if (at < R.d) load8(static_cast<const E*>(R.x) + row * R.ldx + at, R.d - at, v);
+    uint32_t top = top_of(v);
+    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+    const uint32_t b = block_exponent(top);
+    const float inverse = block_inverse(b);
+    int q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = block_code(v[j], inverse);
+    if (at < R.pad) store8(R.codes + row * R.ldc + at, R.pad - at, q);
+    if ((i & 3) == 0) static_cast<uint8_t*>(R.scale)[row * groups + at / 32] = (uint8_t)b;
+  }
+}
+
+// Codes back to values of DT (16-bit types: rounded to nearest even; exact for
+// blocks), 8 a thread; columns d .. pad - 1 become zeros.
+template <int DT, int Block> __global__ void __launch_bounds__(256) dequantize(Int8Rows R, int64_t per, int64_t total) {
+  typedef typename Elem<DT>::type E;
+  typedef E E8 __attribute__((ext_vector_type(8)));
+  typedef E8 E8u __attribute__((aligned(sizeof(E))));
+  const int64_t groups = (R.d + 31) / 32;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per, at = (i - row * per) * 8;
+    float step = 0.0f;
+    if constexpr (Block == 0) step = static_cast<const float*>(R.scale)[row];
+    else if (at < R.d) step = block_step(static_cast<const uint8_t*>(R.scale)[row * groups + at / 32]);
+    const int8_t* c = R.codes + row * R.ldc + at;
+    E* o = static_cast<E*>(const_cast<void*>(R.x)) + row * R.ldx + at;
+    E8 v;
+    if (at + 8 <= R.d) {
+      const uint2 w = *reinterpret_cast<const uint2_at1*>(c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = from_f32<E>(unpack(j < 4 ? w.x : w.y, j & 3) * step);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = from_f32<E>(at + j < R.d ? (float)c[j] * step : 0.0f);
+    }
+    if (at + 8 <= R.pad) {
+      *reinterpret_cast<E8u*>(o) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at + j < R.pad) o[j] = v[j];
+    }
+  }
+}
+
+int grid_of(int64_t threads) { return (int)std::min<int64_t>((threads + 255) / 256, 8192); }
+
+template <int DT> hipError_t quantize_type(const Int8Rows& r, int block, hipStream_t stream) {
+  if (block == 0) {
+    for (int64_t r0 = 0; r0 < r.n; r0 += 1 << 20) {
+      Int8Rows p = r;
+      p.n = std::min<int64_t>((int64_t)1 << 20, r.n - r0);
+      p.x = static_cast<const char*>(r.x) + r0 * r.ldx * Elem<DT>::size;
+      p.codes = r.codes + r0 * r.ldc;
+      p.scale = static_cast<float*>(r.scale) + r0;
+      quantize_rows<DT, 256, 2><<<(unsigned)p.n, 256, 0, stream>>>(p);
+    }
+  } else {
+    const int64_t groups = (r.d + 31) / 32, total = r.n * groups * 4;
+    quantize_blocks<DT><<<grid_of(total), 256, 0, stream>>>(r, groups, total);
+  }
+  return hipGetLastError();
+}
+
+template <int DT> hipError_t dequantize_type(const Int8Rows& r, int block, hipStream_t stream) {
+  const int64_t per = (r.pad + 7) / 8, total = r.n * per;
+  if (block == 0) dequantize<DT, 0><<<grid_of(total), 256, 0, stream>>>(r, per, total);
+  else dequantize<DT, 32><<<grid_of(total), 256, 0, stream>>>(r, per, total);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8_quantize(const Int8Rows& r, int block, int dtype, hipStream_t stream) {
+  if (r.n == 0) return hipSuccess;
+  if (dtype == kInBF16) return quantize_type<kInBF16>(r, block, stream);
+  if (dtype == kInF16) return quantize_type<kInF16>(r, block, stream);
+  return quantize_type<kInF32>(r, block, stream);
+}
+
+hipError_t launch_int8_dequantize(const Int8Rows& r, int block, int dtype, hipStream_t stream) {
+  if (r.n == 0) return hipSuccess;
+  if (dtype == kInBF16) return dequantize_type<kInBF16>(r, block, stream);
+  if (dtype == kInF16) return dequantize_type<kInF16>(r, block, stream);
+  return dequantize_type<kInF32>(r, block, stream);
+}
+
+}  // namespace hess

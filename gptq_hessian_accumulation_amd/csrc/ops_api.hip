@@ -11,100 +11,14 @@
 #include "distill_internal.hpp"
 #include "ffn_internal.hpp"
 #include "hess_internal.hpp"
+#include "ops_checks.hpp"
 
 using namespace hess;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 24;
-constexpr int64_t kMaxWidth = (int64_t)1 << 17;
-constexpr int64_t kMaxStride = (int64_t)1 << 20;
 constexpr int64_t kMaxVocab = (int64_t)1 << 28;
 constexpr int kMaxTop = 1024;
-
-bool dtype_ok(int t) { return t == HESS_BF16 || t == HESS_F32 || t == HESS_F16; }
-int64_t elem_bytes(int t) { return t == HESS_F32 ? 4 : 2; }
-int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-
-bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)a == 0; }
-
-// A matrix argument: rows x cols at p with row stride ld elements.
-struct Mat {
-  const char* name;
-  const void* p;
-  int64_t ld, rows, cols;
-  int64_t own = 0;  // bytes of an element, where it is not the call's type
-  int64_t bytes(int64_t es) const { return rows > 0 ? ((rows - 1) * ld + cols) * (own ? own : es) : 0; }
-};
-
-int check_mat(const Mat& m, int64_t es) {
-  if (!m.p) return fail(HESS_EINVAL, "null %s", m.name);
-  if (m.ld < m.cols || m.ld > kMaxStride)
-    return fail(HESS_EINVAL, "row stride %lld of %s outside [%lld, %lld]", (long long)m.ld, m.name, (long long)m.cols,
-                (long long)kMaxStride);
-  if (!aligned(m.p, es)) return fail(HESS_EALIGN, "%s not aligned to its element size", m.name);
-  return HESS_OK;
-}
-
-// No output may meet another output or an input.
-int check_outputs(const Mat* outs, int no, const Mat* ins, int ni, int64_t es, const void* work, int64_t wbytes) {
-  for (int a = 0; a < no; ++a) {
-    if (!outs[a].p) continue;
-    for (int b = 0; b < ni; ++b)
-      if (ins[b].p && overlaps(outs[a].p, outs[a].bytes(es), ins[b].p, ins[b].bytes(es)))
-        return fail(HESS_EINVAL, "%s overlaps %s", outs[a].name, ins[b].name);
-    for (int b = a + 1; b < no; ++b)
-      if (outs[b].p && overlaps(outs[a].p, outs[a].bytes(es), outs[b].p, outs[b].bytes(es)))
-        return fail(HESS_EINVAL, "%s overlaps %s", outs[a].name, outs[b].name);
-    if (wbytes > 0 && overlaps(outs[a].p, outs[a].bytes(es), work, wbytes))
-      return fail(HESS_EINVAL, "%s overlaps the workspace", outs[a].name);
-  }
-  for (int b = 0; b < ni; ++b)
-    if (wbytes > 0 && ins[b].p && overlaps(ins[b].p, ins[b].bytes(es), work, wbytes))
-      return fail(HESS_EINVAL, "%s overlaps the workspace", ins[b].name);
-  return HESS_OK;
-}
-
-int check_ffn_sizes(int64_t n, int64_t d, int64_t f, int dtype) {
-  if (!dtype_ok(dtype)) return fail(HESS_EINVAL, "unknown dtype %d", dtype);
-  if (n < 0 || n > kMaxRows) return fail(HESS_EINVAL, "n = %lld outside [0, 2^24]", (long long)n);
-  if (d < 1 || d > kMaxWidth || f < 1 || f > kMaxWidth)
-    return fail(HESS_EINVAL, "d = %lld, f = %lld outside [1, 2^17]", (long long)d, (long long)f);
-  return HESS_OK;
-}
-
-int check_work(const void* work, int64_t have, int64_t need) {
-  if (need == 0) return HESS_OK;
-  if (!work) return fail(HESS_EINVAL, "null workspace");
-  if (!aligned(work, 16)) return fail(HESS_EALIGN, "workspace not 16-byte aligned");
-  if (have < need)
-    return fail(HESS_EINVAL, "workspace of %lld bytes, %lld needed", (long long)have, (long long)need);
-  return HESS_OK;
-}
-
-FfnGemm shape(int64_t M, int64_t N, int64_t K) {
-  FfnGemm g{};
-  g.M = M;
-  g.N = N;
-  g.K = K;
-  return g;
-}
-
-// Bytes of partial tiles a product needs.
-int64_t slot_bytes(FfnGemm g, int mode, int dtype) {
-  const int edge = ffn_schedule(g, mode, dtype);
-  return (int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4;
-}
-
-// One product by tiles, its partial sums in `room` bytes at g.ws.  (The schedule
-// is the one the room was taken for, unless hess_set_ffn_schedule ran between.)
-int run_product(FfnGemm& g, int mode, int dtype, int64_t room, hipStream_t s, const char* what) {
-  const int edge = ffn_schedule(g, mode, dtype);
-  if ((int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4 > room)
-    return fail(HESS_EINVAL, "schedule changed during the call");
-  const hipError_t e = launch_ffn_gemm(g, mode, edge, dtype, s);
-  return e == hipSuccess ? HESS_OK : hip_fail(e, what);
-}
 
 // The tiles take 16-byte pieces of the rows of x and the weights: widths that
 // are no whole number of them are copied to padded rows in the workspace.
@@ -117,15 +31,32 @@ int64_t pack_bytes(int64_t rows, int64_t d, int dtype) { return up(rows * up(d, 
 struct FfnWork {
   int64_t pack, slots, total;
 };
-FfnWork ffn_work(int64_t n, int64_t d, int64_t f, int dtype, bool backward) {
+FfnGemm two_segments(FfnGemm g) {
+  g.segs = 2;
+  return g;
+}
+FfnWork ffn_work(int64_t n, int64_t d, int64_t f, int dtype, bool backward, bool pre8 = false) {
   FfnWork w{};
-  if (!backward && n <= kFfnFew && (packed(d, dtype) || ffn_prefers_few(n, d, f, elem_bytes(dtype)))) return w;
+  // (a pair in 8 bits comes from tiles, whose workgroups hold whole blocks of it)
+  if (!backward && !pre8 && n <= kFfnFew && (packed(d, dtype) || ffn_prefers_few(n, d, f, elem_bytes(dtype)))) return w;
   w.pack = backward ? up(n * 2 * up(f, 8) * elem_bytes(dtype), 256) : 0;
   w.slots = w.pack + (packed(d, dtype) ? pack_bytes(n, d, dtype) + 2 * pack_bytes(f, d, dtype) : 0);
-  w.total = w.slots + (backward ? std::max(slot_bytes(shape(n, d, f), kFfnDx, dtype),
+  w.total = w.slots + (backward ? std::max(slot_bytes(two_segments(shape(n, d, f)), kFfnDx, dtype),
                                            slot_bytes(shape(2 * up(f, 8), d, n), kFfnDw, dtype))
                                 : slot_bytes(shape(n, f, d), kFfnFwd, dtype));
   return w;
+}
+
+// The pair's type from the bits added to act, which are taken off (both: none).
+PairType pair_type(int& act) {
+  const int bits = act < 0 ? 0 : act & (HESS_PREACT_F32 | HESS_PREACT_I8);
+  if (bits == (HESS_PREACT_F32 | HESS_PREACT_I8)) return kPairSame;
+  act &= ~bits;
+  return bits == HESS_PREACT_F32 ? kPairF32 : bits == HESS_PREACT_I8 ? kPairI8 : kPairSame;
+}
+Mat pair_mat(const void* p, PairType pair, int64_t n, int64_t f) {
+  if (pair == kPairI8) return {"preact", p, pair8_cols(f), n, pair8_cols(f), 1};
+  return {"preact", p, 2 * up(f, 8), n, 2 * up(f, 8), pair == kPairF32 ? 4 : 0};
 }
 
 // x, gate and up as the tiles take them: where they are, or copied to padded
@@ -194,28 +125,36 @@ int64_t hess_gated_ffn_preact_cols(int64_t f) {
 int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int backward) {
   if (check_ffn_sizes(n, d, f, dtype) != HESS_OK) return -1;
   if (n == 0) return 0;
-  return ffn_work(n, d, f, dtype, backward != 0).total;
+  return ffn_work(n, d, f, dtype, backward != 0 && backward != 2, backward == 2).total;
+}
+
+int64_t hess_gated_ffn_preact_i8_cols(int64_t f) {
+  if (f < 1 || f > kMaxWidth) {
+    fail(HESS_EINVAL, "f = %lld outside [1, 2^17]", (long long)f);
+    return -1;
+  }
+  return pair8_cols(f);
 }
 
 int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64_t ldg, const void* w_up, int64_t ldu,
                            int dtype, int act, int64_t n, int64_t d, int64_t f, void* h, int64_t ldh, void* preact,
                            void* work, int64_t work_bytes, hess_stream_t stream) {
   if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
-  const bool pre32 = act >= 0 && (act & HESS_PREACT_F32);
-  if (pre32) act &= ~HESS_PREACT_F32;
+  const PairType pair = pair_type(act);
   if (act < HESS_SILU || act > HESS_GELU_TANH) return fail(HESS_EINVAL, "unknown activation %d", act);
   if (n == 0) return HESS_OK;
   const int64_t es = elem_bytes(dtype), fp = up(f, 8);
   const Mat ins[3] = {{"x", x, ldx, n, d}, {"w_gate", w_gate, ldg, f, d}, {"w_up", w_up, ldu, f, d}};
-  const Mat outs[2] = {{"h", h, ldh, n, f}, {"preact", preact, 2 * fp, n, 2 * fp, pre32 ? 4 : 0}};
+  const Mat outs[2] = {{"h", h, ldh, n, f}, pair_mat(preact, pair, n, f)};
+  const bool pre8 = preact && pair == kPairI8;
   for (const Mat& m : ins)
     if (int rc = check_mat(m, es)) return rc;
   if (int rc = check_mat(outs[0], es)) return rc;
   if (!aligned(preact, 16)) return fail(HESS_EALIGN, "preact not 16-byte aligned");
   FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
   // few tokens whose rows the tiles cannot read where they are: no copies
-  const bool few = n <= kFfnFew && (packed(d, dtype) || ffn_prefers_few(n, d, f, es) || !rows_in_place(o, n, f, dtype));
-  const FfnWork room = few ? FfnWork{} : ffn_work(n, d, f, dtype, false);
+  const bool few = !pre8 && n <= kFfnFew && (packed(d, dtype) || ffn_prefers_few(n, d, f, es) || !rows_in_place(o, n, f, dtype));
+  const FfnWork room = few ? FfnWork{} : ffn_work(n, d, f, dtype, false, pre8);
   if (int rc = check_work(work, work_bytes, room.total)) return rc;
   if (int rc = check_outputs(outs, 2, ins, 3, es, work, room.total)) return rc;
 
@@ -233,12 +172,13 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
   g.o0 = h;
   g.ldo0 = ldh;
   g.o1 = preact;
-  g.ldo1 = 2 * fp;
+  g.ldo1 = pre8 ? pair8_cols(f) : 2 * fp;
   g.ws = few ? nullptr : reinterpret_cast<float*>(base + room.slots);
   g.f = f;
   g.fp = fp;
   g.act = act;
-  g.pre32 = pre32;
+  g.pre32 = pair == kPairF32;
+  g.pre8 = pre8;
   if (!few) return run_product(g, kFfnFwd, dtype, room.total - room.slots, s, "gated feed-forward launch");
   const hipError_t e = launch_ffn_few(g, dtype, s);
   return e == hipSuccess ? HESS_OK : hip_fail(e, "gated feed-forward launch");
@@ -249,8 +189,7 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
                             int64_t d, int64_t f, void* dx, int64_t lddx, void* dw_gate, int64_t lddg, void* dw_up,
                             int64_t lddu, void* work, int64_t work_bytes, hess_stream_t stream) {
   if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
-  const bool pre32 = act >= 0 && (act & HESS_PREACT_F32);
-  if (pre32) act &= ~HESS_PREACT_F32;
+  const PairType pair = pair_type(act);
   if (act < HESS_SILU || act > HESS_GELU_TANH) return fail(HESS_EINVAL, "unknown activation %d", act);
   if (!dw_gate != !dw_up) return fail(HESS_EINVAL, "dw_gate and dw_up: both or neither");
   const int64_t es = elem_bytes(dtype), fp = up(f, 8);
@@ -259,10 +198,11 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
                       {"x", x, ldx, n, d},
                       {"w_gate", w_gate, ldg, f, d},
                       {"w_up", w_up, ldu, f, d},
-                      {"preact", preact, 2 * fp, n, 2 * fp, pre32 ? 4 : 0}};
+                      pair_mat(preact, pair, n, f)};
   const Mat outs[3] = {{"dx", dx, lddx, n, d}, {"dw_gate", dw_gate, lddg, f, d}, {"dw_up", dw_up, lddu, f, d}};
   for (const Mat& m : ins) {
     if (n == 0 && m.rows == 0) continue;
+    if (&m == &ins[1] && !x && !dw_gate) continue;  // dx alone does not read it
     if (int rc = check_mat(m, es)) return rc;
   }
   for (const Mat& m : outs)
@@ -286,10 +226,11 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
   float* slots = reinterpret_cast<float*>(dgu + room.slots);
   FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
   if (int rc = place_operands(o, dgu + room.pack, n, f, dtype, dw_gate != nullptr, dx != nullptr, s)) return rc;
-  e = launch_ffn_dgu(dh, lddh, preact, pre32, dgu, n, f, fp, act, dtype, s);
+  e = launch_ffn_dgu(dh, lddh, preact, pair, dgu, n, f, fp, act, dtype, s);
   if (e != hipSuccess) return hip_fail(e, "gate gradient launch");
   if (dx) {
     FfnGemm g = shape(n, d, f);
+    g.segs = 2;
     g.a = dgu;
     g.lda = 2 * fp;
     g.b0 = o.wg;

@@ -578,6 +578,20 @@ enum hess_act { HESS_SILU = 0, HESS_GELU = 1, HESS_GELU_TANH = 2 };
  * last rounding (bf16, fp16). */
 enum { HESS_PREACT_F32 = 16 };
 
+/* Added to act instead: the pair is held in 8 bits, for a backward pass that
+ * comes much later or of many layers (33 / 32 bytes for a value and what goes
+ * with it, instead of 2 or 4).  Each block of 32 features of a token's g, and of
+ * its u, has a step of its own, a power of two (see hess_int8_quantize, block
+ * 32); h does not change, and the backward pass takes its derivatives at what the
+ * codes stand for.  preact is then n rows of hess_gated_ffn_preact_i8_cols(f)
+ * bytes: with fq = f rounded up to a multiple of 32, fq codes of g, fq of u (zeros
+ * from f on), fq / 32 exponent bytes of g, fq / 32 of u.  Such a forward call
+ * needs hess_gated_ffn_workspace with backward = 2, takes tiles whatever n is
+ * (so that h of few tokens may differ from another call's in its last bit), and
+ * has the tiles' rule on alignment. */
+enum { HESS_PREACT_I8 = 64 };
+int64_t hess_gated_ffn_preact_i8_cols(int64_t f); /* -1 for bad f */
+
 int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int backward);
 
 /* Elements per row of the pre-activation pair a backward pass needs: 2 fp
@@ -611,8 +625,9 @@ int hess_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, int64
  * hess_gated_ffn_backward -- the gradients of sum(dh * h):
  *   dg = dh u act'(g), du = dh act(g),
  *   dx = dg Wg + du Wu (n x d), dw_gate = dg^T x, dw_up = du^T x (f x d).
- *   preact    as the forward call wrote it, with the same HESS_PREACT_F32
- *             (unchanged by this call).
+ *   preact    as the forward call wrote it, with the same HESS_PREACT_F32 or
+ *             HESS_PREACT_I8 (unchanged by this call).
+ *   x         may be NULL where dw_gate and dw_up are not wanted.
  *   dx        or NULL: not wanted.
  *   dw_gate, dw_up  both, or both NULL: not wanted.
  * Outputs are of dtype and are overwritten.  For 16-bit types dg and du are
@@ -679,6 +694,81 @@ int hess_distill_topk_backward(const float* dloss, const void* logits, int64_t l
                                int64_t vocab, const void* ids, int ids64, int64_t ldi, const void* values,
                                int values_dtype, int64_t ldv, int k, const float* weight, float temperature,
                                const float* stats, void* dlogits, int64_t lddz, hess_stream_t stream);
+
+/*
+ * Rows in 8-bit integers -- n rows of d values held as int8 codes with scales:
+ * the operands of the 8-bit product below, and activations kept for a backward
+ * pass.
+ *   block 0   a float scale a row: with a = max |x| of the row,
+ *             code = rint(127 x / a), ties to even (the exact quotient's),
+ *             scale = a / 127.  A row of zeros has scale 0.
+ *   block 32  an exponent byte e for each 32 columns of a row (the last block may
+ *             be shorter): the step 2^(e - 127) is the power of two with
+ *             64 <= a / step < 128, and at least 2^-126; code = rint(x / step), ties
+ *             to even, and 127 or -127 past those.
+ *             What the codes stand for is exact in bf16 and, from 2^-24 to 65504,
+ *             in fp16.
+ * A row (block) that holds an infinity or NaN has scale NaN (e = 255) and codes
+ * 0: it stands for NaN.
+ *   x         n x d of dtype, row stride ldx, any element alignment.
+ *   codes     n x d, row stride ldc, any alignment.
+ *   pad       quantize: columns written, d <= pad <= ldc, zeros from d on.
+ *   scale     n floats, or n x ceil(d / 32) bytes, contiguous.
+ * hess_int8_dequantize writes code * scale, rounded once to dtype.
+ * Outputs must not overlap the inputs or one another.  0 <= n <= 2^24,
+ * 1 <= d <= 2^17; n = 0 is a no-op.  Errors: EINVAL, EALIGN, EHIP.  These and the
+ * calls below neither allocate nor synchronize: they may be captured into a HIP
+ * graph; the same call gives the same bits every time.
+ */
+int hess_int8_quantize(const void* x, int64_t ldx, int dtype, int64_t n, int64_t d, int block, int8_t* codes,
+                       int64_t ldc, int64_t pad, void* scale, hess_stream_t stream);
+int hess_int8_dequantize(const int8_t* codes, int64_t ldc, const void* scale, int64_t n, int64_t d, int block,
+                         void* x, int64_t ldx, int dtype, hess_stream_t stream);
+
+/*
+ * hess_int8_matmul -- the product of rows of codes with a scale each:
+ *   y[t][o] = (sum_k a[t][k] b[o][k]) a_scale[t] b_scale[o]
+ * a n x d, b f x d (int8, any alignment), y n x f of dtype.  Sums are int32 and
+ * exact; a sum is rounded to float32, times b_scale, times a_scale, rounded
+ * to dtype.  1 <= d < 2^17, otherwise sizes, errors and workspace as above and
+ * below.
+ */
+int64_t hess_int8_matmul_workspace(int64_t n, int64_t d, int64_t f);
+int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
+                     const float* b_scale, int64_t n, int64_t d, int64_t f, void* y, int64_t ldy, int dtype, void* work,
+                     int64_t work_bytes, hess_stream_t stream);
+
+/*
+ * A linear layer in 8-bit integers -- x of dtype is quantized a row (token) at a
+ * time on its way into the product with f x d weights held as codes with a scale
+ * for each output channel (hess_int8_quantize, block 0, or the whole-row codes of
+ * hess_gptq_quantize less 8 with their steps):
+ *   forward   y = xq wq^T, xq and wq what the codes stand for.
+ *   backward  through the rounding as if it were not there (straight through):
+ *             dx = dy wq, dw = dy^T xq.
+ *   x_codes, x_scale  both or neither (NULL): where the forward call leaves the
+ *             codes of x, an 8-bit checkpoint for the backward call.  Rows of
+ *             round16(d) bytes are written (zeros from d on): ldc a multiple of 16
+ *             of at least that, 16-byte aligned.
+ *   dx        n x d, dw f x d, of dtype; NULL: not wanted.  The backward call reads
+ *             x_codes and x_scale only for dw, w and w_scale only for dx.
+ * Backward: xq and wq are rounded to dtype (16-bit types: the matrix instructions
+ * take such operands), sums are float32.  Where a row of dy is a multiple of 16
+ * bytes, every row must start at 16 (EALIGN); other rows are copied first.
+ * Workspace: hess_int8_linear_workspace(n, d, f, dtype, pass), 16-byte aligned,
+ * not shared by calls that may overlap; pass 0: forward, 1: backward for dx, 2: for
+ * dw, 3: for both; -1 for bad arguments.
+ * Outputs must not overlap the inputs, one another or the workspace.  n = 0 is a
+ * no-op, but dw becomes zero.
+ */
+int64_t hess_int8_linear_workspace(int64_t n, int64_t d, int64_t f, int dtype, int pass);
+int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t* w, int64_t ldw, const float* w_scale,
+                             int64_t n, int64_t d, int64_t f, void* y, int64_t ldy, int8_t* x_codes, int64_t ldc,
+                             float* x_scale, void* work, int64_t work_bytes, hess_stream_t stream);
+int hess_int8_linear_backward(const void* dy, int64_t lddy, int dtype, const int8_t* x_codes, int64_t ldc,
+                              const float* x_scale, const int8_t* w, int64_t ldw, const float* w_scale, int64_t n,
+                              int64_t d, int64_t f, void* dx, int64_t lddx, void* dw, int64_t lddw, void* work,
+                              int64_t work_bytes, hess_stream_t stream);
 
 #ifdef __cplusplus
 }

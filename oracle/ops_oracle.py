@@ -82,3 +82,41 @@ def distill_topk(logits, ids, values, weight, temperature):
             np.subtract.at(q, j, p)
             grad[r] = weight[r] / temperature * q
     return loss, stats, grad
+
+
+def quantize_rows(x):
+    """(codes, scales) of rows: rint(127 x / a) with a = max |x|, ties to even, and a / 127."""
+    codes, scales = np.zeros(x.shape), np.zeros(x.shape[0])
+    for r, v in enumerate(x):
+        if not np.isfinite(v).all():
+            scales[r] = np.nan
+            continue
+        a = np.abs(v).max()
+        if a > 0.0:
+            codes[r] = np.rint(127.0 * v / a)
+        scales[r] = a / 127.0
+    return codes, scales
+
+
+def quantize_blocks(x, block=32):
+    """(codes, steps) of blocks of 32 columns: s the power of two with 64 <= a / s < 128, at least 2^-126."""
+    n, d = x.shape
+    groups = -(-d // block)
+    codes, steps = np.zeros((n, d)), np.zeros((n, groups))
+    for r in range(n):
+        for b in range(groups):
+            v = x[r, b * block:(b + 1) * block]
+            if not np.isfinite(v).all():
+                steps[r, b] = np.nan
+                continue
+            s, a = 2.0 ** -126, np.abs(v).max()
+            while a / s >= 128.0:
+                s *= 2.0
+            codes[r, b * block:(b + 1) * block] = np.clip(np.rint(v / s), -127, 127)
+            steps[r, b] = s
+    return codes, steps
+
+
+def stand_for(codes, steps, block=32):
+    """What the codes of blocks stand for."""
+    return codes * np.repeat(steps, block, axis=1)[:, :codes.shape[1]]
