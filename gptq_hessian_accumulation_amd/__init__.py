@@ -254,7 +254,7 @@ def set_tile_override(edge: int) -> None:
 
 
 def set_ffn_schedule(edge: int = 0, whole: int = 0, parts: int = 1) -> None:
-    """Force the feed-forward block's tiles (edge 0 = automatic, 64, 128 or 256), the first ``whole`` done whole
+    """Force the feed-forward block's and the 8-bit product's tiles (edge 0 = automatic, 64, 128 or 256), the first ``whole`` done whole
     and the others in ``parts`` ranges of the sum; process-wide."""
     _check(_load().hess_set_ffn_schedule(int(edge), int(whole), int(parts)))
 
@@ -978,8 +978,10 @@ class Int8Rows(NamedTuple):
     block: int = 0
 
 
-def _int8_args(name: str, rows: Int8Rows, block=None):
-    """(tensors to keep, leading shape, n, d, code pointer, row stride, scale pointer) of checked rows."""
+def _int8_args(name: str, rows: Int8Rows, block=None, product=False):
+    """(tensors to keep, leading shape, n, d, code pointer, row stride, scale pointer) of checked rows.
+
+    product: rows of a multiple of 16 codes that do not start at 16 bytes are copied, as its tiles need it."""
     codes, scale, b = rows
     index = codes.get_device()
     if index < 0:
@@ -1002,7 +1004,7 @@ def _int8_args(name: str, rows: Int8Rows, block=None):
                          f"{tuple(lead) if b == 0 else (*lead, -(-d // 32))} tensor on {codes.device}")
     if not scale.is_contiguous():
         scale = scale.contiguous()
-    c2, cp, ldc = _rows(codes if len(shape) == 2 else codes.reshape(-1, d))
+    c2, cp, ldc = _rows(codes if len(shape) == 2 else codes.reshape(-1, d), 16 if product and d % 16 == 0 else 1)
     return (c2, scale), lead, c2.shape[0], d, cp, ldc, scale.data_ptr()
 
 
@@ -1073,8 +1075,8 @@ def int8_matmul(a: Int8Rows, b: Int8Rows, dtype: torch.dtype = torch.bfloat16, o
         with torch.cuda.stream(stream):
             return int8_matmul(a, b, dtype, out, workspace)
     lib = _load()
-    keep, lead, n, d, ap, lda, asp = _int8_args("a", a, 0)
-    keep_b, lead_b, f, db, bp, ldb, bsp = _int8_args("b", b, 0)
+    keep, lead, n, d, ap, lda, asp = _int8_args("a", a, 0, True)
+    keep_b, lead_b, f, db, bp, ldb, bsp = _int8_args("b", b, 0, True)
     if len(lead_b) != 1 or db != d:
         raise ValueError(f"b must hold (f, {d}) codes, not {tuple(b.codes.shape)}")
     code = _CODES.get(dtype)
@@ -1105,7 +1107,7 @@ def int8_linear_forward(x: torch.Tensor, w: Int8Rows, save: bool = False, out: t
             return int8_linear_forward(x, w, save, out, workspace)
     lib = _load()
     code = _float_code("x", x)
-    keep, lead_w, f, d, wp8, ldw, wsp = _int8_args("w", w, 0)
+    keep, lead_w, f, d, wp8, ldw, wsp = _int8_args("w", w, 0, True)
     if len(lead_w) != 1 or x.dim() < 1 or x.shape[-1] != d:
         raise ValueError(f"w must hold (f, d) codes and x be (..., d), not {tuple(w.codes.shape)} and {tuple(x.shape)}")
     lead = x.shape[:-1]

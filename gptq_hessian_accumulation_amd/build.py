@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libhess.so")
 
 SOURCES = ["hess_api.hip", "chol.hip", "quant.hip", "syrk.hip", "syrk_big.hip", "syrk_thin.hip", "materialize.hip", "local_blocks.hip", "stage.hip",
            "imatrix.hip", "ops_api.hip", "gated_ffn.hip", "ffn_tile.hip", "ffn_few.hip",
-           "distill.hip", "int8_api.hip", "int8_rows.hip", "int8_few.hip"]
+           "distill.hip", "int8_api.hip", "int8_rows.hip", "int8_few.hip", "int8_tile.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -50,6 +50,7 @@ struct FfnForced {
   int edge, whole, parts;
 };
 void ffn_force_schedule(FfnForced f);
+FfnForced ffn_forced();
 
 // One product by tiles.  Every operand row 16-byte aligned; where an operand's
 // rows run along K, K is a whole number of 16-byte pieces.

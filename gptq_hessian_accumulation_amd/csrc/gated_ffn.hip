@@ -204,6 +204,7 @@ namespace {
 FfnForced g_forced{0, 0, 1};
 }
 void ffn_force_schedule(FfnForced f) { g_forced = f; }
+FfnForced ffn_forced() { return g_forced; }
 
 int ffn_schedule(FfnGemm& g, int mode, int dtype) {
   const FfnForced forced = g_forced;

@@ -45,19 +45,71 @@ int check_product(int64_t n, int64_t d, int64_t f, int dtype) {
 // Codes as the product's tiles take them: rows of a multiple of 16 bytes.
 int64_t code_stride(int64_t d) { return up(d, 16); }
 
-// Forward workspace of a linear layer: codes and scales of x.
-struct LinearWork {
-  int64_t scale, total;
+Int8Gemm product(int64_t n, int64_t d, int64_t f) {
+  Int8Gemm g{};
+  g.M = n, g.N = f, g.K = d;
+  return g;
+}
+
+// Workspace of a product: a, b with padded rows | partial tiles; before them for
+// a linear layer the codes and scales of x.  Room for copied rows is there
+// where d is no multiple of 16.
+struct ProductWork {
+  int64_t a, b, slots, total;
 };
-LinearWork linear_work(int64_t n, int64_t d) {
+int64_t int8_slots(Int8Gemm g) {
+  const int edge = int8_schedule(g);
+  return (int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4;
+}
+ProductWork product_work(int64_t n, int64_t d, int64_t f) {
+  ProductWork w{};
+  if (n <= kInt8Few) return w;
+  const bool copy = d % 16 != 0;
+  w.b = copy ? up(n * code_stride(d), 256) : 0;
+  w.slots = w.b + (copy ? up(f * code_stride(d), 256) : 0);
+  w.total = w.slots + int8_slots(product(n, d, f));
+  return w;
+}
+struct LinearWork {
+  int64_t scale, product, total;
+};
+LinearWork linear_work(int64_t n, int64_t d, int64_t f) {
   LinearWork w{};
   w.scale = up(n * code_stride(d), 256);
-  w.total = w.scale + up(4 * n, 256);
+  w.product = w.scale + up(4 * n, 256);
+  w.total = w.product + product_work(n, d, f).total;
   return w;
 }
 
-int run_int8(const Int8Gemm& g, int dtype, hipStream_t s) {
-  const hipError_t e = launch_int8_few(g, dtype, s);
+bool rows_of_16(const void* p, int64_t ld, int64_t rows) { return aligned(p, 16) && (rows <= 1 || ld % 16 == 0); }
+
+// One product; zeros: a's codes are zeros from d to the next multiple of 16.
+int run_int8(Int8Gemm g, bool zeros, char* work, const ProductWork& room, int dtype, hipStream_t s) {
+  if (g.M <= kInt8Few) {
+    const hipError_t e = launch_int8_few(g, dtype, s);
+    return e == hipSuccess ? HESS_OK : hip_fail(e, "8-bit product launch");
+  }
+  const bool tidy = g.K % 16 == 0;
+  PackCodes p{};
+  p.cols = g.K, p.pad = code_stride(g.K);
+  auto copy = [&](const int8_t*& src, int64_t& ld, int64_t rows, char* dst) {
+    p.src[p.count] = src, p.ld[p.count] = ld, p.rows[p.count] = rows;
+    p.dst[p.count++] = reinterpret_cast<int8_t*>(dst);
+    src = reinterpret_cast<int8_t*>(dst), ld = p.pad;
+  };
+  if (tidy && (!rows_of_16(g.a, g.lda, g.M) || !rows_of_16(g.b, g.ldb, g.N)))
+    return fail(HESS_EALIGN, "rows of codes must be 16-byte aligned where d is a multiple of 16");
+  if (!tidy && !(zeros && rows_of_16(g.a, g.lda, g.M))) copy(g.a, g.lda, g.M, work + room.a);
+  if (!tidy && !(rows_of_16(g.b, g.ldb, g.N) && g.ldb >= p.pad)) copy(g.b, g.ldb, g.N, work + room.b);
+  if (p.count > 0) {
+    const hipError_t e = launch_pack_codes(p, s);
+    if (e != hipSuccess) return hip_fail(e, "operand copy launch");
+  }
+  const int edge = int8_schedule(g);
+  if ((int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4 > room.total - room.slots)
+    return fail(HESS_EINVAL, "schedule changed during the call");
+  g.ws = reinterpret_cast<int*>(work + room.slots);
+  const hipError_t e = launch_int8_tile(g, edge, dtype, s);
   return e == hipSuccess ? HESS_OK : hip_fail(e, "8-bit product launch");
 }
 
@@ -110,7 +162,7 @@ int hess_int8_dequantize(const int8_t* codes, int64_t ldc, const void* scale, in
 
 int64_t hess_int8_matmul_workspace(int64_t n, int64_t d, int64_t f) {
   if (check_product(n, d, f, HESS_BF16) != HESS_OK) return -1;
-  return 0;
+  return n == 0 ? 0 : product_work(n, d, f).total;
 }
 
 int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
@@ -126,11 +178,14 @@ int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const i
   const Mat out{"y", y, ldy, n, f};
   if (int rc = check_mat(out, es)) return rc;
   const Mat ins[4] = {{"a", a, lda, n, d, 1}, {"b", b, ldb, f, d, 1}, {"a_scale", a_scale, n, 1, n, 4}, {"b_scale", b_scale, f, 1, f, 4}};
-  const int64_t need = hess_int8_matmul_workspace(n, d, f);
-  if (int rc = check_work(work, work_bytes, need)) return rc;
-  if (int rc = check_outputs(&out, 1, ins, 4, es, work, need)) return rc;
-  const Int8Gemm g{a, lda, a_scale, b, ldb, b_scale, y, ldy, n, f, d};
-  return run_int8(g, dtype, static_cast<hipStream_t>(stream));
+  const ProductWork room = product_work(n, d, f);
+  if (int rc = check_work(work, work_bytes, room.total)) return rc;
+  if (int rc = check_outputs(&out, 1, ins, 4, es, work, room.total)) return rc;
+  Int8Gemm g = product(n, d, f);
+  g.a = a, g.lda = lda, g.sa = a_scale;
+  g.b = b, g.ldb = ldb, g.sb = b_scale;
+  g.y = y, g.ldy = ldy;
+  return run_int8(g, false, static_cast<char*>(work), room, dtype, static_cast<hipStream_t>(stream));
 }
 
 int64_t hess_int8_linear_workspace(int64_t n, int64_t d, int64_t f, int dtype, int pass) {
@@ -140,7 +195,7 @@ int64_t hess_int8_linear_workspace(int64_t n, int64_t d, int64_t f, int dtype, i
     return -1;
   }
   if (n == 0) return 0;
-  return pass == 0 ? linear_work(n, d).total : grad_work(n, d, f, dtype, pass & 1, pass & 2).total;
+  return pass == 0 ? linear_work(n, d, f).total : grad_work(n, d, f, dtype, pass & 1, pass & 2).total;
 }
 
 int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t* w, int64_t ldw, const float* w_scale,
@@ -161,9 +216,11 @@ int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t
     if (!aligned(x_codes, 16) || ldc % 16 != 0) return fail(HESS_EALIGN, "rows of x_codes not 16-byte aligned");
     if (int rc = check_scale("x_scale", x_scale)) return rc;
   }
-  const LinearWork room = linear_work(n, d);
+  const LinearWork room = linear_work(n, d, f);
   if (int rc = check_work(work, work_bytes, room.total)) return rc;
   if (int rc = check_outputs(outs, 3, ins, 3, es, work, room.total)) return rc;
+  if (n > kInt8Few && d % 16 == 0 && !rows_of_16(w, ldw, f))
+    return fail(HESS_EALIGN, "rows of w must be 16-byte aligned where d is a multiple of 16");
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* base = static_cast<char*>(work);
   if (!x_codes) {
@@ -174,8 +231,11 @@ int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t
   const Int8Rows r{x, ldx, x_codes, ldc, x_scale, n, d, code_stride(d)};
   const hipError_t e = launch_int8_quantize(r, 0, dtype, s);
   if (e != hipSuccess) return hip_fail(e, "quantize launch");
-  const Int8Gemm g{x_codes, ldc, x_scale, w, ldw, w_scale, y, ldy, n, f, d};
-  return run_int8(g, dtype, s);
+  Int8Gemm g = product(n, d, f);
+  g.a = x_codes, g.lda = ldc, g.sa = x_scale;
+  g.b = w, g.ldb = ldw, g.sb = w_scale;
+  g.y = y, g.ldy = ldy;
+  return run_int8(g, true, base + room.product, product_work(n, d, f), dtype, s);
 }
 
 int hess_int8_linear_backward(const void* dy, int64_t lddy, int dtype, const int8_t* x_codes, int64_t ldc,

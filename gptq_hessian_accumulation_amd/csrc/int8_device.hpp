@@ -41,6 +41,15 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
 }
 
+// A product's sum times its scales, in float32.  (The value is pinned before it
+// is rounded to the output's type: a fused multiply and conversion in one kernel
+// and not in another would give other bits.)
+__device__ __forceinline__ float scale_sum(int sum, float sb, float sa) {
+  float v = (float)sum * sb * sa;
+  asm("" : "+v"(v));
+  return v;
+}
+
 // Code j of a packed word, as a float.
 __device__ __forceinline__ float unpack(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
 

@@ -85,7 +85,7 @@ template <int DT, int MB, int W, int U> __global__ void __launch_bounds__(64 * W
     T* y = static_cast<T*>(P.y) + row * P.ldy + c;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (c + j < P.N) y[j] = from_f32<T>((float)s[j] * P.sb[c + j] * sa);
+      if (c + j < P.N) y[j] = from_f32<T>(scale_sum(s[j], P.sb[c + j], sa));
   }
 }
 

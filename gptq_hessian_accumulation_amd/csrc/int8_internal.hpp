@@ -32,9 +32,34 @@ struct Int8Gemm {
   void* y;
   int64_t ldy;
   int64_t M, N, K;
+  int* ws;          // partial tiles of the split items
+  // schedule: tiles 0 .. full - 1 are done whole; each of the others is cut into
+  // `parts` ranges of part_len K-iterations, whose partial sums go to workspace
+  // slot part * (ntiles - full) + (tile - full)
+  int tm, tn, ntiles, full, parts, part_len, niter;
 };
 
 // Operands of any alignment, no workspace.
 hipError_t launch_int8_few(const Int8Gemm& g, int dtype, hipStream_t stream);
+
+// Chooses the tile's edge (returned) and fills the schedule.
+int int8_schedule(Int8Gemm& g);
+// By tiles: every row of a and b 16-byte aligned, a's codes zero from K to the
+// next multiple of 16.
+hipError_t launch_int8_tile(const Int8Gemm& g, int edge, int dtype, hipStream_t stream);
+
+// Up to how many rows of a take the kernel without tiles.
+constexpr int64_t kInt8Few = 64;
+
+// Copies up to two matrices of rows[m] x cols bytes (row stride ld[m]) to rows of
+// pad >= cols (a multiple of 16) bytes, zeros past cols.
+struct PackCodes {
+  const int8_t* src[2];
+  int8_t* dst[2];
+  int64_t ld[2], rows[2];
+  int count;
+  int64_t cols, pad;
+};
+hipError_t launch_pack_codes(const PackCodes& p, hipStream_t stream);
 
 }  // namespace hess

@@ -198,6 +198,25 @@ template <int DT, int Block> __global__ void __launch_bounds__(256) dequantize(I
   }
 }
 
+// Matrix blockIdx.y: 16 codes a thread.
+__global__ void __launch_bounds__(256) pack_codes(PackCodes P) {
+  const int m = blockIdx.y;
+  const int64_t per = P.pad / 16, total = P.rows[m] * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per, c = (i - r * per) * 16;
+    const int8_t* p = P.src[m] + r * P.ld[m] + c;
+    u32x4 v{};
+    if (c + 16 <= P.cols) {
+      v = *reinterpret_cast<const u32x4_at1*>(p);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c + j < P.cols) v[j / 4] |= (uint32_t)(uint8_t)p[j] << (8 * (j % 4));
+    }
+    *reinterpret_cast<u32x4*>(P.dst[m] + r * P.pad + c) = v;
+  }
+}
+
 int grid_of(int64_t threads) { return (int)std::min<int64_t>((threads + 255) / 256, 8192); }
 
 template <int DT> hipError_t quantize_type(const Int8Rows& r, int block, hipStream_t stream) {
@@ -231,6 +250,15 @@ hipError_t launch_int8_quantize(const Int8Rows& r, int block, int dtype, hipStre
   if (dtype == kInBF16) return quantize_type<kInBF16>(r, block, stream);
   if (dtype == kInF16) return quantize_type<kInF16>(r, block, stream);
   return quantize_type<kInF32>(r, block, stream);
+}
+
+hipError_t launch_pack_codes(const PackCodes& p, hipStream_t stream) {
+  int64_t most = 0;
+  for (int m = 0; m < p.count; ++m) most = std::max(most, p.rows[m]);
+  const int64_t total = most * (p.pad / 16);
+  if (total == 0) return hipSuccess;
+  pack_codes<<<dim3((unsigned)std::min<int64_t>((total + 255) / 256, 2048), p.count), 256, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 hipError_t launch_int8_dequantize(const Int8Rows& r, int block, int dtype, hipStream_t stream) {

@@ -1,0 +1,341 @@
+// The product of int8 rows by tiles of edge 256, 128 or 64 with int32
+// accumulators, on v_mfma_i32_16x16x64_i8.  A stage is 64 bytes of K.
+//
+//  * 8 waves of 128 x 64 (edge 256) or 4 of 64 x 64 (edge 128) or 32 x 32 (edge
+//    64); two waves share each SIMD (edge 128: two workgroups a CU; edge 64:
+//    four).  The B operand goes first, so that a lane holds four consecutive
+//    columns; two neighbouring blocks are exchanged between lane rows before
+//    they are stored (eight columns, one 16-byte store).
+//  * Both operands go from memory straight into LDS, five stages deep (the loads
+//    of four iterations are in flight while one is multiplied, one barrier an
+//    iteration), kept row by row, 64 bytes a row, their 16-byte chunks
+//    XOR-swizzled by bits 1-2 of the row, and are read with ds_read_b128.
+//  * Rows past the matrix and chunks of K past it get an offset past every
+//    descriptor's range and read as zeros.  Inside the last 16-byte chunk of K
+//    the codes of A past K are zeros in memory, whatever those of B are.
+//  * Sums are exact, so that a split along K and its order change nothing.
+
+#include <algorithm>
+#include <type_traits>
+
+#include "ffn_device.hpp"
+#include "int8_device.hpp"
+#include "int8_internal.hpp"
+
+namespace hess {
+
+namespace {
+
+constexpr uint32_t kOOB = 0x80000000u;  // an offset past any descriptor's range
+constexpr int64_t kAll = 0x7fffffff;
+constexpr int kStages = 5, kAhead = 4;
+
+__device__ __forceinline__ i32x4 mma_i8(const u32x4& a, const u32x4& b, const i32x4& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// Tile t: groups of 8 tile rows, column by column inside a group.
+__device__ __forceinline__ void coords(const Int8Gemm& P, int t, int& I, int& J) {
+  const int per = 8 * P.tn, grp = t / per;
+  const int rows = min(8, P.tm - grp * 8), in = t - grp * per;
+  J = in / rows;
+  I = grp * 8 + in - J * rows;
+}
+
+template <int DT, int Edge>
+__global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) int8_tile(Int8Gemm P) {
+  constexpr int kColWaves = Edge == 256 ? 4 : 2;    // the tile's waves are 2 x kColWaves
+  constexpr int kCols = Edge / kColWaves;           // columns of a wave
+  constexpr int kBm = Edge / 32, kBn = kCols / 16;  // 16-wide blocks of a wave
+  constexpr int kPanel = Edge * 64, kStage = 2 * kPanel;
+  constexpr int kLoads = kPanel / 1024 / (2 * kColWaves);  // 1-KB loads per wave, panel and stage
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / kColWaves, wc = wave % kColWaves;
+  const uint32_t lds0 = (uint32_t) reinterpret_cast<uintptr_t>((HESS_LDS char*)lds);
+
+  // the whole tiles and the parts are dealt to the XCDs separately, so that
+  // each has its share of either
+  const int block = blockIdx.x;
+  const int item = block < P.full ? item_of_block(block, P.full)
+                                  : P.full + item_of_block(block - P.full, (int)gridDim.x - P.full);
+  const int tail = P.ntiles - P.full;
+  int t = item, part = 0;
+  const bool whole = item < P.full;
+  if (!whole) {
+    part = (item - P.full) / tail;
+    t = P.full + (item - P.full) % tail;
+  }
+  const int it0 = __builtin_amdgcn_readfirstlane(whole ? 0 : part * P.part_len);
+  const int it1 = __builtin_amdgcn_readfirstlane(whole ? P.niter : min(P.niter, it0 + P.part_len));
+  int I, J;
+  coords(P, t, I, J);
+  const int64_t i0 = (int64_t)I * Edge, j0 = (int64_t)J * Edge;
+
+  // Offsets of this wave's loads: load i holds 16 rows, lane l row l / 4 of
+  // them and position l % 4, where chunk (l % 4) ^ (row / 2 % 4) lives.
+  const int chunk = (lane & 3) ^ ((lane >> 3) & 3);
+  uint32_t voffA[kLoads], voffB[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = 16 * (kLoads * wave + i) + (lane >> 2);
+    voffA[i] = i0 + row < P.M ? (uint32_t)(row * P.lda + chunk * 16) : kOOB;
+    voffB[i] = j0 + row < P.N ? (uint32_t)(row * P.ldb + chunk * 16) : kOOB;
+  }
+  const uint64_t baseA = reinterpret_cast<uint64_t>(P.a) + (uint64_t)(i0 * P.lda);
+  const uint64_t baseB = reinterpret_cast<uint64_t>(P.b) + (uint64_t)(j0 * P.ldb);
+  struct Next {
+    u32x4 ra, rb;
+    int lim;  // chunks of K left
+  };
+  auto describe = [&](int j) {
+    Next d;
+    const int64_t k0 = (int64_t)j * 64;
+    const bool live = j < it1;
+    d.lim = (int)((P.K - k0 + 15) / 16);
+    d.ra = rsrc_words(baseA + (uint64_t)k0, live ? kAll : 0);
+    d.rb = rsrc_words(baseB + (uint64_t)k0, live ? kAll : 0);
+    return d;
+  };
+  // load i of the wave's 2 kLoads of one stage
+  auto load1 = [&](uint32_t stage, const Next& d, int i) {
+    const bool isA = i < kLoads;
+    const int q = isA ? i : i - kLoads;
+    const uint32_t off = chunk < d.lim ? (isA ? voffA[q] : voffB[q]) : kOOB;
+    lds_dma16(isA ? d.ra : d.rb, off, stage + (isA ? 0 : kPanel) + (uint32_t)((kLoads * wave + q) * 1024));
+  };
+  auto load_stage = [&](uint32_t stage, int j) {
+    const Next d = describe(j);
+#pragma unroll
+    for (int i = 0; i < 2 * kLoads; ++i) load1(stage, d, i);
+  };
+
+  // Operand block m of a wave's share: lane l holds row l % 16 of the block,
+  // the l / 16-th chunk of K.
+  const int in_block = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
+  const int posA = wr * (Edge / 2) * 64 + in_block, posB = kPanel + wc * kCols * 64 + in_block;
+  auto read_a = [&](uint32_t stage, int m) { return *reinterpret_cast<const u32x4*>(lds + stage + posA + m * 1024); };
+  auto read_b = [&](uint32_t stage, int n) { return *reinterpret_cast<const u32x4*>(lds + stage + posB + n * 1024); };
+
+  i32x4 acc[kBm][kBn];
+#pragma unroll
+  for (int m = 0; m < kBm; ++m)
+#pragma unroll
+    for (int n = 0; n < kBn; ++n) acc[m][n] = i32x4{};
+
+  // Iteration j on the stage at cur (its first A blocks are in a, its B blocks
+  // in b), group by group: the matrix instructions of one A block, the read of
+  // the A block kRot groups later (of the next stage at the end), a read of the
+  // next stage's B (into c) and a load of iteration j + 4.  Before the first read
+  // of the next stage the wave waits for its own loads of it and meets the
+  // others (the next stage is then complete, and nobody reads the one before cur).
+  constexpr int kRot = kBm < 4 ? kBm : 4;
+  constexpr int kMeet = kBm - 6 > 0 ? kBm - 6 : 0;
+  u32x4 a[kRot];
+  auto step = [&](uint32_t cur, uint32_t nxt, uint32_t target, int j, const u32x4 (&b)[kBn], u32x4 (&c)[kBn]) {
+    const Next d = describe(j + kAhead);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < kBm; ++m) {
+      if (m == kMeet) {
+        __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 2)));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int n = 0; n < kBn; ++n) acc[m][n] = mma_i8(b[n], a[m % kRot], acc[m][n]);
+      a[m % kRot] = m + kRot < kBm ? read_a(cur, m + kRot) : read_a(nxt, m + kRot - kBm);
+      if (m >= kMeet && m < kMeet + kRot) {
+        c[m - kMeet] = read_b(nxt, m - kMeet);
+        load1(lds0 + target, d, m - kMeet);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  static_assert(2 * kLoads == kRot && kBn == kRot, "one load and one read of B in each of kRot groups");
+
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) load_stage(lds0 + q * kStage, it0 + q);
+  __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 1)));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  u32x4 b[kBn], c[kBn];
+#pragma unroll
+  for (int q = 0; q < kRot; ++q) a[q] = read_a(0, q);
+#pragma unroll
+  for (int q = 0; q < kBn; ++q) b[q] = read_b(0, q);
+  // two iterations a trip (two sets of B registers); an extra iteration
+  // multiplies zeros
+  uint32_t cur = 0, nxt = kStage, ld = kAhead * kStage;
+  auto rotate = [&] {
+    cur = nxt;
+    nxt = nxt + kStage == kStages * kStage ? 0u : nxt + kStage;
+    ld = ld + kStage == kStages * kStage ? 0u : ld + kStage;
+  };
+  for (int j = it0; j < it1; j += 2) {
+    step(cur, nxt, ld, j, b, c);
+    rotate();
+    step(cur, nxt, ld, j + 1, c, b);
+    rotate();
+  }
+  // the trailing loads write LDS: they end before the workgroup does
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_sched_barrier(0);
+
+  if (!whole) {
+    int* W = P.ws + ((int64_t)part * tail + (t - P.full)) * (Edge * Edge) +
+             (wr * (Edge / 2) + (lane & 15)) * Edge + wc * kCols + 4 * (lane >> 4);
+#pragma unroll
+    for (int m = 0; m < kBm; ++m)
+#pragma unroll
+      for (int n = 0; n < kBn; ++n) *reinterpret_cast<i32x4*>(W + 16 * m * Edge + 16 * n) = acc[m][n];
+    return;
+  }
+  // A tile's outputs.  Blocks n, n + 1: after exchanging the odd 16-lane rows of
+  // the first with the even ones of the second, lane row g holds columns
+  // 8 (g / 2) .. + 7 of block n + g % 2.
+  typedef typename Elem<DT>::type T;
+  int lv = lane;
+  asm volatile("" : "+v"(lv));  // the offsets are computed here, not kept through the loop
+  const int64_t c0 = j0 + wc * kCols + 16 * ((lv >> 4) & 1) + 8 * (lv >> 5);
+  float sb[kBn / 2][8];
+#pragma unroll
+  for (int n = 0; n < kBn / 2; ++n)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sb[n][j] = c0 + 32 * n + j < P.N ? P.sb[c0 + 32 * n + j] : 0.0f;
+#pragma unroll
+  for (int m = 0; m < kBm; ++m) {
+    const int64_t r = i0 + wr * (Edge / 2) + (lv & 15) + 16 * m;
+    const float sa = r < P.M ? P.sa[r] : 0.0f;
+    T* row = static_cast<T*>(P.y) + r * P.ldy;
+#pragma unroll
+    for (int n = 0; n < kBn; n += 2) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const auto s = __builtin_amdgcn_permlane16_swap((uint32_t)acc[m][n][j], (uint32_t)acc[m][n + 1][j], false, false);
+        v[j] = scale_sum((int)s[0], sb[n / 2][j], sa);
+        v[4 + j] = scale_sum((int)s[1], sb[n / 2][4 + j], sa);
+      }
+      const int64_t col = c0 + 16 * n;
+      if (r < P.M && col < P.N) store_n(row + col, v, (int)min((int64_t)8, P.N - col));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Split tiles: the parts' sums added, then the scales.  Block (t, s) handles
+// rows s * (1024 / Edge) .. of tile full + t; a thread takes four columns.
+template <int DT, int Edge> __global__ void __launch_bounds__(256) int8_join(Int8Gemm P) {
+  typedef typename Elem<DT>::type T;
+  const int tail = P.ntiles - P.full, t = blockIdx.x;
+  int I, J;
+  coords(P, P.full + t, I, J);
+  constexpr int kQuads = Edge / 4;
+  const int id = blockIdx.y * 256 + threadIdx.x, row = id / kQuads, quad = id % kQuads;
+  const int64_t r = (int64_t)I * Edge + row, c = (int64_t)J * Edge + 4 * quad;
+  if (r >= P.M || c >= P.N) return;
+  const int* W = P.ws + (int64_t)t * (Edge * Edge) + row * Edge + 4 * quad;
+  i32x4 s{};
+  for (int p = 0; p < P.parts; ++p) s += *reinterpret_cast<const i32x4*>(W + (int64_t)p * tail * (Edge * Edge));
+  const float sa = P.sa[r];
+  float v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = c + j < P.N ? scale_sum(s[j], P.sb[c + j], sa) : 0.0f;
+  store_n(static_cast<T*>(P.y) + r * P.ldy + c, v, (int)min((int64_t)4, P.N - c));
+}
+
+template <int DT, int Edge> void launch_edge(const Int8Gemm& g, hipStream_t stream) {
+  const int tail = g.ntiles - g.full;
+  int8_tile<DT, Edge><<<g.full + tail * g.parts, Edge == 256 ? 512 : 256, 0, stream>>>(g);
+  if (tail > 0) int8_join<DT, Edge><<<dim3(tail, Edge * (Edge / 4) / 256), 256, 0, stream>>>(g);
+}
+
+template <int DT> void launch_type(const Int8Gemm& g, int edge, hipStream_t stream) {
+  if (edge == 256) launch_edge<DT, 256>(g, stream);
+  else if (edge == 128) launch_edge<DT, 128>(g, stream);
+  else launch_edge<DT, 64>(g, stream);
+}
+
+// Places for workgroups on the card, and what `groups` workgroups at once take
+// per stage of K (us), from products timed at 65 .. 16384 rows: us at 256 x 4096 x
+// 4096 with edges 64 / 128 / 256 13.4 / 20.3 / 46.2, at 1999 x 2560 x 9728 99.7 /
+// 68.3 / 71.7, at 8192 x 4096 x 11264 720 / 467 / 343.
+int slots_of(int edge) { return edge == 256 ? 256 : edge == 128 ? 512 : 1024; }
+double stage_us(int edge, int groups) {
+  const int each = (groups + 255) / 256;  // on the busiest CU
+  if (edge == 256) return 0.53 + 0.25 * groups / 256;
+  if (edge == 128) return each > 1 ? 0.28 * each : 0.25 + 0.07 * groups / 256;
+  return std::max(0.15, 0.12 * each);
+}
+
+// The schedule for tiles of one edge, and its estimated time in us: whole tiles
+// fill complete rounds of the card, the tiles of a last, partly empty round may
+// be cut along K.
+double schedule_for(Int8Gemm& g, int edge) {
+  const int slots = slots_of(edge);
+  g.tm = (int)((g.M + edge - 1) / edge);
+  g.tn = (int)((g.N + edge - 1) / edge);
+  g.ntiles = g.tm * g.tn;
+  g.niter = (int)((g.K + 63) / 64);
+  g.full = g.ntiles;
+  g.parts = 1;
+  g.part_len = g.niter;
+  const double enter = edge == 256 ? 8.0 : 4.0, join = 6.0;
+  const int tail = g.ntiles % slots;
+  double us = (double)(g.ntiles / slots) * (g.niter * stage_us(edge, slots) + enter);
+  if (tail == 0) return us;
+  double best = 1e30;
+  for (int parts = 1; parts <= std::max(1, std::min(2 * slots / tail, g.niter / 4)); ++parts) {
+    const int len = (g.niter + parts - 1) / parts, work = tail * parts;
+    double t = work / slots * (len * stage_us(edge, slots) + enter);
+    if (work % slots > 0) t += len * stage_us(edge, work % slots) + enter;
+    if (parts > 1) t += join + (double)work * edge * edge * 8.0 / 12e6;
+    if (t >= best) continue;
+    best = t;
+    if (parts > 1) {
+      g.part_len = len;
+      g.parts = (g.niter + len - 1) / len;
+      g.full = g.ntiles - tail;
+    }
+  }
+  return us + best;
+}
+
+}  // namespace
+
+int int8_schedule(Int8Gemm& g) {
+  const FfnForced forced = ffn_forced();
+  if (forced.edge != 0) {
+    schedule_for(g, forced.edge);
+    g.part_len = (g.niter + forced.parts - 1) / forced.parts;
+    g.parts = (g.niter + g.part_len - 1) / g.part_len;
+    // (the tiles cut along K are at most as many as the estimate would cut)
+    g.full = g.parts == 1 ? g.ntiles : std::max(std::min(forced.whole, g.ntiles), g.ntiles - 1024);
+    return forced.edge;
+  }
+  int edge = 0;
+  double least = 1e30;
+  Int8Gemm chosen{};
+  for (int e : {256, 128, 64}) {
+    Int8Gemm s = g;
+    const double us = schedule_for(s, e);
+    if (us >= least) continue;
+    least = us;
+    edge = e;
+    chosen = s;
+  }
+  g = chosen;
+  return edge;
+}
+
+hipError_t launch_int8_tile(const Int8Gemm& g, int edge, int dtype, hipStream_t stream) {
+  if (dtype == kInBF16) launch_type<kInBF16>(g, edge, stream);
+  else if (dtype == kInF16) launch_type<kInF16>(g, edge, stream);
+  else launch_type<kInF32>(g, edge, stream);
+  return hipGetLastError();
+}
+
+}  // namespace hess

@@ -604,7 +604,8 @@ int64_t hess_gated_ffn_preact_cols(int64_t f);
  * the first `whole` of them (and all but the last 1,024) done whole, the others
  * in `parts` (1 .. 64) ranges of K added by a second launch.  edge 0: the
  * choice per call, an estimate of the time.  Workspaces are sized for the
- * schedule in force.  EINVAL for other values. */
+ * schedule in force.  EINVAL for other values.  The 8-bit product's tiles follow
+ * it too. */
 int hess_set_ffn_schedule(int edge, int whole, int parts);
 
 /*
@@ -730,8 +731,11 @@ int hess_int8_dequantize(const int8_t* codes, int64_t ldc, const void* scale, in
  *   y[t][o] = (sum_k a[t][k] b[o][k]) a_scale[t] b_scale[o]
  * a n x d, b f x d (int8, any alignment), y n x f of dtype.  Sums are int32 and
  * exact; a sum is rounded to float32, times b_scale, times a_scale, rounded
- * to dtype.  1 <= d < 2^17, otherwise sizes, errors and workspace as above and
- * below.
+ * to dtype.  1 <= d < 2^17.  With more than 64 rows of a, and d a multiple of 16,
+ * every row of a and b must start at 16 bytes (EALIGN); where d is no such
+ * multiple, rows of a are copied to padded ones, and those of b too unless they
+ * start at 16 bytes and are at least round16(d) bytes apart (codes of b between d
+ * and there may be any).  The linear layer below has the same rule for w.
  */
 int64_t hess_int8_matmul_workspace(int64_t n, int64_t d, int64_t f);
 int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,

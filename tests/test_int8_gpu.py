@@ -348,3 +348,22 @@ def test_ffn_checkpoint_not_finite():
     got = pair_of(hs.gated_ffn_forward(x, wg, wu, save=torch.int8)[1], f)
     for a, b in zip(got[:2], clean[:2]):
         assert np.isnan(a[5]).all() and np.array_equal(np.delete(a, 5, 0), np.delete(b, 5, 0))
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("edge,whole,parts", [(64, 1 << 30, 1), (64, 0, 2), (64, 5, 3), (128, 1 << 30, 1), (128, 0, 3),
+                                              (128, 2, 2), (256, 1 << 30, 1), (256, 0, 2), (256, 1, 3)])
+@pytest.mark.parametrize("n,d,f", [(300, 1040, 330), (300, 1001, 513)])
+def test_matmul_schedules(n, d, f, edge, whole, parts, dt):
+    """Each tile, done whole, split, and both at once: the same bits, since the sums are exact."""
+    say(f"matmul {dt} {n}x{d}x{f} edge {edge} whole {whole} parts {parts}")
+    a, b = random_codes(11, n, d), random_codes(12, f, d)
+    want = hs.int8_matmul(a, b, dtype=TYPES[dt])
+    exact = product(a, b)
+    check("y", want, exact, np.abs(exact) * (half(dt) + 3.01 * U) * (1 + half(dt)) + FLOOR[dt])
+    try:
+        hs.set_ffn_schedule(edge, whole, parts)
+        got = hs.int8_matmul(a, b, dtype=TYPES[dt])
+    finally:
+        hs.set_ffn_schedule()
+    assert torch.equal(got, want)
