@@ -75,6 +75,7 @@ struct LinearWork {
 };
 LinearWork linear_work(int64_t n, int64_t d, int64_t f) {
   LinearWork w{};
+  if (n == 1 && d <= kInt8One) return w;  // quantized by the product itself, or into x_codes
   w.scale = up(n * code_stride(d), 256);
   w.product = w.scale + up(4 * n, 256);
   w.total = w.product + product_work(n, d, f).total;
@@ -84,26 +85,23 @@ LinearWork linear_work(int64_t n, int64_t d, int64_t f) {
 bool rows_of_16(const void* p, int64_t ld, int64_t rows) { return aligned(p, 16) && (rows <= 1 || ld % 16 == 0); }
 
 // One product; zeros: a's codes are zeros from d to the next multiple of 16.
-int run_int8(Int8Gemm g, bool zeros, char* work, const ProductWork& room, int dtype, hipStream_t s) {
+// Puts codes with padded rows in the workspace in place of m's.
+void copied(PackCodes& p, const int8_t*& m, int64_t& ld, int64_t rows, int64_t d, char* dst) {
+  p.cols = d, p.pad = code_stride(d);
+  p.src[p.count] = m, p.ld[p.count] = ld, p.rows[p.count] = rows;
+  p.dst[p.count++] = reinterpret_cast<int8_t*>(dst);
+  m = reinterpret_cast<int8_t*>(dst), ld = p.pad;
+}
+// Whether the tiles cannot take b's rows where they are (d no multiple of 16).
+bool untidy(const Int8Gemm& g) {
+  return g.M > kInt8Few && g.K % 16 != 0 && !(rows_of_16(g.b, g.ldb, g.N) && g.ldb >= code_stride(g.K));
+}
+
+// One product; its operands are as the kernel for its size takes them.
+int run_int8(Int8Gemm g, char* work, const ProductWork& room, int dtype, hipStream_t s) {
   if (g.M <= kInt8Few) {
     const hipError_t e = launch_int8_few(g, dtype, s);
     return e == hipSuccess ? HESS_OK : hip_fail(e, "8-bit product launch");
-  }
-  const bool tidy = g.K % 16 == 0;
-  PackCodes p{};
-  p.cols = g.K, p.pad = code_stride(g.K);
-  auto copy = [&](const int8_t*& src, int64_t& ld, int64_t rows, char* dst) {
-    p.src[p.count] = src, p.ld[p.count] = ld, p.rows[p.count] = rows;
-    p.dst[p.count++] = reinterpret_cast<int8_t*>(dst);
-    src = reinterpret_cast<int8_t*>(dst), ld = p.pad;
-  };
-  if (tidy && (!rows_of_16(g.a, g.lda, g.M) || !rows_of_16(g.b, g.ldb, g.N)))
-    return fail(HESS_EALIGN, "rows of codes must be 16-byte aligned where d is a multiple of 16");
-  if (!tidy && !(zeros && rows_of_16(g.a, g.lda, g.M))) copy(g.a, g.lda, g.M, work + room.a);
-  if (!tidy && !(rows_of_16(g.b, g.ldb, g.N) && g.ldb >= p.pad)) copy(g.b, g.ldb, g.N, work + room.b);
-  if (p.count > 0) {
-    const hipError_t e = launch_pack_codes(p, s);
-    if (e != hipSuccess) return hip_fail(e, "operand copy launch");
   }
   const int edge = int8_schedule(g);
   if ((int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4 > room.total - room.slots)
@@ -185,7 +183,19 @@ int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const i
   g.a = a, g.lda = lda, g.sa = a_scale;
   g.b = b, g.ldb = ldb, g.sb = b_scale;
   g.y = y, g.ldy = ldy;
-  return run_int8(g, false, static_cast<char*>(work), room, dtype, static_cast<hipStream_t>(stream));
+  char* base = static_cast<char*>(work);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (n > kInt8Few && d % 16 == 0 && (!rows_of_16(a, lda, n) || !rows_of_16(b, ldb, f)))
+    return fail(HESS_EALIGN, "rows of codes must be 16-byte aligned where d is a multiple of 16");
+  if (n > kInt8Few && d % 16 != 0) {
+    PackCodes p{};
+    const bool copy_b = untidy(g);
+    copied(p, g.a, g.lda, n, d, base + room.a);
+    if (copy_b) copied(p, g.b, g.ldb, f, d, base + room.b);
+    const hipError_t e = launch_pack_codes(p, s);
+    if (e != hipSuccess) return hip_fail(e, "operand copy launch");
+  }
+  return run_int8(g, base, room, dtype, s);
 }
 
 int64_t hess_int8_linear_workspace(int64_t n, int64_t d, int64_t f, int dtype, int pass) {
@@ -223,19 +233,27 @@ int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t
     return fail(HESS_EALIGN, "rows of w must be 16-byte aligned where d is a multiple of 16");
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* base = static_cast<char*>(work);
+  Int8Gemm g = product(n, d, f);
+  g.b = w, g.ldb = ldw, g.sb = w_scale;
+  g.y = y, g.ldy = ldy;
+  if (n == 1 && d <= kInt8One && !x_codes) {
+    g.x = x, g.ldx = ldx;
+    const hipError_t e = launch_int8_one(g, dtype, s);
+    return e == hipSuccess ? HESS_OK : hip_fail(e, "8-bit product launch");
+  }
   if (!x_codes) {
     x_codes = reinterpret_cast<int8_t*>(base);
     ldc = code_stride(d);
     x_scale = reinterpret_cast<float*>(base + room.scale);
   }
+  const ProductWork rest = product_work(n, d, f);
   const Int8Rows r{x, ldx, x_codes, ldc, x_scale, n, d, code_stride(d)};
-  const hipError_t e = launch_int8_quantize(r, 0, dtype, s);
+  PackCodes p{};
+  if (untidy(g)) copied(p, g.b, g.ldb, f, d, base + room.product + rest.b);
+  const hipError_t e = launch_int8_quantize_and_pack(r, dtype, p, s);
   if (e != hipSuccess) return hip_fail(e, "quantize launch");
-  Int8Gemm g = product(n, d, f);
   g.a = x_codes, g.lda = ldc, g.sa = x_scale;
-  g.b = w, g.ldb = ldw, g.sb = w_scale;
-  g.y = y, g.ldy = ldy;
-  return run_int8(g, true, base + room.product, product_work(n, d, f), dtype, s);
+  return run_int8(g, base + room.product, rest, dtype, s);
 }
 
 int hess_int8_linear_backward(const void* dy, int64_t lddy, int dtype, const int8_t* x_codes, int64_t ldc,
@@ -276,21 +294,18 @@ int hess_int8_linear_backward(const void* dy, int64_t lddy, int dtype, const int
   if (int rc = check_outputs(outs, 2, ins, 5, es, work, room.total)) return rc;
 
   char* base = static_cast<char*>(work);
+  GradOperands o{};
+  if (dx) o.rows[0] = {base + room.w, dp, const_cast<int8_t*>(w), ldw, const_cast<float*>(w_scale), f, d, dp};
+  if (dw) o.rows[1] = {base + room.x, dp, const_cast<int8_t*>(x_codes), ldc, const_cast<float*>(x_scale), n, d, dp};
   if (f != fp) {
-    const int64_t half = es / 2;  // a float32 moves as two 16-bit halves
-    PackRows p{};
-    p.src[0] = dy, p.dst[0] = base, p.ld[0] = lddy * half, p.rows[0] = n;
-    p.count = 1, p.cols = (int)(f * half), p.pad = (int)(fp * half);
-    const hipError_t e = launch_pack_rows16(p, s);
-    if (e != hipSuccess) return hip_fail(e, "operand copy launch");
+    o.src = dy, o.dst = base, o.ld = lddy, o.n = n, o.cols = f, o.pad = fp;
     dy = base;
     lddy = fp;
   }
+  const hipError_t e = launch_int8_grad_operands(o, dtype, s);
+  if (e != hipSuccess) return hip_fail(e, "operand launch");
   float* slots = reinterpret_cast<float*>(base + room.slots);
   if (dx) {
-    const Int8Rows r{base + room.w, dp, const_cast<int8_t*>(w), ldw, const_cast<float*>(w_scale), f, d, dp};
-    const hipError_t e = launch_int8_dequantize(r, 0, dtype, s);
-    if (e != hipSuccess) return hip_fail(e, "dequantize launch");
     FfnGemm g = shape(n, d, f);
     g.segs = 1;
     g.a = dy, g.lda = lddy;
@@ -302,9 +317,6 @@ int hess_int8_linear_backward(const void* dy, int64_t lddy, int dtype, const int
     if (int rc = run_product(g, kFfnDx, dtype, room.total - room.slots, s, "input gradient launch")) return rc;
   }
   if (dw) {
-    const Int8Rows r{base + room.x, dp, const_cast<int8_t*>(x_codes), ldc, const_cast<float*>(x_scale), n, d, dp};
-    const hipError_t e = launch_int8_dequantize(r, 0, dtype, s);
-    if (e != hipSuccess) return hip_fail(e, "dequantize launch");
     FfnGemm g = shape(fp, d, n);
     g.a = dy, g.lda = lddy;
     g.b0 = base + room.x, g.ldb0 = dp;

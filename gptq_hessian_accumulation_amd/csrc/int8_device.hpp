@@ -53,4 +53,63 @@ __device__ __forceinline__ float scale_sum(int sum, float sb, float sa) {
 // Code j of a packed word, as a float.
 __device__ __forceinline__ float unpack(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
 
+// 8 values at p (any element alignment), the first `left` of them inside the row.
+template <class T> __device__ __forceinline__ void load8(const T* p, int64_t left, float (&v)[8]) {
+  if (left >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      typedef T T8 __attribute__((ext_vector_type(8)));
+      typedef T8 T8u __attribute__((aligned(sizeof(T))));
+      const T8 t = *reinterpret_cast<const T8u*>(p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = to_f32(t[j]);
+    } else {
+      typedef float F4u __attribute__((ext_vector_type(4), aligned(4)));
+      const F4u a = *reinterpret_cast<const F4u*>(p), b = *reinterpret_cast<const F4u*>(p + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < left ? to_f32(p[j]) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ uint32_t top_of(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+  return m;
+}
+
+// What turns a row's values into codes, from the bits of its largest magnitude.
+template <class T> struct RowCode {
+  float lift, inverse;
+  double inverse64;
+  bool zero;
+  __device__ __forceinline__ explicit RowCode(uint32_t top) {
+    const float a = __uint_as_float(top);
+    zero = top == 0u || top >= kInfBits;
+    if constexpr (sizeof(T) == 2) {
+      // (rows of tiny values are lifted by a power of two first)
+      lift = a < 1e-30f ? 0x1p96f : 1.0f;
+      inverse = zero ? 0.0f : 127.0f / (a * lift);
+    } else {
+      inverse64 = zero ? 0.0 : 127.0 / (double)a;
+    }
+  }
+  __device__ __forceinline__ int operator()(float v) const {
+    if (zero) return 0;
+    if constexpr (sizeof(T) == 2) {
+      const float t = v * lift * inverse;
+      return (int)rintf(__uint_as_float((__float_as_uint(t) + 4u) & ~7u));
+    } else {
+      const double t = (double)v * inverse64;
+      return (int)rint((t + 6144.0) - 6144.0);
+    }
+  }
+};
+__device__ __forceinline__ float row_scale(uint32_t top) {
+  return top >= kInfBits ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
+}
+
 }  // namespace hess

@@ -19,6 +19,19 @@ struct Int8Rows {
   int64_t pad;    // columns written: d, or more (zeros past d)
 };
 hipError_t launch_int8_quantize(const Int8Rows& r, int block, int dtype, hipStream_t stream);
+struct PackCodes;
+// block 0, and in the same launch the copy of one matrix of codes (count 0 or 1).
+hipError_t launch_int8_quantize_and_pack(const Int8Rows& r, int dtype, const PackCodes& p, hipStream_t stream);
+// What a backward pass needs of a linear layer, in one launch: up to two sets of
+// rows with a scale each as values of dtype (rows.x null: not wanted), and dy
+// copied to rows of dy_pad values (src null: not wanted).
+struct GradOperands {
+  Int8Rows rows[2];
+  const void* src;
+  void* dst;
+  int64_t ld, n, cols, pad;
+};
+hipError_t launch_int8_grad_operands(const GradOperands& g, int dtype, hipStream_t stream);
 hipError_t launch_int8_dequantize(const Int8Rows& r, int block, int dtype, hipStream_t stream);
 
 // y[t][o] = (sum_k a[t][k] b[o][k]) sa[t] sb[o].
@@ -32,6 +45,8 @@ struct Int8Gemm {
   void* y;
   int64_t ldy;
   int64_t M, N, K;
+  const void* x;    // one row: the values that a would hold
+  int64_t ldx;
   int* ws;          // partial tiles of the split items
   // schedule: tiles 0 .. full - 1 are done whole; each of the others is cut into
   // `parts` ranges of part_len K-iterations, whose partial sums go to workspace
@@ -41,6 +56,9 @@ struct Int8Gemm {
 
 // Operands of any alignment, no workspace.
 hipError_t launch_int8_few(const Int8Gemm& g, int dtype, hipStream_t stream);
+// One row of values x of dtype (M = 1, K <= kInt8One; a and sa not read).
+hipError_t launch_int8_one(const Int8Gemm& g, int dtype, hipStream_t stream);
+constexpr int64_t kInt8One = 8192;
 
 // Chooses the tile's edge (returned) and fills the schedule.
 int int8_schedule(Int8Gemm& g);

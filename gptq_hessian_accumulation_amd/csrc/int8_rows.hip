@@ -21,27 +21,6 @@ namespace hess {
 
 namespace {
 
-// 8 values at p (any element alignment), the first `left` of them inside the row.
-template <class T> __device__ __forceinline__ void load8(const T* p, int64_t left, float (&v)[8]) {
-  if (left >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      typedef T T8 __attribute__((ext_vector_type(8)));
-      typedef T8 T8u __attribute__((aligned(sizeof(T))));
-      const T8 t = *reinterpret_cast<const T8u*>(p);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = to_f32(t[j]);
-    } else {
-      typedef float F4u __attribute__((ext_vector_type(4), aligned(4)));
-      const F4u a = *reinterpret_cast<const F4u*>(p), b = *reinterpret_cast<const F4u*>(p + 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < left ? to_f32(p[j]) : 0.0f;
-  }
-}
-
 // 8 codes to p (any alignment), the first `left` of them inside what is written.
 __device__ __forceinline__ void store8(int8_t* p, int64_t left, const int (&q)[8]) {
   if (left >= 8) {
@@ -53,50 +32,37 @@ __device__ __forceinline__ void store8(int8_t* p, int64_t left, const int (&q)[8
   }
 }
 
-__device__ __forceinline__ uint32_t top_of(const float (&v)[8]) {
-  uint32_t m = 0;
+// Matrix m of a set of copies: 16 codes a thread, from thread `first` of `all`.
+__device__ __forceinline__ void pack_range(const PackCodes& P, int m, int64_t first, int64_t all) {
+  const int64_t per = P.pad / 16, total = P.rows[m] * per;
+  for (int64_t i = first; i < total; i += all) {
+    const int64_t r = i / per, c = (i - r * per) * 16;
+    const int8_t* p = P.src[m] + r * P.ld[m] + c;
+    u32x4 v{};
+    if (c + 16 <= P.cols) {
+      v = *reinterpret_cast<const u32x4_at1*>(p);
+    } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-  return m;
+      for (int j = 0; j < 16; ++j)
+        if (c + j < P.cols) v[j / 4] |= (uint32_t)(uint8_t)p[j] << (8 * (j % 4));
+    }
+    *reinterpret_cast<u32x4*>(P.dst[m] + r * P.pad + c) = v;
+  }
 }
-
-// What turns a row's values into codes, from the bits of its largest magnitude.
-template <class T> struct RowCode {
-  float lift, inverse;
-  double inverse64;
-  bool zero;
-  __device__ __forceinline__ explicit RowCode(uint32_t top) {
-    const float a = __uint_as_float(top);
-    zero = top == 0u || top >= kInfBits;
-    if constexpr (sizeof(T) == 2) {
-      // (rows of tiny values are lifted by a power of two first)
-      lift = a < 1e-30f ? 0x1p96f : 1.0f;
-      inverse = zero ? 0.0f : 127.0f / (a * lift);
-    } else {
-      inverse64 = zero ? 0.0 : 127.0 / (double)a;
-    }
-  }
-  __device__ __forceinline__ int operator()(float v) const {
-    if (zero) return 0;
-    if constexpr (sizeof(T) == 2) {
-      const float t = v * lift * inverse;
-      return (int)rintf(__uint_as_float((__float_as_uint(t) + 4u) & ~7u));
-    } else {
-      const double t = (double)v * inverse64;
-      return (int)rint((t + 6144.0) - 6144.0);
-    }
-  }
-};
-__device__ __forceinline__ float row_scale(uint32_t top) {
-  return top >= kInfBits ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
+__global__ void __launch_bounds__(256) pack_codes(PackCodes P) {
+  pack_range(P, blockIdx.y, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // A row a workgroup of T threads, P pieces of 8 values a thread in registers
 // (rows longer than that are read twice).
-template <int DT, int T, int P> __global__ void __launch_bounds__(T) quantize_rows(Int8Rows R) {
+template <int DT, int T, int P> __global__ void __launch_bounds__(T) quantize_rows(Int8Rows R, PackCodes C) {
   typedef typename Elem<DT>::type E;
   __shared__ uint32_t part[T / 64];
   const int64_t row = blockIdx.x;
+  if (row >= R.n) {  // the workgroups behind the rows copy codes
+    pack_range(C, 0, (row - R.n) * T + threadIdx.x, (int64_t)(gridDim.x - R.n) * T);
+    return;
+  }
   const E* x = static_cast<const E*>(R.x) + row * R.ldx;
   int8_t* c = R.codes + row * R.ldc;
   float v[P][8];
@@ -166,13 +132,15 @@ template <int DT> __global__ void __launch_bounds__(256) quantize_blocks(Int8Row
 }
 
 // Codes back to values of DT (16-bit types: rounded to nearest even; exact for
-// blocks), 8 a thread; columns d .. pad - 1 become zeros.
-template <int DT, int Block> __global__ void __launch_bounds__(256) dequantize(Int8Rows R, int64_t per, int64_t total) {
+// blocks), 8 a thread, from thread `first` of `all`; columns d .. pad - 1 become
+// zeros.
+template <int DT, int Block>
+__device__ __forceinline__ void dequantize_range(const Int8Rows& R, int64_t first, int64_t all) {
   typedef typename Elem<DT>::type E;
   typedef E E8 __attribute__((ext_vector_type(8)));
   typedef E8 E8u __attribute__((aligned(sizeof(E))));
-  const int64_t groups = (R.d + 31) / 32;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  const int64_t groups = (R.d + 31) / 32, per = (R.pad + 7) / 8, total = R.n * per;
+  for (int64_t i = first; i < total; i += all) {
     const int64_t row = i / per, at = (i - row * per) * 8;
     float step = 0.0f;
     if constexpr (Block == 0) step = static_cast<const float*>(R.scale)[row];
@@ -197,37 +165,49 @@ template <int DT, int Block> __global__ void __launch_bounds__(256) dequantize(I
     }
   }
 }
+template <int DT, int Block> __global__ void __launch_bounds__(256) dequantize(Int8Rows R) {
+  dequantize_range<DT, Block>(R, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
 
-// Matrix blockIdx.y: 16 codes a thread.
-__global__ void __launch_bounds__(256) pack_codes(PackCodes P) {
-  const int m = blockIdx.y;
-  const int64_t per = P.pad / 16, total = P.rows[m] * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per, c = (i - r * per) * 16;
-    const int8_t* p = P.src[m] + r * P.ld[m] + c;
-    u32x4 v{};
-    if (c + 16 <= P.cols) {
-      v = *reinterpret_cast<const u32x4_at1*>(p);
+// The operands of a linear layer's gradients: blockIdx.y 0 and 1 the sets of rows,
+// 2 the copy of dy.
+template <int DT> __global__ void __launch_bounds__(256) grad_operands(GradOperands G) {
+  typedef typename Elem<DT>::type E;
+  typedef E E8 __attribute__((ext_vector_type(8)));
+  typedef E8 E8u __attribute__((aligned(sizeof(E))));
+  const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
+  if (blockIdx.y < 2) {
+    if (G.rows[blockIdx.y].x) dequantize_range<DT, 0>(G.rows[blockIdx.y], first, all);
+    return;
+  }
+  const int64_t per = (G.pad + 7) / 8, total = G.n * per;
+  for (int64_t i = first; i < total; i += all) {
+    const int64_t row = i / per, at = (i - row * per) * 8;
+    const E* p = static_cast<const E*>(G.src) + row * G.ld + at;
+    E* o = static_cast<E*>(G.dst) + row * G.pad + at;
+    if (at + 8 <= G.cols) {
+      *reinterpret_cast<E8u*>(o) = *reinterpret_cast<const E8u*>(p);
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (c + j < P.cols) v[j / 4] |= (uint32_t)(uint8_t)p[j] << (8 * (j % 4));
+      for (int j = 0; j < 8; ++j)
+        if (at + j < G.pad) o[j] = at + j < G.cols ? p[j] : (E)0.0f;
     }
-    *reinterpret_cast<u32x4*>(P.dst[m] + r * P.pad + c) = v;
   }
 }
 
 int grid_of(int64_t threads) { return (int)std::min<int64_t>((threads + 255) / 256, 8192); }
 
-template <int DT> hipError_t quantize_type(const Int8Rows& r, int block, hipStream_t stream) {
+template <int DT> hipError_t quantize_type(const Int8Rows& r, int block, const PackCodes& c, hipStream_t stream) {
   if (block == 0) {
-    for (int64_t r0 = 0; r0 < r.n; r0 += 1 << 20) {
+    const int64_t most = (int64_t)1 << 20;  // workgroups of a launch (fewer than 2^32 threads)
+    for (int64_t r0 = 0; r0 < r.n; r0 += most) {
       Int8Rows p = r;
-      p.n = std::min<int64_t>((int64_t)1 << 20, r.n - r0);
+      p.n = std::min(most, r.n - r0);
       p.x = static_cast<const char*>(r.x) + r0 * r.ldx * Elem<DT>::size;
       p.codes = r.codes + r0 * r.ldc;
       p.scale = static_cast<float*>(r.scale) + r0;
-      quantize_rows<DT, 256, 2><<<(unsigned)p.n, 256, 0, stream>>>(p);
+      const int extra = c.count > 0 && r0 == 0 ? (int)std::min<int64_t>((c.rows[0] * (c.pad / 16) + 255) / 256, 1024) : 0;
+      quantize_rows<DT, 256, 2><<<(unsigned)(p.n + extra), 256, 0, stream>>>(p, c);
     }
   } else {
     const int64_t groups = (r.d + 31) / 32, total = r.n * groups * 4;
@@ -237,19 +217,37 @@ template <int DT> hipError_t quantize_type(const Int8Rows& r, int block, hipStre
 }
 
 template <int DT> hipError_t dequantize_type(const Int8Rows& r, int block, hipStream_t stream) {
-  const int64_t per = (r.pad + 7) / 8, total = r.n * per;
-  if (block == 0) dequantize<DT, 0><<<grid_of(total), 256, 0, stream>>>(r, per, total);
-  else dequantize<DT, 32><<<grid_of(total), 256, 0, stream>>>(r, per, total);
+  const int grid = grid_of(r.n * ((r.pad + 7) / 8));
+  if (block == 0) dequantize<DT, 0><<<grid, 256, 0, stream>>>(r);
+  else dequantize<DT, 32><<<grid, 256, 0, stream>>>(r);
   return hipGetLastError();
 }
 
 }  // namespace
 
+hipError_t launch_int8_quantize_and_pack(const Int8Rows& r, int dtype, const PackCodes& p, hipStream_t stream) {
+  if (dtype == kInBF16) return quantize_type<kInBF16>(r, 0, p, stream);
+  if (dtype == kInF16) return quantize_type<kInF16>(r, 0, p, stream);
+  return quantize_type<kInF32>(r, 0, p, stream);
+}
+
 hipError_t launch_int8_quantize(const Int8Rows& r, int block, int dtype, hipStream_t stream) {
   if (r.n == 0) return hipSuccess;
-  if (dtype == kInBF16) return quantize_type<kInBF16>(r, block, stream);
-  if (dtype == kInF16) return quantize_type<kInF16>(r, block, stream);
-  return quantize_type<kInF32>(r, block, stream);
+  const PackCodes none{};
+  if (dtype == kInBF16) return quantize_type<kInBF16>(r, block, none, stream);
+  if (dtype == kInF16) return quantize_type<kInF16>(r, block, none, stream);
+  return quantize_type<kInF32>(r, block, none, stream);
+}
+
+hipError_t launch_int8_grad_operands(const GradOperands& g, int dtype, hipStream_t stream) {
+  int64_t most = g.src ? g.n * ((g.pad + 7) / 8) : 0;
+  for (const Int8Rows& r : g.rows)
+    if (r.x) most = std::max(most, r.n * ((r.pad + 7) / 8));
+  const dim3 grid(grid_of(most), g.src ? 3 : 2);
+  if (dtype == kInBF16) grad_operands<kInBF16><<<grid, 256, 0, stream>>>(g);
+  else if (dtype == kInF16) grad_operands<kInF16><<<grid, 256, 0, stream>>>(g);
+  else grad_operands<kInF32><<<grid, 256, 0, stream>>>(g);
+  return hipGetLastError();
 }
 
 hipError_t launch_pack_codes(const PackCodes& p, hipStream_t stream) {

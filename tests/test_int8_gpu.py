@@ -367,3 +367,32 @@ def test_matmul_schedules(n, d, f, edge, whole, parts, dt):
     finally:
         hs.set_ffn_schedule()
     assert torch.equal(got, want)
+
+
+# one row has kernels of its own, by width and length; up to 64 rows others, by both
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("n,d,f", [(1, 40, 70), (1, 1001, 2731), (1, 2048, 100), (1, 2049, 4096), (1, 2500, 4113),
+                                   (1, 4096, 4113), (1, 5000, 4200), (1, 8192, 48), (1, 8192, 4100), (1, 8193, 33),
+                                   (16, 260, 4100), (17, 260, 4096), (32, 333, 4097), (33, 64, 100), (20, 200, 8193),
+                                   (64, 200, 8200), (33, 1030, 8210), (64, 130, 8192)])
+def test_few_rows(n, d, f, dt):
+    say(f"few rows {dt} {n}x{d}x{f}")
+    x, w, qx, sx, qw, sw = layer_case(13, n, d, f, dt)
+    w8 = hs.quantize_int8(w)
+    want = (qx @ qw.T) * np.outer(sx, sw)
+    y = hs.int8_linear_forward(x, w8)
+    check("y", y, want, np.abs(want) * (half(dt) + 5.01 * U) * (1 + half(dt)) + FLOOR[dt])
+    y2, x8 = hs.int8_linear_forward(x, w8, save=True)
+    assert torch.equal(y, y2) and torch.equal(y, hs.int8_matmul(x8, w8, dtype=x.dtype))
+    packed = hs.Int8Rows(w8.codes.contiguous(), w8.scale)
+    assert torch.equal(y, hs.int8_linear_forward(x, packed))
+
+
+def test_one_row_not_finite():
+    say("one row, not finite")
+    w8 = hs.quantize_int8(torch.randn(50, 300, device="cuda"))
+    x = torch.randn(1, 300, device="cuda")
+    assert (hs.int8_linear_forward(torch.zeros_like(x), w8) == 0).all()
+    for bad in (float("inf"), float("nan")):
+        x[0, 299] = bad
+        assert torch.isnan(hs.int8_linear_forward(x, w8)).all()
