@@ -1008,11 +1008,15 @@ def _int8_args(name: str, rows: Int8Rows, block=None, product=False):
     return (c2, scale), lead, c2.shape[0], d, cp, ldc, scale.data_ptr()
 
 
-def _new_codes(lead, d: int, like: torch.Tensor):
-    """(codes, row stride): int8 (*lead, d), rows of a multiple of 16 bytes apart."""
+def _new_codes(shape, n: int, d: int, like: torch.Tensor):
+    """(codes, row stride): int8 of a shape of n rows of d, rows of a multiple of 16 bytes apart."""
     pad = -(-d // 16) * 16
-    codes = like.new_empty((*lead, pad), dtype=torch.int8)
-    return (codes if pad == d else codes[..., :d]), pad
+    if pad == d:
+        return like.new_empty(shape, dtype=torch.int8), pad
+    codes = like.new_empty((n, pad), dtype=torch.int8)
+    if len(shape) == 2:
+        return codes.as_strided((n, d), (pad, 1)), pad
+    return codes.view(*shape[:-1], pad)[..., :d], pad
 
 
 def quantize_int8(x: torch.Tensor, block: int = 0, stream=None) -> Int8Rows:
@@ -1031,13 +1035,18 @@ def quantize_int8(x: torch.Tensor, block: int = 0, stream=None) -> Int8Rows:
     code = _float_code("x", x)
     if block != 0 and block != 32:
         raise ValueError(f"block must be 0 or 32, not {block}")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    d = shape[-1] if len(shape) > 0 else 0
+    if d < 1:
         raise ValueError("x must be (..., d) with d >= 1")
-    lead, d = x.shape[:-1], x.shape[-1]
-    x2, xp, ldx = _rows(x if x.dim() == 2 else x.reshape(-1, d))
-    codes, pad = _new_codes(lead, d, x)
-    scale = x.new_empty(lead, dtype=torch.float32) if block == 0 else x.new_empty((*lead, -(-d // 32)), dtype=_E8)
-    rc = lib.hess_int8_quantize(xp, ldx, code, x2.shape[0], d, block, codes.data_ptr(), pad, pad, scale.data_ptr(),
+    x2, xp, ldx = _rows(x if len(shape) == 2 else x.reshape(-1, d))
+    n = x2.shape[0]
+    codes, pad = _new_codes(shape, n, d, x)
+    if block != 0:
+        scale = x.new_empty((*shape[:-1], -(-d // 32)), dtype=_E8)
+    else:
+        scale = x.new_empty(n if len(shape) == 2 else shape[:-1], dtype=torch.float32)
+    rc = lib.hess_int8_quantize(xp, ldx, code, n, d, block, codes.data_ptr(), pad, pad, scale.data_ptr(),
                                 _stream(None, x.get_device()))
     if rc != 0:
         _check(rc)
@@ -1055,9 +1064,12 @@ def dequantize_int8(rows: Int8Rows, dtype: torch.dtype = torch.bfloat16, out: to
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}; use torch.bfloat16, torch.float16 or torch.float32")
-    x = _out("out", out, (*lead, d), keep[0].new_empty(0, dtype=dtype)) if out is not None \
-        else keep[0].new_empty((*lead, d), dtype=dtype)
-    ldx = x.stride(0) if x.dim() == 2 and n > 1 else d
+    ldx = d
+    if out is None:
+        x = keep[0].new_empty((n, d) if len(lead) == 1 else (*lead, d), dtype=dtype)
+    else:
+        x = _out("out", out, (*lead, d), keep[0].new_empty(0, dtype=dtype))
+        ldx = x.stride(0) if x.dim() == 2 and n > 1 else d
     rc = lib.hess_int8_dequantize(cp, ldc, sp, n, d, rows.block, x.data_ptr(), ldx, code,
                                   _stream(None, x.get_device()))
     if rc != 0:
@@ -1118,9 +1130,10 @@ def int8_linear_forward(x: torch.Tensor, w: Int8Rows, save: bool = False, out: t
     codes = scale = None
     ldc = 0
     if save:
-        codes, ldc = _new_codes(lead, d, x)
-        scale = x.new_empty(lead, dtype=torch.float32)
-    wp, wb, work = _workspace(workspace, lib.hess_int8_linear_workspace(n, d, f, code, 0), x)
+        codes, ldc = _new_codes(x.shape, n, d, x)
+        scale = x.new_empty(n if len(lead) == 1 else lead, dtype=torch.float32)
+    need = lib.hess_int8_linear_workspace(n, d, f, code, 0)
+    wp, wb, work = _workspace(workspace, need, x) if need else (None, 0, None)
     rc = lib.hess_int8_linear_forward(xp, ldx, code, wp8, ldw, wsp, n, d, f, y.data_ptr(), ldy,
                                       codes.data_ptr() if save and n > 0 else None, ldc,
                                       scale.data_ptr() if save and n > 0 else None, wp, wb,

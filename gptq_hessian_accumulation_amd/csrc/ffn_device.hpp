@@ -156,14 +156,16 @@ __device__ __forceinline__ void put_pair8(const FfnGemm& P, int64_t r, int64_t c
   if (r >= P.M || c >= fq) return;
   char* row = static_cast<char*>(P.o1) + r * P.ldo1;
   const uint32_t bg = block_exponent(top_g), bu = block_exponent(top_u);
-  const float ig = block_inverse(bg), iu = block_inverse(bu);
+  const BlockCode cg(bg), cu(bu);
+  typedef uint32_t Words __attribute__((ext_vector_type(N / 4)));
+  Words wg, wu;
 #pragma unroll
-  for (int j = 0; j < N; j += 4) {
-    *reinterpret_cast<uint32_t*>(row + c + j) =
-        pack4(block_code(g[j], ig), block_code(g[j + 1], ig), block_code(g[j + 2], ig), block_code(g[j + 3], ig));
-    *reinterpret_cast<uint32_t*>(row + fq + c + j) =
-        pack4(block_code(u[j], iu), block_code(u[j + 1], iu), block_code(u[j + 2], iu), block_code(u[j + 3], iu));
+  for (int j = 0; j < N / 4; ++j) {
+    wg[j] = cg(g[4 * j], g[4 * j + 1], g[4 * j + 2], g[4 * j + 3]);
+    wu[j] = cu(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
   }
+  *reinterpret_cast<Words*>(row + c) = wg;
+  *reinterpret_cast<Words*>(row + fq + c) = wu;
   if (first) {
     row[2 * fq + c / 32] = (char)bg;
     row[2 * fq + fq / 32 + c / 32] = (char)bu;
@@ -171,11 +173,11 @@ __device__ __forceinline__ void put_pair8(const FfnGemm& P, int64_t r, int64_t c
 }
 // Columns past f are zeros (absent weight rows read as zeros, but times an
 // infinite x they are none).
-template <int N> __device__ __forceinline__ uint32_t top_inside(const FfnGemm& P, int64_t c, float (&v)[N]) {
+template <bool In, int N> __device__ __forceinline__ uint32_t top_inside(const FfnGemm& P, int64_t c, float (&v)[N]) {
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    v[j] = c + j < P.f ? v[j] : 0.0f;
+    if constexpr (!In) v[j] = c + j < P.f ? v[j] : 0.0f;
     m = max(m, abs_bits(v[j]));
   }
   return m;

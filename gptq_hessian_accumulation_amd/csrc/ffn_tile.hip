@@ -319,9 +319,7 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) f
       if (P.pre8) {
         // a block's 32 features are in the four lanes of one row (edge 64: in
         // two of this wave and two of the next, which meet in LDS)
-        uint32_t tg = top_inside(P, col, g), tu = top_inside(P, col, u);
-        tg = max(tg, (uint32_t)__shfl_xor((int)tg, 32));
-        tu = max(tu, (uint32_t)__shfl_xor((int)tu, 32));
+        uint32_t tg = max_over_32(top_inside<In>(P, col, g)), tu = max_over_32(top_inside<In>(P, col, u));
         if constexpr (Edge == 64) {
           uint2* tops = reinterpret_cast<uint2*>(lds);
           const int at = (int)(r - i0);
@@ -332,8 +330,8 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) f
           tg = max(tg, o.x);
           tu = max(tu, o.y);
         } else {
-          tg = max(tg, (uint32_t)__shfl_xor((int)tg, 16));
-          tu = max(tu, (uint32_t)__shfl_xor((int)tu, 16));
+          tg = max_over_16(tg);
+          tu = max_over_16(tu);
         }
         put_pair8(P, r, col, g, u, tg, tu, (col & 31) == 0);
       }
@@ -408,7 +406,7 @@ template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn
     put_fwd<DT>(P, r, c, g, u);
     if (P.pre8) {
       // eight neighbouring lanes hold a block's 32 features
-      uint32_t tg = top_inside(P, c, g), tu = top_inside(P, c, u);
+      uint32_t tg = top_inside<false>(P, c, g), tu = top_inside<false>(P, c, u);
 #pragma unroll
       for (int o = 1; o < 8; o *= 2) {
         tg = max(tg, (uint32_t)__shfl_xor((int)tg, o));

@@ -30,11 +30,33 @@ __device__ __forceinline__ float block_step(uint32_t b) {
   return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7fc00000u : b << 23);
 }
 
-// The nearest whole number, ties to even, of magnitude up to 127 (values past
-// 127.5 steps are less than a step off; 0 for what a block that is not finite holds).
-__device__ __forceinline__ int block_code(float v, float inverse) {
-  const float t = v * inverse;
-  return inverse == 0.0f ? 0 : (int)rintf(fminf(fmaxf(t, -127.0f), 127.0f));
+
+// Four codes of a block in a word: the nearest whole numbers, ties to even, of
+// magnitude up to 127 (values past 127.5 steps are less than a step off).  Values
+// are first held to 127 steps (0 in a block that is not finite, whose codes are 0);
+// v / step + 1.5 * 2^23, rounded once, then has the code in its lowest byte.
+struct BlockCode {
+  float inverse, most;
+  __device__ __forceinline__ explicit BlockCode(uint32_t b)
+      : inverse(block_inverse(b)), most(b == 255u ? 0.0f : 127.0f * block_step(b)) {}
+  __device__ __forceinline__ uint32_t one(float v) const {
+    return __float_as_uint(fmaf(__builtin_amdgcn_fmed3f(v, -most, most), inverse, 12582912.0f));
+  }
+  __device__ __forceinline__ uint32_t operator()(float a, float b, float c, float d) const {
+    const uint32_t ab = __builtin_amdgcn_perm(one(b), one(a), 0x0c0c0400u);
+    const uint32_t cd = __builtin_amdgcn_perm(one(d), one(c), 0x0c0c0400u);
+    return __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+  }
+};
+
+// The larger of a lane's value and that of the lane 32 (16) further on or back.
+__device__ __forceinline__ uint32_t max_over_32(uint32_t v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max((uint32_t)s[0], (uint32_t)s[1]);
+}
+__device__ __forceinline__ uint32_t max_over_16(uint32_t v) {
+  const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return max((uint32_t)s[0], (uint32_t)s[1]);
 }
 
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {

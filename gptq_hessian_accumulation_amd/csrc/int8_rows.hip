@@ -22,13 +22,13 @@ namespace hess {
 namespace {
 
 // 8 codes to p (any alignment), the first `left` of them inside what is written.
-__device__ __forceinline__ void store8(int8_t* p, int64_t left, const int (&q)[8]) {
+__device__ __forceinline__ void store8(int8_t* p, int64_t left, const uint2& q) {
   if (left >= 8) {
-    *reinterpret_cast<uint2_at1*>(p) = uint2{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
+    *reinterpret_cast<uint2_at1*>(p) = q;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < left) p[j] = (int8_t)q[j];
+      if (j < left) p[j] = (int8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
   }
 }
 
@@ -95,7 +95,7 @@ template <int DT, int T, int P> __global__ void __launch_bounds__(T) quantize_ro
     int q[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) q[j] = code(w[j]);
-    store8(c + at, R.pad - at, q);
+    store8(c + at, R.pad - at, uint2{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])});
   };
 #pragma unroll
   for (int i = 0; i < P; ++i) {
@@ -122,10 +122,8 @@ template <int DT> __global__ void __launch_bounds__(256) quantize_blocks(Int8Row
     top = max(top, (uint32_t)__shfl_xor((int)top, 1));
     top = max(top, (uint32_t)__shfl_xor((int)top, 2));
     const uint32_t b = block_exponent(top);
-    const float inverse = block_inverse(b);
-    int q[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = block_code(v[j], inverse);
+    const BlockCode code(b);
+    const uint2 q{code(v[0], v[1], v[2], v[3]), code(v[4], v[5], v[6], v[7])};
     if (at < R.pad) store8(R.codes + row * R.ldc + at, R.pad - at, q);
     if ((i & 3) == 0) static_cast<uint8_t*>(R.scale)[row * groups + at / 32] = (uint8_t)b;
   }
