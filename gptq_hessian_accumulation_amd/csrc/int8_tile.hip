@@ -28,7 +28,7 @@ namespace {
 
 constexpr uint32_t kOOB = 0x80000000u;  // an offset past any descriptor's range
 constexpr int64_t kAll = 0x7fffffff;
-constexpr int kStages = 5, kAhead = 4;
+constexpr int kUnits = 5;
 
 __device__ __forceinline__ i32x4 mma_i8(const u32x4& a, const u32x4& b, const i32x4& c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
@@ -47,9 +47,9 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) i
   constexpr int kColWaves = Edge == 256 ? 4 : 2;    // the tile's waves are 2 x kColWaves
   constexpr int kCols = Edge / kColWaves;           // columns of a wave
   constexpr int kBm = Edge / 32, kBn = kCols / 16;  // 16-wide blocks of a wave
-  constexpr int kPanel = Edge * 64, kStage = 2 * kPanel;
-  constexpr int kLoads = kPanel / 1024 / (2 * kColWaves);  // 1-KB loads per wave, panel and stage
-  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+  constexpr int kUnit = Edge * 128;
+  constexpr int kLoads = kUnit / 1024 / (2 * kColWaves);  // 1-KB loads per wave and unit
+  __shared__ __attribute__((aligned(1024))) char lds[kUnits * kUnit];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -74,50 +74,51 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) i
   coords(P, t, I, J);
   const int64_t i0 = (int64_t)I * Edge, j0 = (int64_t)J * Edge;
 
-  // Offsets of this wave's loads: load i holds 16 rows, lane l row l / 4 of
-  // them and position l % 4, where chunk (l % 4) ^ (row / 2 % 4) lives.
-  const int chunk = (lane & 3) ^ ((lane >> 3) & 3);
+  // Offsets of this wave's loads: load i of a unit holds 8 rows, lane l row l / 8
+  // of them and position l % 8, where chunk (l % 8) ^ (row / 2 % 8) lives.
+  const int chunk = (lane & 7) ^ (lane >> 4);  // of even loads; of odd ones ^ 4
   uint32_t voffA[kLoads], voffB[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int row = 16 * (kLoads * wave + i) + (lane >> 2);
-    voffA[i] = i0 + row < P.M ? (uint32_t)(row * P.lda + chunk * 16) : kOOB;
-    voffB[i] = j0 + row < P.N ? (uint32_t)(row * P.ldb + chunk * 16) : kOOB;
+    const int row = 8 * (kLoads * wave + i) + (lane >> 3);
+    const int c = chunk ^ (4 * (i & 1));  // (kLoads is even: so is kLoads * wave)
+    voffA[i] = i0 + row < P.M ? (uint32_t)(row * P.lda + c * 16) : kOOB;
+    voffB[i] = j0 + row < P.N ? (uint32_t)(row * P.ldb + c * 16) : kOOB;
   }
   const uint64_t baseA = reinterpret_cast<uint64_t>(P.a) + (uint64_t)(i0 * P.lda);
   const uint64_t baseB = reinterpret_cast<uint64_t>(P.b) + (uint64_t)(j0 * P.ldb);
   struct Next {
-    u32x4 ra, rb;
+    u32x4 r;
     int lim;  // chunks of K left
   };
-  auto describe = [&](int j) {
+  auto describe = [&](uint64_t base, int j) {
     Next d;
-    const int64_t k0 = (int64_t)j * 64;
-    const bool live = j < it1;
+    const int64_t k0 = (int64_t)j * 128;
     d.lim = (int)((P.K - k0 + 15) / 16);
-    d.ra = rsrc_words(baseA + (uint64_t)k0, live ? kAll : 0);
-    d.rb = rsrc_words(baseB + (uint64_t)k0, live ? kAll : 0);
+    d.r = rsrc_words(base + (uint64_t)k0, j < it1 ? kAll : 0);
     return d;
   };
-  // load i of the wave's 2 kLoads of one stage
-  auto load1 = [&](uint32_t stage, const Next& d, int i) {
-    const bool isA = i < kLoads;
-    const int q = isA ? i : i - kLoads;
-    const uint32_t off = chunk < d.lim ? (isA ? voffA[q] : voffB[q]) : kOOB;
-    lds_dma16(isA ? d.ra : d.rb, off, stage + (isA ? 0 : kPanel) + (uint32_t)((kLoads * wave + q) * 1024));
+  // load i of the wave's kLoads of one unit
+  auto load1 = [&](uint32_t unit, const Next& d, const uint32_t (&voff)[kLoads], int i) {
+    const uint32_t off = (chunk ^ (4 * (i & 1))) < d.lim ? voff[i] : kOOB;
+    lds_dma16(d.r, off, lds0 + unit + (uint32_t)((kLoads * wave + i) * 1024));
   };
-  auto load_stage = [&](uint32_t stage, int j) {
-    const Next d = describe(j);
+  auto load_unit = [&](uint32_t unit, uint64_t base, const uint32_t (&voff)[kLoads], int j) {
+    const Next d = describe(base, j);
 #pragma unroll
-    for (int i = 0; i < 2 * kLoads; ++i) load1(stage, d, i);
+    for (int i = 0; i < kLoads; ++i) load1(unit, d, voff, i);
   };
 
-  // Operand block m of a wave's share: lane l holds row l % 16 of the block,
-  // the l / 16-th chunk of K.
-  const int in_block = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
-  const int posA = wr * (Edge / 2) * 64 + in_block, posB = kPanel + wc * kCols * 64 + in_block;
-  auto read_a = [&](uint32_t stage, int m) { return *reinterpret_cast<const u32x4*>(lds + stage + posA + m * 1024); };
-  auto read_b = [&](uint32_t stage, int n) { return *reinterpret_cast<const u32x4*>(lds + stage + posB + n * 1024); };
+  // Operand block m of a wave's share: lane l holds row l % 16 of the block, chunk
+  // l / 16 of the stage's half h (whose position differs in bit 2: 64 bytes).
+  const int in_block = (lane & 15) * 128 + (((lane >> 4) ^ ((lane & 15) >> 1)) << 4);
+  const int posA = wr * (Edge / 2) * 128 + in_block, posB = wc * kCols * 128 + in_block;
+  auto read_a = [&](uint32_t unit, int h, int m) {
+    return *reinterpret_cast<const u32x4*>(lds + unit + (posA ^ (64 * h)) + m * 2048);
+  };
+  auto read_b = [&](uint32_t unit, int h, int n) {
+    return *reinterpret_cast<const u32x4*>(lds + unit + (posB ^ (64 * h)) + n * 2048);
+  };
 
   i32x4 acc[kBm][kBn];
 #pragma unroll
@@ -125,60 +126,70 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) i
 #pragma unroll
     for (int n = 0; n < kBn; ++n) acc[m][n] = i32x4{};
 
-  // Iteration j on the stage at cur (its first A blocks are in a, its B blocks
-  // in b), group by group: the matrix instructions of one A block, the read of
-  // the A block kRot groups later (of the next stage at the end), a read of the
-  // next stage's B (into c) and a load of iteration j + 4.  Before the first read
-  // of the next stage the wave waits for its own loads of it and meets the
-  // others (the next stage is then complete, and nobody reads the one before cur).
+  // Stage j, half h, group by group: the matrix instructions of one A block, the
+  // read of the A block kRot groups later (of the other half, or of the next stage,
+  // at the end), reads of the following half's B (into c), and one load.  In half 0
+  // the loads are of A of stage j + 2.  In half 1, once its last block of the
+  // stage is read, the wave waits for its own loads of the next stage and meets the
+  // others: the next stage is then complete and nobody reads this one, whose first
+  // unit takes B of stage j + 2.
   constexpr int kRot = kBm < 4 ? kBm : 4;
-  constexpr int kMeet = kBm - 6 > 0 ? kBm - 6 : 0;
-  u32x4 a[kRot];
-  auto step = [&](uint32_t cur, uint32_t nxt, uint32_t target, int j, const u32x4 (&b)[kBn], u32x4 (&c)[kBn]) {
-    const Next d = describe(j + kAhead);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int m = 0; m < kBm; ++m) {
-      if (m == kMeet) {
-        __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 2)));
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int n = 0; n < kBn; ++n) acc[m][n] = mma_i8(b[n], a[m % kRot], acc[m][n]);
-      a[m % kRot] = m + kRot < kBm ? read_a(cur, m + kRot) : read_a(nxt, m + kRot - kBm);
-      if (m >= kMeet && m < kMeet + kRot) {
-        c[m - kMeet] = read_b(nxt, m - kMeet);
-        load1(lds0 + target, d, m - kMeet);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
+  constexpr int kMeet = kBm - kRot;
+  static_assert(kLoads <= kRot && kBn == kRot, "one load and one read of B in each of kRot groups");
+  u32x4 a[kRot], b[kBn], c[kBn];
+  uint32_t s0 = 0;  // the unit of A of this stage; those of B, of the next stage and of A of the one after follow
+  auto unit_at = [&](int k) {
+    const uint32_t u = s0 + k * kUnit;
+    return u >= kUnits * kUnit ? u - kUnits * kUnit : u;
   };
-  static_assert(2 * kLoads == kRot && kBn == kRot, "one load and one read of B in each of kRot groups");
 
-#pragma unroll
-  for (int q = 0; q < kAhead; ++q) load_stage(lds0 + q * kStage, it0 + q);
-  __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 1)));
+  load_unit(0, baseA, voffA, it0);
+  load_unit(kUnit, baseB, voffB, it0);
+  load_unit(2 * kUnit, baseA, voffA, it0 + 1);
+  load_unit(3 * kUnit, baseB, voffB, it0 + 1);
+  __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads));
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
-  u32x4 b[kBn], c[kBn];
 #pragma unroll
-  for (int q = 0; q < kRot; ++q) a[q] = read_a(0, q);
+  for (int q = 0; q < kRot; ++q) a[q] = read_a(0, 0, q);
 #pragma unroll
-  for (int q = 0; q < kBn; ++q) b[q] = read_b(0, q);
-  // two iterations a trip (two sets of B registers); an extra iteration
-  // multiplies zeros
-  uint32_t cur = 0, nxt = kStage, ld = kAhead * kStage;
-  auto rotate = [&] {
-    cur = nxt;
-    nxt = nxt + kStage == kStages * kStage ? 0u : nxt + kStage;
-    ld = ld + kStage == kStages * kStage ? 0u : ld + kStage;
-  };
-  for (int j = it0; j < it1; j += 2) {
-    step(cur, nxt, ld, j, b, c);
-    rotate();
-    step(cur, nxt, ld, j + 1, c, b);
-    rotate();
+  for (int q = 0; q < kBn; ++q) b[q] = read_b(kUnit, 0, q);
+  for (int j = it0; j < it1; ++j) {
+    const uint32_t uB = unit_at(1), nA = unit_at(2), nB = unit_at(3), far = unit_at(4);
+    {
+      const Next d = describe(baseA, j + 2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < kBm; ++m) {
+#pragma unroll
+        for (int n = 0; n < kBn; ++n) acc[m][n] = mma_i8(b[n], a[m % kRot], acc[m][n]);
+        a[m % kRot] = m + kRot < kBm ? read_a(s0, 0, m + kRot) : read_a(s0, 1, m + kRot - kBm);
+        if (m >= kMeet) c[m - kMeet] = read_b(uB, 1, m - kMeet);
+        if (m < kLoads) load1(far, d, voffA, m);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    {
+      const Next d = describe(baseB, j + 2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < kBm; ++m) {
+        if (m == kMeet) {
+          __builtin_amdgcn_s_waitcnt(0x0070 | kLoads);  // all but A of stage j + 2, and the wave's own reads
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int n = 0; n < kBn; ++n) acc[m][n] = mma_i8(c[n], a[m % kRot], acc[m][n]);
+        a[m % kRot] = m + kRot < kBm ? read_a(s0, 1, m + kRot) : read_a(nA, 0, m + kRot - kBm);
+        if (m >= kMeet) {
+          b[m - kMeet] = read_b(nB, 0, m - kMeet);
+          if (m - kMeet < kLoads) load1(s0, d, voffB, m - kMeet);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    s0 = nA;
   }
   // the trailing loads write LDS: they end before the workgroup does
   __builtin_amdgcn_s_waitcnt(0x0070);
@@ -266,9 +277,9 @@ template <int DT> void launch_type(const Int8Gemm& g, int edge, hipStream_t stre
 int slots_of(int edge) { return edge == 256 ? 256 : edge == 128 ? 512 : 1024; }
 double stage_us(int edge, int groups) {
   const int each = (groups + 255) / 256;  // on the busiest CU
-  if (edge == 256) return 0.53 + 0.25 * groups / 256;
-  if (edge == 128) return each > 1 ? 0.28 * each : 0.25 + 0.07 * groups / 256;
-  return std::max(0.15, 0.12 * each);
+  if (edge == 256) return 1.06 + 0.50 * groups / 256;
+  if (edge == 128) return each > 1 ? 0.56 * each : 0.50 + 0.14 * groups / 256;
+  return std::max(0.30, 0.24 * each);
 }
 
 // The schedule for tiles of one edge, and its estimated time in us: whole tiles
@@ -279,7 +290,7 @@ double schedule_for(Int8Gemm& g, int edge) {
   g.tm = (int)((g.M + edge - 1) / edge);
   g.tn = (int)((g.N + edge - 1) / edge);
   g.ntiles = g.tm * g.tn;
-  g.niter = (int)((g.K + 63) / 64);
+  g.niter = (int)((g.K + 127) / 128);
   g.full = g.ntiles;
   g.parts = 1;
   g.part_len = g.niter;
@@ -288,7 +299,7 @@ double schedule_for(Int8Gemm& g, int edge) {
   double us = (double)(g.ntiles / slots) * (g.niter * stage_us(edge, slots) + enter);
   if (tail == 0) return us;
   double best = 1e30;
-  for (int parts = 1; parts <= std::max(1, std::min(2 * slots / tail, g.niter / 4)); ++parts) {
+  for (int parts = 1; parts <= std::max(1, std::min(2 * slots / tail, g.niter / 2)); ++parts) {
     const int len = (g.niter + parts - 1) / parts, work = tail * parts;
     double t = work / slots * (len * stage_us(edge, slots) + enter);
     if (work % slots > 0) t += len * stage_us(edge, work % slots) + enter;
