@@ -32,11 +32,16 @@ __device__ __forceinline__ void store8(int8_t* p, int64_t left, const uint2& q) 
   }
 }
 
+// i / per, by 32-bit division where that is enough
+__device__ __forceinline__ int64_t row_of(int64_t i, int64_t per) {
+  return ((uint64_t)(i | per) >> 32) == 0 ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
+}
+
 // Matrix m of a set of copies: 16 codes a thread, from thread `first` of `all`.
 __device__ __forceinline__ void pack_range(const PackCodes& P, int m, int64_t first, int64_t all) {
   const int64_t per = P.pad / 16, total = P.rows[m] * per;
   for (int64_t i = first; i < total; i += all) {
-    const int64_t r = i / per, c = (i - r * per) * 16;
+    const int64_t r = row_of(i, per), c = (i - r * per) * 16;
     const int8_t* p = P.src[m] + r * P.ld[m] + c;
     u32x4 v{};
     if (c + 16 <= P.cols) {
@@ -114,7 +119,7 @@ template <int DT> __global__ void __launch_bounds__(256) quantize_blocks(Int8Row
   typedef typename Elem<DT>::type E;
   // (whole waves run: total is a whole number of groups of four lanes)
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / (groups * 4);
+    const int64_t row = row_of(i, groups * 4);
     const int64_t at = (i - row * groups * 4) * 8;
     float v[8] = {};
     if (at < R.d) load8(static_cast<const E*>(R.x) + row * R.ldx + at, R.d - at, v);
@@ -130,35 +135,37 @@ template <int DT> __global__ void __launch_bounds__(256) quantize_blocks(Int8Row
 }
 
 // Codes back to values of DT (16-bit types: rounded to nearest even; exact for
-// blocks), 8 a thread, from thread `first` of `all`; columns d .. pad - 1 become
-// zeros.
+// blocks), 16 bytes of them a thread (float32 at 16384 x 4096: 32 bytes took 91 us,
+// 3.7 TB/s), from thread `first` of `all`; columns d .. pad - 1 become zeros.
 template <int DT, int Block>
 __device__ __forceinline__ void dequantize_range(const Int8Rows& R, int64_t first, int64_t all) {
   typedef typename Elem<DT>::type E;
-  typedef E E8 __attribute__((ext_vector_type(8)));
-  typedef E8 E8u __attribute__((aligned(sizeof(E))));
-  const int64_t groups = (R.d + 31) / 32, per = (R.pad + 7) / 8, total = R.n * per;
+  constexpr int N = 16 / sizeof(E);
+  typedef E EN __attribute__((ext_vector_type(N)));
+  typedef EN ENu __attribute__((aligned(sizeof(E))));
+  typedef uint32_t Words __attribute__((ext_vector_type(N / 4), aligned(1)));
+  const int64_t groups = (R.d + 31) / 32, per = (R.pad + N - 1) / N, total = R.n * per;
   for (int64_t i = first; i < total; i += all) {
-    const int64_t row = i / per, at = (i - row * per) * 8;
+    const int64_t row = row_of(i, per), at = (i - row * per) * N;
     float step = 0.0f;
     if constexpr (Block == 0) step = static_cast<const float*>(R.scale)[row];
     else if (at < R.d) step = block_step(static_cast<const uint8_t*>(R.scale)[row * groups + at / 32]);
     const int8_t* c = R.codes + row * R.ldc + at;
     E* o = static_cast<E*>(const_cast<void*>(R.x)) + row * R.ldx + at;
-    E8 v;
-    if (at + 8 <= R.d) {
-      const uint2 w = *reinterpret_cast<const uint2_at1*>(c);
+    EN v;
+    if (at + N <= R.d) {
+      const Words w = *reinterpret_cast<const Words*>(c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = from_f32<E>(unpack(j < 4 ? w.x : w.y, j & 3) * step);
+      for (int j = 0; j < N; ++j) v[j] = from_f32<E>(unpack(w[j / 4], j & 3) * step);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = from_f32<E>(at + j < R.d ? (float)c[j] * step : 0.0f);
+      for (int j = 0; j < N; ++j) v[j] = from_f32<E>(at + j < R.d ? (float)c[j] * step : 0.0f);
     }
-    if (at + 8 <= R.pad) {
-      *reinterpret_cast<E8u*>(o) = v;
+    if (at + N <= R.pad) {
+      *reinterpret_cast<ENu*>(o) = v;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < N; ++j)
         if (at + j < R.pad) o[j] = v[j];
     }
   }
@@ -180,7 +187,7 @@ template <int DT> __global__ void __launch_bounds__(256) grad_operands(GradOpera
   }
   const int64_t per = (G.pad + 7) / 8, total = G.n * per;
   for (int64_t i = first; i < total; i += all) {
-    const int64_t row = i / per, at = (i - row * per) * 8;
+    const int64_t row = row_of(i, per), at = (i - row * per) * 8;
     const E* p = static_cast<const E*>(G.src) + row * G.ld + at;
     E* o = static_cast<E*>(G.dst) + row * G.pad + at;
     if (at + 8 <= G.cols) {
@@ -195,18 +202,27 @@ template <int DT> __global__ void __launch_bounds__(256) grad_operands(GradOpera
 
 int grid_of(int64_t threads) { return (int)std::min<int64_t>((threads + 255) / 256, 8192); }
 
+template <int DT, int T, int P> void launch_rows(const Int8Rows& r, const PackCodes& c, hipStream_t stream) {
+  const int64_t most = (int64_t)1 << 20;  // workgroups of a launch (fewer than 2^32 threads)
+  for (int64_t r0 = 0; r0 < r.n; r0 += most) {
+    Int8Rows p = r;
+    p.n = std::min(most, r.n - r0);
+    p.x = static_cast<const char*>(r.x) + r0 * r.ldx * Elem<DT>::size;
+    p.codes = r.codes + r0 * r.ldc;
+    p.scale = static_cast<float*>(r.scale) + r0;
+    const int extra = c.count > 0 && r0 == 0 ? (int)std::min<int64_t>((c.rows[0] * (c.pad / 16) + T - 1) / T, 1024) : 0;
+    quantize_rows<DT, T, P><<<(unsigned)(p.n + extra), T, 0, stream>>>(p, c);
+  }
+}
+
+// As few threads as hold a row in 2 or 4 pieces each: a wave up to 2,048 columns.
 template <int DT> hipError_t quantize_type(const Int8Rows& r, int block, const PackCodes& c, hipStream_t stream) {
   if (block == 0) {
-    const int64_t most = (int64_t)1 << 20;  // workgroups of a launch (fewer than 2^32 threads)
-    for (int64_t r0 = 0; r0 < r.n; r0 += most) {
-      Int8Rows p = r;
-      p.n = std::min(most, r.n - r0);
-      p.x = static_cast<const char*>(r.x) + r0 * r.ldx * Elem<DT>::size;
-      p.codes = r.codes + r0 * r.ldc;
-      p.scale = static_cast<float*>(r.scale) + r0;
-      const int extra = c.count > 0 && r0 == 0 ? (int)std::min<int64_t>((c.rows[0] * (c.pad / 16) + 255) / 256, 1024) : 0;
-      quantize_rows<DT, 256, 2><<<(unsigned)(p.n + extra), 256, 0, stream>>>(p, c);
-    }
+    if (r.d <= 1024) launch_rows<DT, 64, 2>(r, c, stream);
+    else if (r.d <= 2048) launch_rows<DT, 64, 4>(r, c, stream);
+    else if (r.d <= 4096) launch_rows<DT, 256, 2>(r, c, stream);
+    else if (r.d <= 8192) launch_rows<DT, 256, 4>(r, c, stream);
+    else launch_rows<DT, 1024, 2>(r, c, stream);
   } else {
     const int64_t groups = (r.d + 31) / 32, total = r.n * groups * 4;
     quantize_blocks<DT><<<grid_of(total), 256, 0, stream>>>(r, groups, total);
@@ -215,7 +231,8 @@ template <int DT> hipError_t quantize_type(const Int8Rows& r, int block, const P
 }
 
 template <int DT> hipError_t dequantize_type(const Int8Rows& r, int block, hipStream_t stream) {
-  const int grid = grid_of(r.n * ((r.pad + 7) / 8));
+  const int64_t piece = 16 / Elem<DT>::size;
+  const int grid = grid_of(r.n * ((r.pad + piece - 1) / piece));
   if (block == 0) dequantize<DT, 0><<<grid, 256, 0, stream>>>(r);
   else dequantize<DT, 32><<<grid, 256, 0, stream>>>(r);
   return hipGetLastError();

@@ -28,7 +28,6 @@ namespace {
 
 constexpr uint32_t kOOB = 0x80000000u;  // an offset past any descriptor's range
 constexpr int64_t kAll = 0x7fffffff;
-constexpr int kUnits = 5;
 
 __device__ __forceinline__ i32x4 mma_i8(const u32x4& a, const u32x4& b, const i32x4& c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
@@ -42,8 +41,9 @@ __device__ __forceinline__ void coords(const Int8Gemm& P, int t, int& I, int& J)
   I = grp * 8 + in - J * rows;
 }
 
-template <int DT, int Edge>
-__global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) int8_tile(Int8Gemm P) {
+template <int DT, int Edge, int kUnits>
+__global__ void __launch_bounds__(Edge == 256 ? 512 : 256, kUnits > 5 ? 1 : Edge == 64 ? 4 : 2) int8_tile(Int8Gemm P) {
+  constexpr int kAhead = (kUnits - 1) / 2;          // stages that are loaded ahead
   constexpr int kColWaves = Edge == 256 ? 4 : 2;    // the tile's waves are 2 x kColWaves
   constexpr int kCols = Edge / kColWaves;           // columns of a wave
   constexpr int kBm = Edge / 32, kBn = kCols / 16;  // 16-wide blocks of a wave
@@ -129,25 +129,37 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) i
   // Stage j, half h, group by group: the matrix instructions of one A block, the
   // read of the A block kRot groups later (of the other half, or of the next stage,
   // at the end), reads of the following half's B (into c), and one load.  In half 0
-  // the loads are of A of stage j + 2.  In half 1, once its last block of the
+  // the loads are of A of stage j + kAhead.  In half 1, once its last block of the
   // stage is read, the wave waits for its own loads of the next stage and meets the
   // others: the next stage is then complete and nobody reads this one, whose first
-  // unit takes B of stage j + 2.
+  // unit takes B of stage j + kAhead.
   constexpr int kRot = kBm < 4 ? kBm : 4;
   constexpr int kMeet = kBm - kRot;
   static_assert(kLoads <= kRot && kBn == kRot, "one load and one read of B in each of kRot groups");
   u32x4 a[kRot], b[kBn], c[kBn];
-  uint32_t s0 = 0;  // the unit of A of this stage; those of B, of the next stage and of A of the one after follow
+  uint32_t s0 = 0;  // the unit of A of this stage; those of B and of the next stages follow
   auto unit_at = [&](int k) {
     const uint32_t u = s0 + k * kUnit;
     return u >= kUnits * kUnit ? u - kUnits * kUnit : u;
   };
 
-  load_unit(0, baseA, voffA, it0);
-  load_unit(kUnit, baseB, voffB, it0);
-  load_unit(2 * kUnit, baseA, voffA, it0 + 1);
-  load_unit(3 * kUnit, baseB, voffB, it0 + 1);
-  __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads));
+  // the scales of the lane's outputs, on their way before the first codes (rows and
+  // columns past the matrix take its last one's)
+  float sa[kBm], sb[kBn / 2][8];
+#pragma unroll
+  for (int m = 0; m < kBm; ++m) sa[m] = P.sa[min(i0 + wr * (Edge / 2) + (lane & 15) + 16 * m, P.M - 1)];
+#pragma unroll
+  for (int n = 0; n < kBn / 2; ++n)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      sb[n][j] = P.sb[min(j0 + wc * kCols + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5) + 32 * n + j, P.N - 1)];
+
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) {
+    load_unit(2 * q * kUnit, baseA, voffA, it0 + q);
+    load_unit((2 * q + 1) * kUnit, baseB, voffB, it0 + q);
+  }
+  __builtin_amdgcn_s_waitcnt(vm_wait(2 * kLoads * (kAhead - 1)));
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -155,9 +167,9 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) i
 #pragma unroll
   for (int q = 0; q < kBn; ++q) b[q] = read_b(kUnit, 0, q);
   for (int j = it0; j < it1; ++j) {
-    const uint32_t uB = unit_at(1), nA = unit_at(2), nB = unit_at(3), far = unit_at(4);
+    const uint32_t uB = unit_at(1), nA = unit_at(2), nB = unit_at(3), far = unit_at(kUnits - 1);
     {
-      const Next d = describe(baseA, j + 2);
+      const Next d = describe(baseA, j + kAhead);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 0; m < kBm; ++m) {
@@ -170,12 +182,13 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) i
       }
     }
     {
-      const Next d = describe(baseB, j + 2);
+      const Next d = describe(baseB, j + kAhead);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 0; m < kBm; ++m) {
         if (m == kMeet) {
-          __builtin_amdgcn_s_waitcnt(0x0070 | kLoads);  // all but A of stage j + 2, and the wave's own reads
+          // all loads but those of later stages than the next, and the wave's own reads
+          __builtin_amdgcn_s_waitcnt(vm_wait((2 * kAhead - 3) * kLoads) & ~0x0f00);
           __builtin_amdgcn_s_barrier();
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -211,15 +224,9 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) i
   int lv = lane;
   asm volatile("" : "+v"(lv));  // the offsets are computed here, not kept through the loop
   const int64_t c0 = j0 + wc * kCols + 16 * ((lv >> 4) & 1) + 8 * (lv >> 5);
-  float sb[kBn / 2][8];
-#pragma unroll
-  for (int n = 0; n < kBn / 2; ++n)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sb[n][j] = c0 + 32 * n + j < P.N ? P.sb[c0 + 32 * n + j] : 0.0f;
 #pragma unroll
   for (int m = 0; m < kBm; ++m) {
     const int64_t r = i0 + wr * (Edge / 2) + (lv & 15) + 16 * m;
-    const float sa = r < P.M ? P.sa[r] : 0.0f;
     T* row = static_cast<T*>(P.y) + r * P.ldy;
 #pragma unroll
     for (int n = 0; n < kBn; n += 2) {
@@ -227,8 +234,8 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) i
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const auto s = __builtin_amdgcn_permlane16_swap((uint32_t)acc[m][n][j], (uint32_t)acc[m][n + 1][j], false, false);
-        v[j] = scale_sum((int)s[0], sb[n / 2][j], sa);
-        v[4 + j] = scale_sum((int)s[1], sb[n / 2][4 + j], sa);
+        v[j] = scale_sum((int)s[0], sb[n / 2][j], sa[m]);
+        v[4 + j] = scale_sum((int)s[1], sb[n / 2][4 + j], sa[m]);
       }
       const int64_t col = c0 + 16 * n;
       if (r < P.M && col < P.N) store_n(row + col, v, (int)min((int64_t)8, P.N - col));
@@ -258,9 +265,15 @@ template <int DT, int Edge> __global__ void __launch_bounds__(256) int8_join(Int
   store_n(static_cast<T*>(P.y) + r * P.ldy + c, v, (int)min((int64_t)4, P.N - c));
 }
 
+// Up to one workgroup (edge 64: two) a CU: they are bound by the loads' latency,
+// and LDS has room for four stages ahead instead of two.
 template <int DT, int Edge> void launch_edge(const Int8Gemm& g, hipStream_t stream) {
-  const int tail = g.ntiles - g.full;
-  int8_tile<DT, Edge><<<g.full + tail * g.parts, Edge == 256 ? 512 : 256, 0, stream>>>(g);
+  const int tail = g.ntiles - g.full, groups = g.full + tail * g.parts;
+  constexpr int kDeep = Edge == 256 ? 5 : 9;
+  if (groups <= (Edge == 64 ? 512 : 256))
+    int8_tile<DT, Edge, kDeep><<<groups, Edge == 256 ? 512 : 256, 0, stream>>>(g);
+  else
+    int8_tile<DT, Edge, 5><<<groups, Edge == 256 ? 512 : 256, 0, stream>>>(g);
   if (tail > 0) int8_join<DT, Edge><<<dim3(tail, Edge * (Edge / 4) / 256), 256, 0, stream>>>(g);
 }
 
@@ -277,9 +290,9 @@ template <int DT> void launch_type(const Int8Gemm& g, int edge, hipStream_t stre
 int slots_of(int edge) { return edge == 256 ? 256 : edge == 128 ? 512 : 1024; }
 double stage_us(int edge, int groups) {
   const int each = (groups + 255) / 256;  // on the busiest CU
-  if (edge == 256) return 1.06 + 0.50 * groups / 256;
-  if (edge == 128) return each > 1 ? 0.56 * each : 0.50 + 0.14 * groups / 256;
-  return std::max(0.30, 0.24 * each);
+  if (edge == 256) return 0.95 + 0.50 * groups / 256;
+  if (edge == 128) return each > 1 ? 0.45 * each : 0.48 + 0.16 * groups / 256;
+  return std::max(0.32, 0.165 * each);
 }
 
 // The schedule for tiles of one edge, and its estimated time in us: whole tiles
