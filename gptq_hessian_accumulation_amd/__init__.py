@@ -144,6 +144,8 @@ def _load():
         "hess_distill_topk_backward": (c_int, [vp, vp, i64, c_int, i64, i64, vp, c_int, i64, vp, c_int, i64, c_int,
                                                vp, ctypes.c_float, vp, vp, i64, vp]),
         "hess_gated_ffn_preact_i8_cols": (i64, [i64]),
+        "hess_gated_ffn_backward_x8": (c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, c_int, c_int, i64, i64, i64,
+                                               vp, i64, vp, i64, vp, i64, vp, i64, vp]),
         "hess_int8_quantize": (c_int, [vp, i64, c_int, i64, i64, c_int, vp, i64, i64, vp, vp]),
         "hess_int8_dequantize": (c_int, [vp, i64, vp, i64, i64, c_int, vp, i64, c_int, vp]),
         "hess_int8_matmul_workspace": (i64, [i64, i64, i64]),
@@ -643,6 +645,23 @@ def _act_mode(act: str) -> int:
     return mode
 
 
+def _ffn_weights(like, w_gate, w_up, name):
+    """(code, f, d, tensors to keep, (gate, stride, up, stride)) of weights of like's type, for tiles."""
+    code = _float_code(name, like)
+    shape = w_gate.shape
+    if len(shape) != 2 or shape != w_up.shape:
+        raise ValueError("w_gate and w_up must be (f, d) matrices of one shape")
+    for w, t in (("w_gate", w_gate), ("w_up", w_up)):
+        if t.dtype != like.dtype or t.get_device() != like.get_device():
+            raise ValueError(f"{w} must have {name}'s dtype and device")
+    f, d = shape
+    step = 4 if code == HESS_F32 else 8
+    step = step if d % step == 0 else 1
+    wg, gp, ldg = _rows(w_gate, step)
+    wu, up, ldu = _rows(w_up, step)
+    return code, f, d, (wg, wu), (gp, ldg, up, ldu)
+
+
 def _ffn_args(x, w_gate, w_up, any_rows=0):
     """(code, n, d, f, tensors to keep, (x, stride, gate, stride, up, stride) for the library).
 
@@ -722,7 +741,7 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     Sums are float32.  For 16-bit types the gradients of the two pre-activations are rounded to that type
     before the products, which leaves the results about 1.4 times as far off as their own last rounding;
     float32 inputs have no such rounding.  ``preact`` from ``save=torch.int8`` gives the derivatives at
-    what its codes stand for.  ``x`` may be an 8-bit checkpoint too (Int8Rows, from quantize_int8), which
+    what its codes stand for.  ``x`` may be an 8-bit checkpoint too (quantize_int8 with ``block=32``), which
     dw_gate and dw_up then take, or None where they are not needed.
     """
     if stream is not None:  # the call, its temporaries and its outputs belong to it
@@ -730,20 +749,25 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
             return gated_ffn_backward(dh, x, w_gate, w_up, preact, act, need_x, need_w, workspace)
     lib = _load()
     mode = _act_mode(act)
-    if isinstance(x, Int8Rows):
-        _int8_args("x", x)
-        if tuple(x.codes.shape) != (*dh.shape[:-1], w_gate.shape[-1]):
-            raise ValueError(f"x must hold {(*dh.shape[:-1], w_gate.shape[-1])} codes")
-        x = dequantize_int8(x, dtype=dh.dtype) if need_w else None
-    elif x is None and need_w:
-        raise ValueError("dw_gate and dw_up need x")
-    if x is None:  # only its shape matters
-        code, n, d, f, keep, (_, _, gp, ldg, up, ldu) = _ffn_args(dh.new_empty((0, w_gate.shape[-1])), w_gate, w_up)
-        x, xp, ldx, n = dh.new_empty(1).expand(*dh.shape[:-1], d), None, d, dh.shape[:-1].numel()
+    x8 = None
+    if isinstance(x, Int8Rows) or x is None:
+        if need_w and x is None:
+            raise ValueError("dw_gate and dw_up need x")
+        code, f, d, keep, (gp, ldg, up, ldu) = _ffn_weights(dh, w_gate, w_up, "dh")
+        lead = dh.shape[:-1]
+        xp, ldx, n = None, d, lead.numel()
+        if dh.dim() < 1 or dh.shape[-1] != f:
+            raise ValueError(f"dh must be (..., {f})")
+        if x is not None:
+            keep_x, lead_x, _, dx8, xp, ldx, x8 = _int8_args("x", x, 32)
+            if lead_x != lead or dx8 != d:
+                raise ValueError(f"x must hold {(*lead, d)} codes, not {tuple(x.codes.shape)}")
+        x = dh
     else:
         code, n, d, f, keep, (xp, ldx, gp, ldg, up, ldu) = _ffn_args(x, w_gate, w_up)
-    if tuple(dh.shape) != (*x.shape[:-1], f) or dh.dtype != x.dtype or dh.device != x.device:
-        raise ValueError(f"dh must be a {x.dtype} {(*x.shape[:-1], f)} tensor on {x.device}")
+        lead = x.shape[:-1]
+        if tuple(dh.shape) != (*lead, f) or dh.dtype != x.dtype or dh.device != x.device:
+            raise ValueError(f"dh must be a {x.dtype} {(*lead, f)} tensor on {x.device}")
     in8 = preact.dtype == torch.int8
     cols = lib.hess_gated_ffn_preact_i8_cols(f) if in8 else 2 * (-(-f // 8) * 8)
     if tuple(preact.shape) != (n, cols) or not (in8 or preact.dtype in (torch.float32, x.dtype)) \
@@ -754,15 +778,18 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     elif preact.dtype == torch.float32:
         mode |= _PREACT_F32
     dh2, dhp, lddh = _rows(dh.reshape(-1, f) if dh.dim() != 2 else dh)
-    dx = x.new_empty(x.shape) if need_x else None
+    dx = x.new_empty((*lead, d)) if need_x else None
     dwg = x.new_empty((f, d)) if need_w else None
     dwu = x.new_empty((f, d)) if need_w else None
-    wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 1), x)
-    rc = lib.hess_gated_ffn_backward(dhp if n > 0 else None, lddh, xp if n > 0 else None, ldx, gp, ldg, up, ldu,
-                                     preact.data_ptr() if n > 0 else None, code, mode, n, d, f,
-                                     dx.data_ptr() if need_x and n > 0 else None, d,
-                                     dwg.data_ptr() if need_w else None, d, dwu.data_ptr() if need_w else None, d,
-                                     wp, wb, _stream(None, x.get_device()))
+    wp, wb, work = _workspace(workspace, lib.hess_gated_ffn_workspace(n, d, f, code, 1 if x8 is None else 3), x)
+    rest = (gp, ldg, up, ldu, preact.data_ptr() if n > 0 else None, code, mode, n, d, f,
+            dx.data_ptr() if need_x and n > 0 else None, d, dwg.data_ptr() if need_w else None, d,
+            dwu.data_ptr() if need_w else None, d, wp, wb, _stream(None, x.get_device()))
+    if x8 is None:
+        rc = lib.hess_gated_ffn_backward(dhp if n > 0 else None, lddh, xp if n > 0 else None, ldx, *rest)
+    else:
+        rc = lib.hess_gated_ffn_backward_x8(dhp if n > 0 else None, lddh, xp if n > 0 else None, ldx,
+                                            x8 if n > 0 else None, *rest)
     if rc != 0:
         _check(rc)
     return dx, dwg, dwu
@@ -1125,14 +1152,18 @@ def int8_linear_forward(x: torch.Tensor, w: Int8Rows, save: bool = False, out: t
     lead = x.shape[:-1]
     x2, xp, ldx = _rows(x if len(lead) == 1 else x.reshape(-1, d))
     n = x2.shape[0]
-    y = _out("out", out, (*lead, f), x)
-    ldy = y.stride(0) if out is not None and y.dim() == 2 and n > 1 else f
+    ldy = f
+    if out is None:
+        y = x.new_empty((n, f) if len(lead) == 1 else (*lead, f))
+    else:
+        y = _out("out", out, (*lead, f), x)
+        ldy = y.stride(0) if y.dim() == 2 and n > 1 else f
     codes = scale = None
     ldc = 0
     if save:
         codes, ldc = _new_codes(x.shape, n, d, x)
         scale = x.new_empty(n if len(lead) == 1 else lead, dtype=torch.float32)
-    need = lib.hess_int8_linear_workspace(n, d, f, code, 0)
+    need = lib.hess_int8_linear_workspace(n, d, f, code, 4 if save else 0)
     wp, wb, work = _workspace(workspace, need, x) if need else (None, 0, None)
     rc = lib.hess_int8_linear_forward(xp, ldx, code, wp8, ldw, wsp, n, d, f, y.data_ptr(), ldy,
                                       codes.data_ptr() if save and n > 0 else None, ldc,

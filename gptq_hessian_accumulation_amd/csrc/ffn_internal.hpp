@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "int8_internal.hpp"
+
 namespace hess {
 
 enum FfnMode {
@@ -101,8 +103,10 @@ inline int64_t pair8_cols(int64_t f) {
 enum PairType { kPairSame = 0, kPairF32 = 1, kPairI8 = 2 };
 
 // dg = dh u act'(g), du = dh act(g) into the n x 2 fp pair dgu (columns past f zero).
+// The pair in 8 bits: x8, where its x is not null, is restored in the same launch
+// (blocks of 32).
 hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, PairType pair, void* dgu, int64_t n,
-                          int64_t f, int64_t fp, int act, int dtype, hipStream_t stream);
+                          int64_t f, int64_t fp, int act, int dtype, const Int8Rows& x8, hipStream_t stream);
 
 // Zeros rows x cols elements of esize bytes at p (row stride ld elements).
 hipError_t launch_zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int esize, hipStream_t stream);

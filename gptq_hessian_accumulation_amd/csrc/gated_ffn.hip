@@ -69,12 +69,17 @@ __global__ void __launch_bounds__(256) ffn_dgu(const typename Elem<DT>::type* dh
 // The same from the pair in 8 bits (rows of pair8_cols(f) bytes).
 template <int DT>
 __global__ void __launch_bounds__(256) ffn_dgu8(const typename Elem<DT>::type* dh, int64_t lddh, const char* pre,
-                                                int64_t ldp, typename Elem<DT>::type* out, int64_t f, int64_t fp,
-                                                int act) {
+                                                int64_t ldp, typename Elem<DT>::type* out, int64_t n, int64_t f,
+                                                int64_t fp, int act, Int8Rows x8) {
   typedef typename Elem<DT>::type T;
   typedef T T8 __attribute__((ext_vector_type(8)));
   typedef T8 T8u __attribute__((aligned(sizeof(T))));
   const int64_t row = blockIdx.y;
+  if (row >= n) {  // the rows of workgroups behind those of the pair
+    dequantize_range<DT, 32>(x8, ((row - n) * gridDim.x + blockIdx.x) * 256 + threadIdx.x,
+                             (int64_t)(gridDim.y - n) * gridDim.x * 256);
+    return;
+  }
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (c >= fp) return;
   const int64_t fq = (f + 31) / 32 * 32;
@@ -125,15 +130,18 @@ hipError_t launch_dgu(const void* dh, int64_t lddh, const void* preact, void* dg
 
 template <int DT>
 hipError_t launch_dgu8(const void* dh, int64_t lddh, const void* preact, void* dgu, int64_t n, int64_t f, int64_t fp,
-                       int act, hipStream_t stream) {
+                       int act, const Int8Rows& x8, hipStream_t stream) {
   typedef typename Elem<DT>::type T;
   const unsigned gx = (unsigned)((fp / 8 + 255) / 256);
   const int64_t ldp = pair8_cols(f);
-  for (int64_t r0 = 0; r0 < n; r0 += 65535) {
-    const unsigned rows = (unsigned)std::min<int64_t>(65535, n - r0);
-    ffn_dgu8<DT><<<dim3(gx, rows), 256, 0, stream>>>(static_cast<const T*>(dh) + r0 * lddh, lddh,
-                                                     static_cast<const char*>(preact) + r0 * ldp, ldp,
-                                                     static_cast<T*>(dgu) + r0 * 2 * fp, f, fp, act);
+  // x8: 16 bytes a thread, at most 8192 workgroups
+  const int64_t piece = 16 / (int64_t)sizeof(T), threads = x8.x ? x8.n * ((x8.pad + piece - 1) / piece) : 0;
+  const int64_t extra = (std::min<int64_t>((threads + 255) / 256, 8192) + gx - 1) / gx;
+  for (int64_t r0 = 0; r0 < n; r0 += 32768) {
+    const int64_t rows = std::min<int64_t>(32768, n - r0);
+    ffn_dgu8<DT><<<dim3(gx, (unsigned)(rows + (r0 == 0 ? extra : 0))), 256, 0, stream>>>(
+        static_cast<const T*>(dh) + r0 * lddh, lddh, static_cast<const char*>(preact) + r0 * ldp, ldp,
+        static_cast<T*>(dgu) + r0 * 2 * fp, rows, f, fp, act, x8);
   }
   return hipGetLastError();
 }
@@ -232,11 +240,13 @@ int ffn_schedule(FfnGemm& g, int mode, int dtype) {
 }
 
 hipError_t launch_ffn_dgu(const void* dh, int64_t lddh, const void* preact, PairType pair, void* dgu, int64_t n,
-                          int64_t f, int64_t fp, int act, int dtype, hipStream_t stream) {
+                          int64_t f, int64_t fp, int act, int dtype, const Int8Rows& x8, hipStream_t stream) {
+  if (pair != kPairI8 && x8.x)
+    if (const hipError_t e = launch_int8_dequantize(x8, 32, dtype, stream); e != hipSuccess) return e;
   if (pair == kPairI8) {
-    if (dtype == kInF32) return launch_dgu8<kInF32>(dh, lddh, preact, dgu, n, f, fp, act, stream);
-    if (dtype == kInBF16) return launch_dgu8<kInBF16>(dh, lddh, preact, dgu, n, f, fp, act, stream);
-    return launch_dgu8<kInF16>(dh, lddh, preact, dgu, n, f, fp, act, stream);
+    if (dtype == kInF32) return launch_dgu8<kInF32>(dh, lddh, preact, dgu, n, f, fp, act, x8, stream);
+    if (dtype == kInBF16) return launch_dgu8<kInBF16>(dh, lddh, preact, dgu, n, f, fp, act, x8, stream);
+    return launch_dgu8<kInF16>(dh, lddh, preact, dgu, n, f, fp, act, x8, stream);
   }
   const bool pre32 = pair == kPairF32;
   if (dtype == kInF32) return launch_dgu<kInF32, float>(dh, lddh, preact, dgu, n, f, fp, act, stream);

@@ -73,11 +73,13 @@ ProductWork product_work(int64_t n, int64_t d, int64_t f) {
 struct LinearWork {
   int64_t scale, product, total;
 };
-LinearWork linear_work(int64_t n, int64_t d, int64_t f) {
+LinearWork linear_work(int64_t n, int64_t d, int64_t f, bool given) {
   LinearWork w{};
   if (n == 1 && d <= kInt8One) return w;  // quantized by the product itself, or into x_codes
-  w.scale = up(n * code_stride(d), 256);
-  w.product = w.scale + up(4 * n, 256);
+  if (!given) {
+    w.scale = up(n * code_stride(d), 256);
+    w.product = w.scale + up(4 * n, 256);
+  }
   w.total = w.product + product_work(n, d, f).total;
   return w;
 }
@@ -200,12 +202,12 @@ int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const i
 
 int64_t hess_int8_linear_workspace(int64_t n, int64_t d, int64_t f, int dtype, int pass) {
   if (check_product(n, d, f, dtype) != HESS_OK) return -1;
-  if (pass < 0 || pass > 3) {
-    fail(HESS_EINVAL, "pass %d outside [0, 3]", pass);
+  if (pass < 0 || pass > 4) {
+    fail(HESS_EINVAL, "pass %d outside [0, 4]", pass);
     return -1;
   }
   if (n == 0) return 0;
-  return pass == 0 ? linear_work(n, d, f).total : grad_work(n, d, f, dtype, pass & 1, pass & 2).total;
+  return pass == 0 || pass == 4 ? linear_work(n, d, f, pass == 4).total : grad_work(n, d, f, dtype, pass & 1, pass & 2).total;
 }
 
 int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t* w, int64_t ldw, const float* w_scale,
@@ -226,7 +228,7 @@ int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t
     if (!aligned(x_codes, 16) || ldc % 16 != 0) return fail(HESS_EALIGN, "rows of x_codes not 16-byte aligned");
     if (int rc = check_scale("x_scale", x_scale)) return rc;
   }
-  const LinearWork room = linear_work(n, d, f);
+  const LinearWork room = linear_work(n, d, f, x_codes != nullptr);
   if (int rc = check_work(work, work_bytes, room.total)) return rc;
   if (int rc = check_outputs(outs, 3, ins, 3, es, work, room.total)) return rc;
   if (n > kInt8Few && d % 16 == 0 && !rows_of_16(w, ldw, f))

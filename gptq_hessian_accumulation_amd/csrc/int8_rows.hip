@@ -32,11 +32,6 @@ __device__ __forceinline__ void store8(int8_t* p, int64_t left, const uint2& q) 
   }
 }
 
-// i / per, by 32-bit division where that is enough
-__device__ __forceinline__ int64_t row_of(int64_t i, int64_t per) {
-  return ((uint64_t)(i | per) >> 32) == 0 ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
-}
-
 // Matrix m of a set of copies: 16 codes a thread, from thread `first` of `all`.
 __device__ __forceinline__ void pack_range(const PackCodes& P, int m, int64_t first, int64_t all) {
   const int64_t per = P.pad / 16, total = P.rows[m] * per;
@@ -134,42 +129,6 @@ template <int DT> __global__ void __launch_bounds__(256) quantize_blocks(Int8Row
   }
 }
 
-// Codes back to values of DT (16-bit types: rounded to nearest even; exact for
-// blocks), 16 bytes of them a thread (float32 at 16384 x 4096: 32 bytes took 91 us,
-// 3.7 TB/s), from thread `first` of `all`; columns d .. pad - 1 become zeros.
-template <int DT, int Block>
-__device__ __forceinline__ void dequantize_range(const Int8Rows& R, int64_t first, int64_t all) {
-  typedef typename Elem<DT>::type E;
-  constexpr int N = 16 / sizeof(E);
-  typedef E EN __attribute__((ext_vector_type(N)));
-  typedef EN ENu __attribute__((aligned(sizeof(E))));
-  typedef uint32_t Words __attribute__((ext_vector_type(N / 4), aligned(1)));
-  const int64_t groups = (R.d + 31) / 32, per = (R.pad + N - 1) / N, total = R.n * per;
-  for (int64_t i = first; i < total; i += all) {
-    const int64_t row = row_of(i, per), at = (i - row * per) * N;
-    float step = 0.0f;
-    if constexpr (Block == 0) step = static_cast<const float*>(R.scale)[row];
-    else if (at < R.d) step = block_step(static_cast<const uint8_t*>(R.scale)[row * groups + at / 32]);
-    const int8_t* c = R.codes + row * R.ldc + at;
-    E* o = static_cast<E*>(const_cast<void*>(R.x)) + row * R.ldx + at;
-    EN v;
-    if (at + N <= R.d) {
-      const Words w = *reinterpret_cast<const Words*>(c);
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = from_f32<E>(unpack(w[j / 4], j & 3) * step);
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = from_f32<E>(at + j < R.d ? (float)c[j] * step : 0.0f);
-    }
-    if (at + N <= R.pad) {
-      *reinterpret_cast<ENu*>(o) = v;
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (at + j < R.pad) o[j] = v[j];
-    }
-  }
-}
 template <int DT, int Block> __global__ void __launch_bounds__(256) dequantize(Int8Rows R) {
   dequantize_range<DT, Block>(R, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }

@@ -27,20 +27,21 @@ bool packed(int64_t d, int dtype) { return d % piece(dtype) != 0; }
 int64_t pack_bytes(int64_t rows, int64_t d, int dtype) { return up(rows * up(d, piece(dtype)) * elem_bytes(dtype), 256); }
 
 // Workspace: forward: packed x, gate, up | partial tiles; backward: the
-// gradient pair | packed x, gate, up | partial tiles.
+// gradient pair | packed x, gate, up | x restored from 8 bits | partial tiles.
 struct FfnWork {
-  int64_t pack, slots, total;
+  int64_t pack, x8, slots, total;
 };
 FfnGemm two_segments(FfnGemm g) {
   g.segs = 2;
   return g;
 }
-FfnWork ffn_work(int64_t n, int64_t d, int64_t f, int dtype, bool backward, bool pre8 = false) {
+FfnWork ffn_work(int64_t n, int64_t d, int64_t f, int dtype, bool backward, bool pre8 = false, bool x8 = false) {
   FfnWork w{};
   // (a pair in 8 bits comes from tiles, whose workgroups hold whole blocks of it)
   if (!backward && !pre8 && n <= kFfnFew && (packed(d, dtype) || ffn_prefers_few(n, d, f, elem_bytes(dtype)))) return w;
   w.pack = backward ? up(n * 2 * up(f, 8) * elem_bytes(dtype), 256) : 0;
-  w.slots = w.pack + (packed(d, dtype) ? pack_bytes(n, d, dtype) + 2 * pack_bytes(f, d, dtype) : 0);
+  w.x8 = w.pack + (packed(d, dtype) ? pack_bytes(n, d, dtype) + 2 * pack_bytes(f, d, dtype) : 0);
+  w.slots = w.x8 + (x8 ? pack_bytes(n, d, dtype) : 0);
   w.total = w.slots + (backward ? std::max(slot_bytes(two_segments(shape(n, d, f)), kFfnDx, dtype),
                                            slot_bytes(shape(2 * up(f, 8), d, n), kFfnDw, dtype))
                                 : slot_bytes(shape(n, f, d), kFfnFwd, dtype));
@@ -102,6 +103,96 @@ int place_operands(FfnOperands& o, char* pack, int64_t n, int64_t f, int dtype, 
   return HESS_OK;
 }
 
+// The backward pass; x8: x is its codes (with row stride ldx) in blocks of 32.
+int ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t ldx, const Int8Rows* x8, const void* w_gate,
+                 int64_t ldg, const void* w_up, int64_t ldu, const void* preact, int dtype, int act, int64_t n,
+                            int64_t d, int64_t f, void* dx, int64_t lddx, void* dw_gate, int64_t lddg, void* dw_up,
+                            int64_t lddu, void* work, int64_t work_bytes, hess_stream_t stream) {
+  if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
+  const PairType pair = pair_type(act);
+  if (act < HESS_SILU || act > HESS_GELU_TANH) return fail(HESS_EINVAL, "unknown activation %d", act);
+  if (!dw_gate != !dw_up) return fail(HESS_EINVAL, "dw_gate and dw_up: both or neither");
+  const int64_t es = elem_bytes(dtype), fp = up(f, 8);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t exps = x8 ? n * ((d + 31) / 32) : 0;
+  const Mat ins[6] = {{"dh", dh, lddh, n, f},
+                      {"x", x, ldx, n, d, x8 ? 1 : 0},
+                      {"w_gate", w_gate, ldg, f, d},
+                      {"w_up", w_up, ldu, f, d},
+                      pair_mat(preact, pair, n, f),
+                      {"x_exponents", x8 ? x8->scale : nullptr, exps, 1, exps, 1}};
+  const Mat outs[3] = {{"dx", dx, lddx, n, d}, {"dw_gate", dw_gate, lddg, f, d}, {"dw_up", dw_up, lddu, f, d}};
+  for (const Mat& m : ins) {
+    if (n == 0 && m.rows == 0) continue;
+    if (&m == &ins[1] && !x && !dw_gate) continue;  // dx alone does not read it
+    if (&m == &ins[5]) {
+      if (x8 && dw_gate && !m.p) return fail(HESS_EINVAL, "null x_exponents");
+      continue;
+    }
+    if (int rc = check_mat(m, m.own ? 1 : es)) return rc;
+  }
+  for (const Mat& m : outs)
+    if (m.p && m.rows > 0)
+      if (int rc = check_mat(m, es)) return rc;
+  if (!aligned(preact, 16)) return fail(HESS_EALIGN, "preact not 16-byte aligned");
+  const FfnWork room = n > 0 ? ffn_work(n, d, f, dtype, true, false, x8 != nullptr) : FfnWork{};
+  if (int rc = check_work(work, work_bytes, room.total)) return rc;
+  if (int rc = check_outputs(outs, 3, ins, 6, es, work, room.total)) return rc;
+  hipError_t e = hipSuccess;
+  if (n == 0) {
+    if (dw_gate) {
+      e = launch_zero_rows(dw_gate, lddg, f, d, (int)es, s);
+      if (e == hipSuccess) e = launch_zero_rows(dw_up, lddu, f, d, (int)es, s);
+    }
+    return e == hipSuccess ? HESS_OK : hip_fail(e, "gradient clear launch");
+  }
+  if (!dx && !dw_gate) return HESS_OK;
+
+  char* dgu = static_cast<char*>(work);
+  float* slots = reinterpret_cast<float*>(dgu + room.slots);
+  // x in 8 bits is restored to rows that the tiles read where they are
+  const int64_t dp = up(d, piece(dtype));
+  Int8Rows restored{};
+  if (x8 && dw_gate) restored = {dgu + room.x8, dp, x8->codes, ldx, x8->scale, n, d, dp};
+  FfnOperands o{x8 ? dgu + room.x8 : x, w_gate, w_up, x8 ? dp : ldx, ldg, ldu, d};
+  if (int rc = place_operands(o, dgu + room.pack, n, f, dtype, dw_gate && !x8, dx != nullptr, s)) return rc;
+  if (x8) o.x = dgu + room.x8, o.ldx = dp;
+  e = launch_ffn_dgu(dh, lddh, preact, pair, dgu, n, f, fp, act, dtype, restored, s);
+  if (e != hipSuccess) return hip_fail(e, "gate gradient launch");
+  if (dx) {
+    FfnGemm g = shape(n, d, f);
+    g.segs = 2;
+    g.a = dgu;
+    g.lda = 2 * fp;
+    g.b0 = o.wg;
+    g.ldb0 = o.ldg;
+    g.b1 = o.wu;
+    g.ldb1 = o.ldu;
+    g.o0 = dx;
+    g.ldo0 = lddx;
+    g.ws = slots;
+    g.f = f;
+    g.fp = fp;
+    if (int rc = run_product(g, kFfnDx, dtype, room.total - room.slots, s, "input gradient launch")) return rc;
+  }
+  if (dw_gate) {
+    FfnGemm g = shape(2 * fp, d, n);
+    g.a = dgu;
+    g.lda = 2 * fp;
+    g.b0 = o.x;
+    g.ldb0 = o.ldx;
+    g.o0 = dw_gate;
+    g.ldo0 = lddg;
+    g.o1 = dw_up;
+    g.ldo1 = lddu;
+    g.ws = slots;
+    g.f = f;
+    g.fp = fp;
+    if (int rc = run_product(g, kFfnDw, dtype, room.total - room.slots, s, "weight gradient launch")) return rc;
+  }
+  return HESS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -125,7 +216,7 @@ int64_t hess_gated_ffn_preact_cols(int64_t f) {
 int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int backward) {
   if (check_ffn_sizes(n, d, f, dtype) != HESS_OK) return -1;
   if (n == 0) return 0;
-  return ffn_work(n, d, f, dtype, backward != 0 && backward != 2, backward == 2).total;
+  return ffn_work(n, d, f, dtype, backward != 0 && backward != 2, backward == 2, backward == 3).total;
 }
 
 int64_t hess_gated_ffn_preact_i8_cols(int64_t f) {
@@ -188,78 +279,20 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
                             const void* w_up, int64_t ldu, const void* preact, int dtype, int act, int64_t n,
                             int64_t d, int64_t f, void* dx, int64_t lddx, void* dw_gate, int64_t lddg, void* dw_up,
                             int64_t lddu, void* work, int64_t work_bytes, hess_stream_t stream) {
-  if (int rc = check_ffn_sizes(n, d, f, dtype)) return rc;
-  const PairType pair = pair_type(act);
-  if (act < HESS_SILU || act > HESS_GELU_TANH) return fail(HESS_EINVAL, "unknown activation %d", act);
-  if (!dw_gate != !dw_up) return fail(HESS_EINVAL, "dw_gate and dw_up: both or neither");
-  const int64_t es = elem_bytes(dtype), fp = up(f, 8);
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const Mat ins[5] = {{"dh", dh, lddh, n, f},
-                      {"x", x, ldx, n, d},
-                      {"w_gate", w_gate, ldg, f, d},
-                      {"w_up", w_up, ldu, f, d},
-                      pair_mat(preact, pair, n, f)};
-  const Mat outs[3] = {{"dx", dx, lddx, n, d}, {"dw_gate", dw_gate, lddg, f, d}, {"dw_up", dw_up, lddu, f, d}};
-  for (const Mat& m : ins) {
-    if (n == 0 && m.rows == 0) continue;
-    if (&m == &ins[1] && !x && !dw_gate) continue;  // dx alone does not read it
-    if (int rc = check_mat(m, es)) return rc;
-  }
-  for (const Mat& m : outs)
-    if (m.p && m.rows > 0)
-      if (int rc = check_mat(m, es)) return rc;
-  if (!aligned(preact, 16)) return fail(HESS_EALIGN, "preact not 16-byte aligned");
-  const FfnWork room = n > 0 ? ffn_work(n, d, f, dtype, true) : FfnWork{};
-  if (int rc = check_work(work, work_bytes, room.total)) return rc;
-  if (int rc = check_outputs(outs, 3, ins, 5, es, work, room.total)) return rc;
-  hipError_t e = hipSuccess;
-  if (n == 0) {
-    if (dw_gate) {
-      e = launch_zero_rows(dw_gate, lddg, f, d, (int)es, s);
-      if (e == hipSuccess) e = launch_zero_rows(dw_up, lddu, f, d, (int)es, s);
-    }
-    return e == hipSuccess ? HESS_OK : hip_fail(e, "gradient clear launch");
-  }
-  if (!dx && !dw_gate) return HESS_OK;
+  return ffn_backward(dh, lddh, x, ldx, nullptr, w_gate, ldg, w_up, ldu, preact, dtype, act, n, d, f, dx, lddx, dw_gate,
+                      lddg, dw_up, lddu, work, work_bytes, stream);
+}
 
-  char* dgu = static_cast<char*>(work);
-  float* slots = reinterpret_cast<float*>(dgu + room.slots);
-  FfnOperands o{x, w_gate, w_up, ldx, ldg, ldu, d};
-  if (int rc = place_operands(o, dgu + room.pack, n, f, dtype, dw_gate != nullptr, dx != nullptr, s)) return rc;
-  e = launch_ffn_dgu(dh, lddh, preact, pair, dgu, n, f, fp, act, dtype, s);
-  if (e != hipSuccess) return hip_fail(e, "gate gradient launch");
-  if (dx) {
-    FfnGemm g = shape(n, d, f);
-    g.segs = 2;
-    g.a = dgu;
-    g.lda = 2 * fp;
-    g.b0 = o.wg;
-    g.ldb0 = o.ldg;
-    g.b1 = o.wu;
-    g.ldb1 = o.ldu;
-    g.o0 = dx;
-    g.ldo0 = lddx;
-    g.ws = slots;
-    g.f = f;
-    g.fp = fp;
-    if (int rc = run_product(g, kFfnDx, dtype, room.total - room.slots, s, "input gradient launch")) return rc;
-  }
-  if (dw_gate) {
-    FfnGemm g = shape(2 * fp, d, n);
-    g.a = dgu;
-    g.lda = 2 * fp;
-    g.b0 = o.x;
-    g.ldb0 = o.ldx;
-    g.o0 = dw_gate;
-    g.ldo0 = lddg;
-    g.o1 = dw_up;
-    g.ldo1 = lddu;
-    g.ws = slots;
-    g.f = f;
-    g.fp = fp;
-    if (int rc = run_product(g, kFfnDw, dtype, room.total - room.slots, s, "weight gradient launch")) return rc;
-  }
-  return HESS_OK;
+int hess_gated_ffn_backward_x8(const void* dh, int64_t lddh, const int8_t* x_codes, int64_t ldc,
+                               const uint8_t* x_exponents, const void* w_gate, int64_t ldg, const void* w_up,
+                               int64_t ldu, const void* preact, int dtype, int act, int64_t n, int64_t d, int64_t f,
+                               void* dx, int64_t lddx, void* dw_gate, int64_t lddg, void* dw_up, int64_t lddu,
+                               void* work, int64_t work_bytes, hess_stream_t stream) {
+  Int8Rows x8{};
+  x8.codes = const_cast<int8_t*>(x_codes);
+  x8.scale = const_cast<uint8_t*>(x_exponents);
+  return ffn_backward(dh, lddh, x_codes, ldc, &x8, w_gate, ldg, w_up, ldu, preact, dtype, act, n, d, f, dx, lddx, dw_gate,
+                      lddg, dw_up, lddu, work, work_bytes, stream);
 }
 
 int64_t hess_distill_topk_workspace(int64_t n, int64_t vocab, int dtype) {

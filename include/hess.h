@@ -642,6 +642,19 @@ int hess_gated_ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t
                             int64_t lddu, void* work, int64_t work_bytes, hess_stream_t stream);
 
 /*
+ * hess_gated_ffn_backward_x8 -- the same with x held in 8 bits, as
+ * hess_int8_quantize with block 32 leaves it: x_codes n x d with row stride ldc,
+ * any alignment, x_exponents n x ceil(d / 32) bytes, contiguous.  dw_gate and dw_up
+ * are those at what the codes stand for; both may be NULL where these are not
+ * wanted.  Needs hess_gated_ffn_workspace with backward = 3.
+ */
+int hess_gated_ffn_backward_x8(const void* dh, int64_t lddh, const int8_t* x_codes, int64_t ldc,
+                               const uint8_t* x_exponents, const void* w_gate, int64_t ldg, const void* w_up,
+                               int64_t ldu, const void* preact, int dtype, int act, int64_t n, int64_t d, int64_t f,
+                               void* dx, int64_t lddx, void* dw_gate, int64_t lddg, void* dw_up, int64_t lddu,
+                               void* work, int64_t work_bytes, hess_stream_t stream);
+
+/*
  * Distillation from a teacher's top logits -- for each row (token) the
  * divergence of the student from the teacher's k highest logits, the usual
  * measure of what quantization cost a model and the loss to mend it with:
@@ -760,8 +773,8 @@ int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const i
  * take such operands), sums are float32.  Where a row of dy is a multiple of 16
  * bytes, every row must start at 16 (EALIGN); other rows are copied first.
  * Workspace: hess_int8_linear_workspace(n, d, f, dtype, pass), 16-byte aligned,
- * not shared by calls that may overlap; pass 0: forward, 1: backward for dx, 2: for
- * dw, 3: for both; -1 for bad arguments.
+ * not shared by calls that may overlap; pass 0: forward, 4: forward with x_codes, 1:
+ * backward for dx, 2: for dw, 3: for both; -1 for bad arguments.
  * Outputs must not overlap the inputs, one another or the workspace.  n = 0 is a
  * no-op, but dw becomes zero.
  */

@@ -158,7 +158,7 @@ def test_linear_refusals():
             (dict(dw=_ptr(5, 64)), EINVAL, b"dx overlaps dw"), (dict(dw=_ptr(1)), EINVAL, b"dw overlaps x_codes"),
             (dict(bytes_=16), EINVAL, b"workspace"), (dict(work=_ptr(3)), EINVAL, b"overlaps the workspace")]:
         assert _backward(**kw) == code and word in _message(), (kw, _message())
-    for bad in (-1, 4):
+    for bad in (-1, 5):
         assert hs._load().hess_int8_linear_workspace(5, 8, 8, 0, bad) == -1
     assert hs._load().hess_int8_linear_workspace(0, 8, 8, 0, 3) == 0
 
@@ -176,6 +176,25 @@ def test_ffn_pair_in_8_bits_refusals():
                            (dict(pre=_ptr(4, 8)), EALIGN, b"preact"), (dict(pre=_ptr(3, 16)), EINVAL, b"h overlaps preact"),
                            (dict(xoff=2), EALIGN, b"16-byte")]:
         assert forward(**kw) == code and word in _message(), (kw, _message())
+
+
+@built
+def test_ffn_backward_x8_refusals():
+    lib = hs._load()
+
+    def backward(xc=_ptr(1), ldc=24, xe=_ptr(9), pre=_ptr(4), act=64, dx=_ptr(5), dwg=_ptr(6), dwu=_ptr(7), bytes_=GB):
+        return lib.hess_gated_ffn_backward_x8(_ptr(0), 40, xc, ldc, xe, _ptr(2), 24, _ptr(3), 24, pre, 0, act, 5, 24, 40,
+                                              dx, 24, dwg, 24, dwu, 24, _ptr(8), bytes_, None)
+
+    assert backward(dx=None, dwg=None, dwu=None) == 0
+    for kw, code, word in [(dict(xc=None), EINVAL, b"null x"), (dict(xe=None), EINVAL, b"x_exponents"),
+                           (dict(ldc=23), EINVAL, b"of x"), (dict(dx=_ptr(1, 8)), EINVAL, b"dx overlaps x"),
+                           (dict(dwg=_ptr(9, 2)), EINVAL, b"dw_gate overlaps x_exponents"),
+                           (dict(pre=_ptr(4, 4)), EALIGN, b"preact"), (dict(act=80), EINVAL, b"activation"),
+                           (dict(bytes_=16), EINVAL, b"workspace")]:
+        assert backward(**kw) == code and word in _message(), (kw, _message())
+    room = lib.hess_gated_ffn_workspace(5, 24, 40, 0, 3) - lib.hess_gated_ffn_workspace(5, 24, 40, 0, 1)
+    assert room >= 5 * 24 * 2
 
 
 @built

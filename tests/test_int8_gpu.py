@@ -310,6 +310,11 @@ def test_ffn_checkpoint(n, d, f, dt):
     assert only[1] is None and torch.equal(only[0], dx)
     only = hs.gated_ffn_backward(dh, x8, wg, wu, pre, act=act, need_x=False)
     assert only[0] is None and torch.equal(only[1], dwg) and torch.equal(only[2], dwu)
+    if dt != "f32":  # a pair in another type beside x in 8 bits
+        mixed = hs.gated_ffn_forward(x, wg, wu, act=act, save=x.dtype)[1]
+        one = hs.gated_ffn_backward(dh, x8, wg, wu, mixed, act=act)
+        two = hs.gated_ffn_backward(dh, hs.dequantize_int8(x8, dtype=x.dtype), wg, wu, mixed, act=act)
+        assert all(torch.equal(p, q) for p, q in zip(one, two))
     same = hs.gated_ffn_backward(dh, hs.dequantize_int8(x8, dtype=x.dtype), wg, wu, pre, act=act)
     assert all(torch.equal(p, q) for p, q in zip(same, (dx, dwg, dwu)))
 
