@@ -126,7 +126,7 @@ int ffn_backward(const void* dh, int64_t lddh, const void* x, int64_t ldx, const
     if (n == 0 && m.rows == 0) continue;
     if (&m == &ins[1] && !x && !dw_gate) continue;  // dx alone does not read it
     if (&m == &ins[5]) {
-      if (x8 && dw_gate && !m.p) return fail(HESS_EINVAL, "null x_exponents");
+      if (n > 0 && x8 && dw_gate && !m.p) return fail(HESS_EINVAL, "null x_exponents");
       continue;
     }
     if (int rc = check_mat(m, m.own ? 1 : es)) return rc;
