@@ -178,13 +178,17 @@ template <bool In, int N> __device__ __forceinline__ uint32_t top_inside(const F
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if constexpr (!In) v[j] = c + j < P.f ? v[j] : 0.0f;
-    m = max(m, abs_bits(v[j]));
+    // (a copy of its own: the compiler otherwise takes |v| from the activation's
+    // branches, one of which does not form it, and the largest value was missed)
+    float w = v[j];
+    asm("" : "+v"(w));
+    m = max(m, abs_bits(w));
   }
   return m;
 }
 
 // Outputs of row r, features c .. c + N - 1 of the forward pass.
-template <int DT, int N>
+template <int DT, bool Pre8 = false, int N>
 __device__ __forceinline__ void put_fwd(const FfnGemm& P, int64_t r, int64_t c, const float (&g)[N],
                                         const float (&u)[N]) {
   typedef typename Elem<DT>::type T;
@@ -193,7 +197,7 @@ __device__ __forceinline__ void put_fwd(const FfnGemm& P, int64_t r, int64_t c, 
 #pragma unroll
   for (int j = 0; j < N; ++j) h[j] = act_value<DT == kInF32>(g[j], P.act) * u[j];
   if (c < P.N) store_n(static_cast<T*>(P.o0) + r * P.ldo0 + c, h, (int)min((int64_t)N, P.N - c));
-  if (!P.o1 || P.pre8) return;
+  if (Pre8 || !P.o1) return;
   // columns f .. fp - 1 are zeros: absent weight rows read as zeros, but times
   // an infinite x they are none
   float gz[N], uz[N];

@@ -54,7 +54,8 @@ constexpr uint32_t kOOB = 0x80000000u;  // an offset past any descriptor's range
 constexpr int64_t kAll = 0x7fffffff;
 constexpr int kStages = 5, kAhead = 4;
 
-template <int DT, int Mode, int Edge>
+// Pre8: forward, the pair is kept in 8 bits.
+template <int DT, int Mode, int Edge, bool Pre8 = false>
 __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) ffn_tile(FfnGemm P) {
   constexpr bool kRowsA = Mode != kFfnDw;  // A's rows run along K
   constexpr bool kRowsB = Mode == kFfnFwd;
@@ -312,11 +313,11 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) f
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = act_value<DT == kInF32>(g[e], P.act) * u[e];
         store_n(static_cast<T*>(P.o0) + r * P.ldo0 + col, h, 8);
-        if (P.o1 && !P.pre8) put_preact<T>(P, r, col, g, u);
+        if (!Pre8 && P.o1) put_preact<T>(P, r, col, g, u);
       } else {
-        put_fwd<DT>(P, r, col, g, u);
+        put_fwd<DT, Pre8>(P, r, col, g, u);
       }
-      if (P.pre8) {
+      if constexpr (Pre8) {
         // a block's 32 features are in the four lanes of one row (edge 64: in
         // two of this wave and two of the next, which meet in LDS)
         uint32_t tg = max_over_32(top_inside<In>(P, col, g)), tu = max_over_32(top_inside<In>(P, col, u));
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(Edge == 256 ? 512 : 256, Edge == 64 ? 4 : 2) f
 // Split tiles: the parts' sums added in part order, then the epilogue.  Block
 // (t, s) handles rows s * (1024 / Edge) .. of tile full + t; a thread takes
 // four columns (forward: of both projections).
-template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn_join(FfnGemm P) {
+template <int DT, int Mode, int Edge, bool Pre8 = false> __global__ void __launch_bounds__(256) ffn_join(FfnGemm P) {
   const int tail = P.ntiles - P.full, t = blockIdx.x;
   int I, J;
   tile_coords<Mode>(P, P.full + t, I, J);
@@ -403,8 +404,8 @@ template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn
       u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
     }
     const int64_t r = (int64_t)I * Edge + row, c = (int64_t)J * (Edge / 2) + w * (cols / 2) + 4 * q;
-    put_fwd<DT>(P, r, c, g, u);
-    if (P.pre8) {
+    put_fwd<DT, Pre8>(P, r, c, g, u);
+    if constexpr (Pre8) {
       // eight neighbouring lanes hold a block's 32 features
       uint32_t tg = top_inside<false>(P, c, g), tu = top_inside<false>(P, c, u);
 #pragma unroll
@@ -424,22 +425,23 @@ template <int DT, int Mode, int Edge> __global__ void __launch_bounds__(256) ffn
   }
 }
 
-template <int DT, int Mode, int Edge> void launch_edge(const FfnGemm& g, hipStream_t stream) {
+template <int DT, int Mode, int Edge, bool Pre8 = false> void launch_edge(const FfnGemm& g, hipStream_t stream) {
   const int tail = g.ntiles - g.full;
-  ffn_tile<DT, Mode, Edge><<<g.full + tail * g.parts, Edge == 256 ? 512 : 256, 0, stream>>>(g);
+  ffn_tile<DT, Mode, Edge, Pre8><<<g.full + tail * g.parts, Edge == 256 ? 512 : 256, 0, stream>>>(g);
   if (tail == 0) return;
   constexpr int quads = Mode == kFfnFwd ? Edge / 8 : Edge / 4;
-  ffn_join<DT, Mode, Edge><<<dim3(tail, Edge * quads / 256), 256, 0, stream>>>(g);
+  ffn_join<DT, Mode, Edge, Pre8><<<dim3(tail, Edge * quads / 256), 256, 0, stream>>>(g);
 }
 
-template <int DT, int Mode> hipError_t launch_mode(const FfnGemm& g, int edge, hipStream_t stream) {
-  if (edge == 256) launch_edge<DT, Mode, 256>(g, stream);
-  else if (edge == 128) launch_edge<DT, Mode, 128>(g, stream);
-  else launch_edge<DT, Mode, 64>(g, stream);
+template <int DT, int Mode, bool Pre8 = false> hipError_t launch_mode(const FfnGemm& g, int edge, hipStream_t stream) {
+  if (edge == 256) launch_edge<DT, Mode, 256, Pre8>(g, stream);
+  else if (edge == 128) launch_edge<DT, Mode, 128, Pre8>(g, stream);
+  else launch_edge<DT, Mode, 64, Pre8>(g, stream);
   return hipGetLastError();
 }
 
 template <int DT> hipError_t launch_type(const FfnGemm& g, int mode, int edge, hipStream_t stream) {
+  if (mode == kFfnFwd && g.pre8) return launch_mode<DT, kFfnFwd, true>(g, edge, stream);
   if (mode == kFfnFwd) return launch_mode<DT, kFfnFwd>(g, edge, stream);
   if (mode == kFfnDx) return launch_mode<DT, kFfnDx>(g, edge, stream);
   return launch_mode<DT, kFfnDw>(g, edge, stream);

@@ -169,7 +169,7 @@ template <int DT, int T, int P> void launch_rows(const Int8Rows& r, const PackCo
     p.x = static_cast<const char*>(r.x) + r0 * r.ldx * Elem<DT>::size;
     p.codes = r.codes + r0 * r.ldc;
     p.scale = static_cast<float*>(r.scale) + r0;
-    const int extra = c.count > 0 && r0 == 0 ? (int)std::min<int64_t>((c.rows[0] * (c.pad / 16) + T - 1) / T, 1024) : 0;
+    const int extra = c.count > 0 && r0 == 0 ? (int)std::min<int64_t>((c.rows[0] * (c.pad / 16) + T - 1) / T, (1 << 18) / T) : 0;
     quantize_rows<DT, T, P><<<(unsigned)(p.n + extra), T, 0, stream>>>(p, c);
   }
 }

@@ -401,3 +401,24 @@ def test_one_row_not_finite():
     for bad in (float("inf"), float("nan")):
         x[0, 299] = bad
         assert torch.isnan(hs.int8_linear_forward(x, w8)).all()
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("edge", [64, 128, 256])
+@pytest.mark.parametrize("act", R.ACTS)
+def test_ffn_checkpoint_activations(act, edge, dt):
+    """Every activation in every tile, inside the matrix and at its end: the pair does not depend on either."""
+    n, d, f = 300, 72, 300
+    say(f"ffn in 8 bits {dt} {act} edge {edge}")
+    x, xn = draw(1, dt, n, d)
+    wg, gn = draw(2, dt, f, d, scale=1.5 / d ** 0.5)
+    wu, un = draw(3, dt, f, d, scale=1.5 / d ** 0.5)
+    want, g, u = R.gated_ffn(xn, gn, un, act)
+    try:
+        hs.set_ffn_schedule(edge, 1 << 30, 1)
+        h, pre = hs.gated_ffn_forward(x, wg, wu, act=act, save=torch.int8)
+    finally:
+        hs.set_ffn_schedule()
+    check("h", h, want, G.forward_tolerance(xn, gn, un, g, u, act, dt)[0])
+    k = (d + 8) * U
+    check_pair(pre, f, g, u, k * (np.abs(xn) @ np.abs(gn).T), k * (np.abs(xn) @ np.abs(un).T))
