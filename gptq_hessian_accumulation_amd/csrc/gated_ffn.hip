@@ -66,7 +66,9 @@ __global__ void __launch_bounds__(256) ffn_dgu(const typename Elem<DT>::type* dh
   *reinterpret_cast<T8*>(o + fp) = du;
 }
 
-// The same from the pair in 8 bits (rows of pair8_cols(f) bytes).
+// The same from the pair in 8 bits (rows of pair8_cols(f) bytes); workgroups behind
+// its rows restore x.  Bound by its bytes (bf16, 8192 x 11264: 130 us, 5.7 TB/s; with
+// x of 4096 columns 153 us, 5.5 TB/s, where a launch of its own for x took 24).
 template <int DT>
 __global__ void __launch_bounds__(256) ffn_dgu8(const typename Elem<DT>::type* dh, int64_t lddh, const char* pre,
                                                 int64_t ldp, typename Elem<DT>::type* out, int64_t n, int64_t f,
