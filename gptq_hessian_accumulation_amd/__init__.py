@@ -1020,7 +1020,7 @@ def _int8_args(name: str, rows: Int8Rows, block=None, product=False):
     if b != 0 and b != 32:
         raise ValueError(f"block of {name} must be 0 or 32, not {b}")
     if block is not None and b != block:
-        raise ValueError(f"{name} must have a scale a row (block 0)")
+        raise ValueError(f"{name} must have " + ("a scale a row (block 0)" if block == 0 else "blocks of 32 columns"))
     shape = codes.shape
     if len(shape) < 1:
         raise ValueError(f"codes of {name} must be (..., d)")

@@ -108,6 +108,13 @@ template <int DT, int MB, int FB, int W, int U> __global__ void __launch_bounds_
   }
 }
 
+// The workgroup's waves meet with their LDS writes done; loads from memory stay in
+// flight (__syncthreads would wait for them).
+__device__ __forceinline__ void meet_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // One row of values: every workgroup quantizes it for itself into LDS (one
 // launch, and no codes in memory).  The row's loads go first and the first
 // weights' right behind them, so that these arrive while the largest magnitude
@@ -150,9 +157,7 @@ template <int DT, int W, int U, int X> __global__ void __launch_bounds__(64 * W)
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
   if (lane == 0) tops[wave] = top;
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // the LDS writes alone: the weights stay in flight
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
+  meet_lds();
 #pragma unroll
   for (int w = 0; w < W; ++w) top = max(top, tops[w]);
   const RowCode<T> code(top);
@@ -164,9 +169,7 @@ template <int DT, int W, int U, int X> __global__ void __launch_bounds__(64 * W)
     *reinterpret_cast<uint2*>(codes + (i * 64 * W + tid) * 8) =
         uint2{pack4(k[0], k[1], k[2], k[3]), pack4(k[4], k[5], k[6], k[7])};
   }
-  __builtin_amdgcn_s_waitcnt(0xc07f);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
+  meet_lds();
   const char* a = codes + at;
   auto code16 = [&](int unit) { return *reinterpret_cast<const u32x4*>(a + unit * 64); };
   i32x4 acc{};

@@ -566,7 +566,8 @@ int hess_imatrix_destroy(hess_imx_t m);
  *
  * Workspace: hess_gated_ffn_workspace(n, d, f, dtype, backward) bytes of
  * device memory, 16-byte aligned, for the forward (backward = 0) or the
- * backward call; -1 for bad arguments.  No call allocates or synchronizes:
+ * backward call (1; 2 and 3: see HESS_PREACT_I8 and hess_gated_ffn_backward_x8);
+ * -1 for bad arguments.  No call allocates or synchronizes:
  * they may be captured into a HIP graph.  The workspace must not be shared by
  * calls that may overlap (two streams).
  */
@@ -720,8 +721,7 @@ int hess_distill_topk_backward(const float* dloss, const void* logits, int64_t l
  *             be shorter): the step 2^(e - 127) is the power of two with
  *             64 <= a / step < 128, and at least 2^-126; code = rint(x / step), ties
  *             to even, and 127 or -127 past those.
- *             What the codes stand for is exact in bf16 and, from 2^-24 to 65504,
- *             in fp16.
+ *             What the codes stand for is exact in bf16, and in fp16 where x is.
  * A row (block) that holds an infinity or NaN has scale NaN (e = 255) and codes
  * 0: it stands for NaN.
  *   x         n x d of dtype, row stride ldx, any element alignment.

@@ -218,6 +218,8 @@ def test_refusals_on_the_gpu():
     both = torch.randn(80, 40, device="cuda").bfloat16()
     with pytest.raises(hs.HessError, match="overlaps"):
         hs.int8_linear_forward(both, hs.quantize_int8(both[:40]), out=both)
+    with pytest.raises(ValueError, match="blocks of 32"):
+        hs.gated_ffn_backward(x[:, :24], x8, both[:24], both[:24], torch.empty(3, 80, dtype=torch.int8, device="cuda"))
     with pytest.raises(ValueError, match="need x"):
         hs.gated_ffn_backward(x[:, :24], None, both[:24], both[:24], torch.empty(3, 80, dtype=torch.int8, device="cuda"))
     with pytest.raises(ValueError, match="save"):
