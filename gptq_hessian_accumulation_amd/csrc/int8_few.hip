@@ -3,7 +3,7 @@
 // step, bound by the weights' bytes.  A workgroup takes all of K, its waves a share
 // each, and their sums meet in LDS.  One row: 4096 x 11264 11.0 us with its
 // quantization (46 MB of weights: 4.2 TB/s), 10.9 without, where a launch that
-// quantizes the row first adds 3.2.  24 rows at 2560 x 9728: 10.5 us.
+// quantizes the row first adds 3.2.  24 rows at 2560 x 9728: 9.6 us.
 //
 // Sums are int32 and exact: |a b| <= 2^14 and K < 2^17.  The output takes the
 // sum as a float32 (2^-24), times the two scales, rounded once to its type.
@@ -217,22 +217,35 @@ template <int DT, int MB, int FB, int W, int U> void launch_few(const Int8Gemm& 
   int8_few<DT, MB, FB, W, U><<<dim3(gx, gy), 64 * W, 0, stream>>>(g);
 }
 
-// 16 features a workgroup as long as that leaves at most one for each of the 256
-// CUs; past that more of them, which read the codes of a less often.  us, weights
-// in the last-level cache, for blocks of (16 tokens, 16 features):
-//   24 tokens  4096 x 4096    (2, 1)  8.5  (2, 2) 10.5  (2, 4) 13.9
-//              2560 x 9728    (2, 1) 12.5  (2, 2) 12.0  (2, 4) 10.5
-//   32 tokens  4096 x 11264   (2, 1) 19.8  (2, 2) 18.1  (2, 4) 15.0
-//   64 tokens  2560 x 2560    (4, 1)  9.0  (2, 2)  7.9  (4, 4) 13.2
-//              4096 x 11264   (4, 1) 30.4  (2, 2) 24.9  (4, 4) 19.5
+// As few features a workgroup as leave at most one workgroup for each of the 256
+// CUs: more read the codes of a less often, fewer fill the card.  Up to 32 tokens
+// two blocks of them, up to 64 four, or twice two where that still leaves one
+// workgroup a CU.  us, weights in the last-level cache, for blocks of (16 tokens,
+// 16 features):
+//   24 tokens  4096 x 4096    (2, 1)  8.5  (2, 2) 11.1  (2, 3) 12.1
+//              4096 x 6144    (2, 1) 12.3  (2, 2) 11.0  (2, 3) 11.8  (2, 4) 13.6  (20 tokens)
+//              2560 x 9728    (2, 1) 12.9  (2, 2) 12.4  (2, 3)  9.6  (2, 4) 10.6
+//   32 tokens  4096 x 11264   (2, 1) 20.2  (2, 2) 18.5  (2, 3) 13.5  (2, 4) 15.2
+//   64 tokens  2560 x 2560    (2, 1) 10.0  (2, 2)  7.9  (2, 3)  9.7  (4, 3) 11.9
+//              4096 x 6144    (2, 2) 18.3  (2, 3) 13.3  (4, 3) 17.3  (4, 4) 18.9
+//              4096 x 11264   (2, 3) 22.6  (2, 4) 25.3  (4, 3) 18.0  (4, 4) 19.6
 // Up to 16 tokens one block of 16 features is best or within 7% (4096 x 11264:
 // 14.4 against 13.4 for (2, 4)).
 template <int DT> void launch_type(const Int8Gemm& g, hipStream_t stream) {
-  if (g.M <= 16) launch_few<DT, 1, 1, 4, 4>(g, stream);
-  else if (g.M <= 32 && g.N <= 4096) launch_few<DT, 2, 1, 4, 4>(g, stream);
-  else if (g.N <= 8192) launch_few<DT, 2, 2, 4, 4>(g, stream);
-  else if (g.M <= 32) launch_few<DT, 2, 4, 8, 2>(g, stream);
-  else launch_few<DT, 4, 4, 8, 2>(g, stream);
+  const int64_t wide = 256 * 16;  // features of one block a CU
+  if (g.M <= 16) {
+    launch_few<DT, 1, 1, 4, 4>(g, stream);
+  } else if (g.M <= 32 || 2 * g.N <= 3 * wide) {
+    const int64_t blocks = g.M <= 32 ? g.N : 2 * g.N;
+    if (blocks <= wide) launch_few<DT, 2, 1, 4, 4>(g, stream);
+    else if (blocks <= 2 * wide) launch_few<DT, 2, 2, 4, 4>(g, stream);
+    else if (blocks <= 3 * wide) launch_few<DT, 2, 3, 8, 2>(g, stream);
+    else launch_few<DT, 2, 4, 8, 2>(g, stream);
+  } else if (g.N <= 3 * wide) {
+    launch_few<DT, 4, 3, 8, 2>(g, stream);
+  } else {
+    launch_few<DT, 4, 4, 8, 2>(g, stream);
+  }
 }
 
 template <int DT, int W, int U, int X> void launch_one(const Int8Gemm& g, hipStream_t stream) {

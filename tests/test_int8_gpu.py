@@ -379,7 +379,9 @@ def test_matmul_schedules(n, d, f, edge, whole, parts, dt):
 @pytest.mark.parametrize("n,d,f", [(1, 40, 70), (1, 1001, 2731), (1, 2048, 100), (1, 2049, 4096), (1, 2500, 4113),
                                    (1, 4096, 4113), (1, 5000, 4200), (1, 8192, 48), (1, 8192, 4100), (1, 8193, 33),
                                    (16, 260, 4100), (17, 260, 4096), (32, 333, 4097), (33, 64, 100), (20, 200, 8193),
-                                   (64, 200, 8200), (33, 1030, 8210), (64, 130, 8192)])
+                                   (64, 200, 8200), (33, 1030, 8210), (64, 130, 8192),
+                                   (17, 70, 12288), (20, 64, 12300), (40, 72, 12289), (40, 130, 6144), (50, 130, 6145),
+                                   (64, 130, 2048), (64, 65, 2049), (33, 70, 4097)])
 def test_few_rows(n, d, f, dt):
     say(f"few rows {dt} {n}x{d}x{f}")
     x, w, qx, sx, qw, sw = layer_case(13, n, d, f, dt)
