@@ -63,7 +63,7 @@ int64_t int8_slots(Int8Gemm g) {
 }
 ProductWork product_work(int64_t n, int64_t d, int64_t f) {
   ProductWork w{};
-  if (n <= kInt8Few) return w;
+  if (int8_few(n, d)) return w;
   const bool copy = d % 16 != 0;
   w.b = copy ? up(n * code_stride(d), 256) : 0;
   w.slots = w.b + (copy ? up(f * code_stride(d), 256) : 0);
@@ -96,12 +96,12 @@ void copied(PackCodes& p, const int8_t*& m, int64_t& ld, int64_t rows, int64_t d
 }
 // Whether the tiles cannot take b's rows where they are (d no multiple of 16).
 bool untidy(const Int8Gemm& g) {
-  return g.M > kInt8Few && g.K % 16 != 0 && !(rows_of_16(g.b, g.ldb, g.N) && g.ldb >= code_stride(g.K));
+  return !int8_few(g.M, g.K) && g.K % 16 != 0 && !(rows_of_16(g.b, g.ldb, g.N) && g.ldb >= code_stride(g.K));
 }
 
 // One product; its operands are as the kernel for its size takes them.
 int run_int8(Int8Gemm g, char* work, const ProductWork& room, int dtype, hipStream_t s) {
-  if (g.M <= kInt8Few) {
+  if (int8_few(g.M, g.K)) {
     const hipError_t e = launch_int8_few(g, dtype, s);
     return e == hipSuccess ? HESS_OK : hip_fail(e, "8-bit product launch");
   }
@@ -187,9 +187,9 @@ int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const i
   g.y = y, g.ldy = ldy;
   char* base = static_cast<char*>(work);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (n > kInt8Few && d % 16 == 0 && (!rows_of_16(a, lda, n) || !rows_of_16(b, ldb, f)))
+  if (!int8_few(n, d) && d % 16 == 0 && (!rows_of_16(a, lda, n) || !rows_of_16(b, ldb, f)))
     return fail(HESS_EALIGN, "rows of codes must be 16-byte aligned where d is a multiple of 16");
-  if (n > kInt8Few && d % 16 != 0) {
+  if (!int8_few(n, d) && d % 16 != 0) {
     PackCodes p{};
     const bool copy_b = untidy(g);
     copied(p, g.a, g.lda, n, d, base + room.a);
@@ -231,7 +231,7 @@ int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t
   const LinearWork room = linear_work(n, d, f, x_codes != nullptr);
   if (int rc = check_work(work, work_bytes, room.total)) return rc;
   if (int rc = check_outputs(outs, 3, ins, 3, es, work, room.total)) return rc;
-  if (n > kInt8Few && d % 16 == 0 && !rows_of_16(w, ldw, f))
+  if (!int8_few(n, d) && d % 16 == 0 && !rows_of_16(w, ldw, f))
     return fail(HESS_EALIGN, "rows of w must be 16-byte aligned where d is a multiple of 16");
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* base = static_cast<char*>(work);

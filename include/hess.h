@@ -744,9 +744,9 @@ int hess_int8_dequantize(const int8_t* codes, int64_t ldc, const void* scale, in
  *   y[t][o] = (sum_k a[t][k] b[o][k]) a_scale[t] b_scale[o]
  * a n x d, b f x d (int8, any alignment), y n x f of dtype.  Sums are int32 and
  * exact; a sum is rounded to float32, times b_scale, times a_scale, rounded
- * to dtype.  1 <= d < 2^17.  With more than 64 rows of a, and d a multiple of 16,
- * every row of a and b must start at 16 bytes (EALIGN); where d is no such
- * multiple, rows of a are copied to padded ones, and those of b too unless they
+ * to dtype.  1 <= d < 2^17.  With more than 64 rows of a (32 from d = 8192 on),
+ * and d a multiple of 16, every row of a and b must start at 16 bytes (EALIGN);
+ * where d is no such multiple, rows of a are copied to padded ones, and those of b too unless they
  * start at 16 bytes and are at least round16(d) bytes apart (codes of b between d
  * and there may be any).  The linear layer below has the same rule for w.
  */

@@ -381,7 +381,8 @@ def test_matmul_schedules(n, d, f, edge, whole, parts, dt):
                                    (16, 260, 4100), (17, 260, 4096), (32, 333, 4097), (33, 64, 100), (20, 200, 8193),
                                    (64, 200, 8200), (33, 1030, 8210), (64, 130, 8192),
                                    (17, 70, 12288), (20, 64, 12300), (40, 72, 12289), (40, 130, 6144), (50, 130, 6145),
-                                   (64, 130, 2048), (64, 65, 2049), (33, 70, 4097)])
+                                   (64, 130, 2048), (64, 65, 2049), (33, 70, 4097), (33, 8191, 50), (33, 8192, 50),
+                                   (40, 8200, 70), (64, 8205, 33), (32, 8205, 33)])
 def test_few_rows(n, d, f, dt):
     say(f"few rows {dt} {n}x{d}x{f}")
     x, w, qx, sx, qw, sw = layer_case(13, n, d, f, dt)
