@@ -341,3 +341,28 @@ def test_quantization_pass_to_8_bit_product():
     # are, with errors of random sign, within a few percent as vectors
     for a, b in zip(grads8, grads16):
         assert torch.isfinite(a).all() and float((a - b).norm() / b.norm()) <= 0.05
+
+
+@pytest.mark.parametrize("n", [5, 70])
+def test_checkpoint_of_odd_places(n):
+    """Inputs of the block that start off 16 bytes, strided checkpoints and gradients: the same bits."""
+    say(f"checkpoint, odd places {n}")
+    for d, f in ((64, 48), (77, 43)):
+        xf, wf = torch.randn(n * d + 1, device="cuda").bfloat16(), (torch.randn(2 * f * d + 1, device="cuda") / 8).bfloat16()
+        x, w = xf[1:].view(n, d), wf[1:].view(2 * f, d)
+        h, pre = hs.gated_ffn_forward(x, w[:f], w[f:], save=torch.int8)
+        h2, pre2 = hs.gated_ffn_forward(x.clone(), w[:f].clone(), w[f:].clone(), save=torch.int8)
+        used = 2 * (-(-f // 32) * 33)
+        assert torch.equal(h, h2) and torch.equal(pre[:, :used], pre2[:, :used])
+        x8 = hs.quantize_int8(x, block=32)
+        want = hs.gated_ffn_backward(h, x8, w[:f], w[f:], pre)
+        codes = torch.zeros(n, d + 5, dtype=torch.int8, device="cuda")[:, 3:d + 3]
+        codes.copy_(x8.codes)
+        scale = torch.empty(n, 2 * x8.scale.shape[1], dtype=torch.uint8, device="cuda")[:, ::2]
+        scale.copy_(x8.scale.view(torch.uint8))
+        odd = hs.Int8Rows(codes, scale.view(torch.float8_e8m0fnu), 32)
+        dh = torch.zeros(n, f + 3, dtype=torch.bfloat16, device="cuda")[:, 1:f + 1]
+        dh.copy_(h)
+        got = hs.gated_ffn_backward(dh, odd, w[:f].clone(), w[f:].clone(), pre2)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        assert torch.equal(hs.dequantize_int8(odd), hs.dequantize_int8(x8))
