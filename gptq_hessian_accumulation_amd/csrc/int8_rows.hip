@@ -116,13 +116,15 @@ template <int DT, int T, int P> __global__ void __launch_bounds__(T) quantize_ro
   }
 }
 
-// Blocks of 32 columns: 8 values a thread, four neighbouring lanes a block.
-template <int DT> __global__ void __launch_bounds__(256) quantize_blocks(Int8Rows R, int64_t groups, int64_t total) {
+// Blocks of 32 columns: 8 values a thread, four neighbouring lanes a block, `wide`
+// blocks a row: its `groups` of values, and those of zeros up to column pad.
+template <int DT>
+__global__ void __launch_bounds__(256) quantize_blocks(Int8Rows R, int64_t groups, int64_t wide, int64_t total) {
   typedef typename Elem<DT>::type E;
   // (whole waves run: total is a whole number of groups of four lanes)
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = row_of(i, groups * 4);
-    const int64_t at = (i - row * groups * 4) * 8;
+    const int64_t row = row_of(i, wide * 4);
+    const int64_t at = (i - row * wide * 4) * 8;
     float v[8] = {};
     if (at < R.d) load8(static_cast<const E*>(R.x) + row * R.ldx + at, R.d - at, v);
     uint32_t top = top_of(v);
@@ -132,7 +134,7 @@ template <int DT> __global__ void __launch_bounds__(256) quantize_blocks(Int8Row
     const BlockCode code(b);
     const uint2 q{code(v[0], v[1], v[2], v[3]), code(v[4], v[5], v[6], v[7])};
     if (at < R.pad) store8(R.codes + row * R.ldc + at, R.pad - at, q);
-    if ((i & 3) == 0) static_cast<uint8_t*>(R.scale)[row * groups + at / 32] = (uint8_t)b;
+    if ((i & 3) == 0 && at < R.d) static_cast<uint8_t*>(R.scale)[row * groups + at / 32] = (uint8_t)b;
   }
 }
 
@@ -190,8 +192,8 @@ template <int DT> hipError_t quantize_type(const Int8Rows& r, int block, const P
     else if (r.d <= 8192) launch_rows<DT, 256, 4>(r, c, stream);
     else launch_rows<DT, 1024, 2>(r, c, stream);
   } else {
-    const int64_t groups = (r.d + 31) / 32, total = r.n * groups * 4;
-    quantize_blocks<DT><<<grid_of(total), 256, 0, stream>>>(r, groups, total);
+    const int64_t groups = (r.d + 31) / 32, wide = std::max(groups, (r.pad + 31) / 32), total = r.n * wide * 4;
+    quantize_blocks<DT><<<grid_of(total), 256, 0, stream>>>(r, groups, wide, total);
   }
   return hipGetLastError();
 }
