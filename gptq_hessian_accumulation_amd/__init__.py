@@ -1032,7 +1032,13 @@ def _int8_args(name: str, rows: Int8Rows, block=None, product=False):
     if not scale.is_contiguous():
         scale = scale.contiguous()
     c2, cp, ldc = _rows(codes if len(shape) == 2 else codes.reshape(-1, d), 16 if product and d % 16 == 0 else 1)
-    return (c2, scale), lead, c2.shape[0], d, cp, ldc, scale.data_ptr()
+    n = c2.shape[0]
+    if product and d % 16 != 0 and cp % 16 == 0 and ldc % 16 == 0 and n > 0 \
+            and c2.storage_offset() + (n - 1) * ldc + (d + 15) // 16 * 16 > c2.untyped_storage().nbytes():
+        # the tiles read such rows where they are, in whole pieces of 16 bytes: the last one's must be there
+        c2 = c2.clone(memory_format=torch.contiguous_format)
+        cp, ldc = c2.data_ptr(), d
+    return (c2, scale), lead, n, d, cp, ldc, scale.data_ptr()
 
 
 def _new_codes(shape, n: int, d: int, like: torch.Tensor):

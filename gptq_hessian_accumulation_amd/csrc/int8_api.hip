@@ -98,6 +98,11 @@ void copied(PackCodes& p, const int8_t*& m, int64_t& ld, int64_t rows, int64_t d
 bool untidy(const Int8Gemm& g) {
   return !int8_few(g.M, g.K) && g.K % 16 != 0 && !(rows_of_16(g.b, g.ldb, g.N) && g.ldb >= code_stride(g.K));
 }
+// The codes of b that a product reads: tiles that take its rows where they are
+// read whole 16-byte pieces, those behind the last row's codes among them.
+Mat codes_read(const char* name, const Int8Gemm& g) {
+  return {name, g.b, g.ldb, g.N, int8_few(g.M, g.K) || untidy(g) ? g.K : code_stride(g.K), 1};
+}
 
 // One product; its operands are as the kernel for its size takes them.
 int run_int8(Int8Gemm g, char* work, const ProductWork& room, int dtype, hipStream_t s) {
@@ -177,14 +182,14 @@ int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const i
   const int64_t es = elem_bytes(dtype);
   const Mat out{"y", y, ldy, n, f};
   if (int rc = check_mat(out, es)) return rc;
-  const Mat ins[4] = {{"a", a, lda, n, d, 1}, {"b", b, ldb, f, d, 1}, {"a_scale", a_scale, n, 1, n, 4}, {"b_scale", b_scale, f, 1, f, 4}};
-  const ProductWork room = product_work(n, d, f);
-  if (int rc = check_work(work, work_bytes, room.total)) return rc;
-  if (int rc = check_outputs(&out, 1, ins, 4, es, work, room.total)) return rc;
   Int8Gemm g = product(n, d, f);
   g.a = a, g.lda = lda, g.sa = a_scale;
   g.b = b, g.ldb = ldb, g.sb = b_scale;
   g.y = y, g.ldy = ldy;
+  const Mat ins[4] = {{"a", a, lda, n, d, 1}, codes_read("b", g), {"a_scale", a_scale, n, 1, n, 4}, {"b_scale", b_scale, f, 1, f, 4}};
+  const ProductWork room = product_work(n, d, f);
+  if (int rc = check_work(work, work_bytes, room.total)) return rc;
+  if (int rc = check_outputs(&out, 1, ins, 4, es, work, room.total)) return rc;
   char* base = static_cast<char*>(work);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!int8_few(n, d) && d % 16 == 0 && (!rows_of_16(a, lda, n) || !rows_of_16(b, ldb, f)))
@@ -217,7 +222,10 @@ int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t
   if (!x_codes != !x_scale) return fail(HESS_EINVAL, "x_codes and x_scale: both or neither");
   if (n == 0) return HESS_OK;
   const int64_t es = elem_bytes(dtype);
-  const Mat ins[3] = {{"x", x, ldx, n, d}, {"w", w, ldw, f, d, 1}, {"w_scale", w_scale, f, 1, f, 4}};
+  Int8Gemm g = product(n, d, f);
+  g.b = w, g.ldb = ldw, g.sb = w_scale;
+  g.y = y, g.ldy = ldy;
+  const Mat ins[3] = {{"x", x, ldx, n, d}, codes_read("w", g), {"w_scale", w_scale, f, 1, f, 4}};
   if (int rc = check_mat(ins[0], es)) return rc;
   if (int rc = check_codes("w", w, ldw, d)) return rc;
   if (int rc = check_scale("w_scale", w_scale)) return rc;
@@ -235,9 +243,6 @@ int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t
     return fail(HESS_EALIGN, "rows of w must be 16-byte aligned where d is a multiple of 16");
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* base = static_cast<char*>(work);
-  Int8Gemm g = product(n, d, f);
-  g.b = w, g.ldb = ldw, g.sb = w_scale;
-  g.y = y, g.ldy = ldy;
   if (n == 1 && d <= kInt8One && !x_codes) {
     g.x = x, g.ldx = ldx;
     const hipError_t e = launch_int8_one(g, dtype, s);

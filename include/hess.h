@@ -747,8 +747,10 @@ int hess_int8_dequantize(const int8_t* codes, int64_t ldc, const void* scale, in
  * to dtype.  1 <= d < 2^17.  With more than 64 rows of a (32 from d = 8192 on),
  * and d a multiple of 16, every row of a and b must start at 16 bytes (EALIGN);
  * where d is no such multiple, rows of a are copied to padded ones, and those of b too unless they
- * start at 16 bytes and are at least round16(d) bytes apart (codes of b between d
- * and there may be any).  The linear layer below has the same rule for w.
+ * start at 16 bytes and are at least round16(d) bytes apart: then every row of b, the last one
+ * among them, is read up to round16(d) bytes (what these hold past d does not matter, but they
+ * must be memory of the caller's that no output of the call lies in).  The linear layer below has
+ * the same rules for w.
  */
 int64_t hess_int8_matmul_workspace(int64_t n, int64_t d, int64_t f);
 int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,

@@ -1,0 +1,38 @@
+"""Limits of the 8-bit calls without a GPU: what is refused before anything runs, workspaces, the import."""
+
+import ctypes
+import os
+
+import pytest
+
+import gptq_hessian_accumulation_amd as hs
+
+pytestmark = pytest.mark.skipif(not os.path.exists(hs.library_path()), reason="libhess.so not built")
+EINVAL = -1
+GB = 1 << 30
+
+
+def _ptr(i, off=0):
+    return ctypes.c_void_p((1 << 40) + i * 64 * GB + off)
+
+
+def _message():
+    return hs._load().hess_last_error()
+
+
+# (weights of 24 rows of d codes, ld bytes apart, whose pieces of 16 bytes the tiles read whole)
+@pytest.mark.parametrize("d,ld", [(40, 48), (33, 64)])
+@pytest.mark.parametrize("where", ["first", "last"])
+def test_outputs_behind_the_last_row_of_weights(d, ld, where):
+    """The bytes between the last row's codes and the end of their 16-byte piece are read: no output may lie there."""
+    lib, n, f = hs._load(), 100, 24
+    end = (f - 1) * ld
+    y = _ptr(2, end + (-(-d // 4) * 4 if where == "first" else -(-d // 16) * 16 - 4))
+    assert lib.hess_int8_matmul(_ptr(0), 64, _ptr(1), _ptr(2), ld, _ptr(3), n, d, f, y, f, 0, _ptr(5), GB, None) == EINVAL
+    assert b"y overlaps b" in _message()
+    assert lib.hess_int8_linear_forward(_ptr(0), d, 0, _ptr(2), ld, _ptr(3), n, d, f, y, f, None, 0, None, _ptr(5), GB,
+                                        None) == EINVAL
+    assert b"y overlaps w" in _message()
+    assert lib.hess_int8_linear_forward(_ptr(0), d, 0, _ptr(2), ld, _ptr(3), n, d, f, _ptr(4), f, _ptr(6), 64, y, _ptr(5),
+                                        GB, None) == EINVAL
+    assert b"x_scale overlaps w" in _message()

@@ -38,3 +38,27 @@ def test_padding_columns(n, d, pad, ldc, block, dt):
     assert not codes[:n, d:pad].any(), "columns d to pad are not zeros"
     assert (codes[:n, pad:] == FILL).all() and (codes[n] == FILL).all() and (scale[used:] == FILL).all()
     assert torch.equal(scale[:used].view(want.scale.dtype).flatten().view(torch.uint8), want.scale.contiguous().flatten().view(torch.uint8))
+
+
+@pytest.mark.parametrize("n,d,f", [(70, 40, 24), (300, 333, 130), (70, 8201, 5)])
+def test_weights_that_end_with_their_last_code(n, d, f, monkeypatch):
+    """Rows that tiles could read in place, but for the end of the last one's storage: copied, the outputs the same."""
+    say(f"weights that end with their last code {n}x{d}x{f}")
+    lib = hs._load()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(n, d, generator=gen, device="cuda").bfloat16()
+    w = hs.quantize_int8(torch.randn(f, d, generator=gen, device="cuda").bfloat16())
+    x8, want, ld = hs.quantize_int8(x), hs.int8_linear_forward(x, w), -(-d // 16) * 16
+    seen = []
+    for name, at in (("hess_int8_linear_forward", 3), ("hess_int8_matmul", 3)):
+        call = getattr(lib, name)
+        monkeypatch.setattr(lib, name, lambda *a, call=call, at=at: seen.append(a[at:at + 2]) or call(*a))
+    whole = torch.empty((f, ld), dtype=torch.int8, device="cuda")[:, :d]
+    short = torch.empty((f - 1) * ld + d, dtype=torch.int8, device="cuda").as_strided((f, d), (ld, 1))
+    for codes, copied in ((whole, False), (short, True)):
+        codes.copy_(w.codes)
+        rows = hs.Int8Rows(codes, w.scale)
+        for y in (hs.int8_linear_forward(x, rows), hs.int8_matmul(x8, rows)):
+            pointer, stride = seen.pop()
+            assert (pointer != codes.data_ptr() and stride < ld) if copied else (pointer, stride) == (codes.data_ptr(), ld)
+            assert torch.equal(y, want)
