@@ -1005,10 +1005,11 @@ class Int8Rows(NamedTuple):
     block: int = 0
 
 
-def _int8_args(name: str, rows: Int8Rows, block=None, product=False):
+def _int8_args(name: str, rows: Int8Rows, block=None, tokens=0):
     """(tensors to keep, leading shape, n, d, code pointer, row stride, scale pointer) of checked rows.
 
-    product: rows of a multiple of 16 codes that do not start at 16 bytes are copied, as its tiles need it."""
+    tokens: rows of the left operand of the product that takes these (0: none does).  Past the few whose
+    kernels take codes of any alignment, rows that do not start where its tiles need it are copied."""
     codes, scale, b = rows
     index = codes.get_device()
     if index < 0:
@@ -1031,9 +1032,10 @@ def _int8_args(name: str, rows: Int8Rows, block=None, product=False):
                          f"{tuple(lead) if b == 0 else (*lead, -(-d // 32))} tensor on {codes.device}")
     if not scale.is_contiguous():
         scale = scale.contiguous()
-    c2, cp, ldc = _rows(codes if len(shape) == 2 else codes.reshape(-1, d), 16 if product and d % 16 == 0 else 1)
+    tiles = tokens > 32 and (tokens > 64 or d >= 8192)  # as the library chooses
+    c2, cp, ldc = _rows(codes if len(shape) == 2 else codes.reshape(-1, d), 16 if tiles and d % 16 == 0 else 1)
     n = c2.shape[0]
-    if product and d % 16 != 0 and cp % 16 == 0 and ldc % 16 == 0 and n > 0 \
+    if tiles and d % 16 != 0 and cp % 16 == 0 and ldc % 16 == 0 and n > 0 \
             and c2.storage_offset() + (n - 1) * ldc + (d + 15) // 16 * 16 > c2.untyped_storage().nbytes():
         # the tiles read such rows where they are, in whole pieces of 16 bytes: the last one's must be there
         c2 = c2.clone(memory_format=torch.contiguous_format)
@@ -1120,8 +1122,8 @@ def int8_matmul(a: Int8Rows, b: Int8Rows, dtype: torch.dtype = torch.bfloat16, o
         with torch.cuda.stream(stream):
             return int8_matmul(a, b, dtype, out, workspace)
     lib = _load()
-    keep, lead, n, d, ap, lda, asp = _int8_args("a", a, 0, True)
-    keep_b, lead_b, f, db, bp, ldb, bsp = _int8_args("b", b, 0, True)
+    keep, lead, n, d, ap, lda, asp = _int8_args("a", a, 0, a.codes.shape[:-1].numel())
+    keep_b, lead_b, f, db, bp, ldb, bsp = _int8_args("b", b, 0, n)
     if len(lead_b) != 1 or db != d:
         raise ValueError(f"b must hold (f, {d}) codes, not {tuple(b.codes.shape)}")
     code = _CODES.get(dtype)
@@ -1152,10 +1154,10 @@ def int8_linear_forward(x: torch.Tensor, w: Int8Rows, save: bool = False, out: t
             return int8_linear_forward(x, w, save, out, workspace)
     lib = _load()
     code = _float_code("x", x)
-    keep, lead_w, f, d, wp8, ldw, wsp = _int8_args("w", w, 0, True)
+    lead = x.shape[:-1]
+    keep, lead_w, f, d, wp8, ldw, wsp = _int8_args("w", w, 0, lead.numel())
     if len(lead_w) != 1 or x.dim() < 1 or x.shape[-1] != d:
         raise ValueError(f"w must hold (f, d) codes and x be (..., d), not {tuple(w.codes.shape)} and {tuple(x.shape)}")
-    lead = x.shape[:-1]
     x2, xp, ldx = _rows(x if len(lead) == 1 else x.reshape(-1, d))
     n = x2.shape[0]
     ldy = f

@@ -62,3 +62,46 @@ def test_weights_that_end_with_their_last_code(n, d, f, monkeypatch):
             pointer, stride = seen.pop()
             assert (pointer != codes.data_ptr() and stride < ld) if copied else (pointer, stride) == (codes.data_ptr(), ld)
             assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("n,d", [(1, 4096), (1, 8192), (24, 4096), (64, 4096), (64, 8176), (32, 8192), (32, 16384)])
+def test_few_rows_of_unaligned_weights_copy_nothing(n, d):
+    """Up to 64 rows the kernels read weights of any alignment: a call takes no memory of the weights' size."""
+    f = 1000
+    say(f"no copies {n}x{d}")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(n, d, generator=gen, device="cuda").bfloat16()
+    w = hs.quantize_int8(torch.randn(f, d, generator=gen, device="cuda").bfloat16())
+    odd = torch.empty(f * d + 1, dtype=torch.int8, device="cuda")[1:].view(f, d)
+    odd.copy_(w.codes)
+    wide = torch.empty(f, d + 5, dtype=torch.int8, device="cuda")[:, :d]
+    wide.copy_(w.codes)
+    want, x8 = hs.int8_linear_forward(x, w), hs.quantize_int8(x)
+    for codes in (odd, wide):
+        w_odd = hs.Int8Rows(codes, w.scale)
+        for call in (lambda: hs.int8_linear_forward(x, w_odd), lambda: hs.int8_linear_forward(x, w_odd, save=True)[0],
+                     lambda: hs.int8_matmul(x8, w_odd), lambda: hs.int8_linear(x, w_odd)):
+            torch.cuda.synchronize()
+            torch.cuda.reset_peak_memory_stats()
+            before = torch.cuda.memory_allocated()
+            got = call()
+            assert torch.cuda.max_memory_allocated() - before < f * d // 2, "the weights were copied"
+            assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n,d", [(33, 8192), (65, 4096), (65, 8192), (33, 16384), (64, 8192)])
+def test_tiles_of_unaligned_weights(n, d):
+    """One row past where the kernels read any alignment: the rows are copied first, the outputs the same."""
+    f = 300
+    say(f"unaligned tiles {n}x{d}")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(n, d, generator=gen, device="cuda").bfloat16()
+    w = hs.quantize_int8(torch.randn(f, d, generator=gen, device="cuda").bfloat16())
+    odd = torch.empty(f * d + 1, dtype=torch.int8, device="cuda")[1:].view(f, d)
+    odd.copy_(w.codes)
+    x8 = hs.quantize_int8(x)
+    ax = torch.empty(n, d + 3, dtype=torch.int8, device="cuda")[:, :d]
+    ax.copy_(x8.codes)
+    want = hs.int8_linear_forward(x, w)
+    assert torch.equal(hs.int8_linear_forward(x, hs.Int8Rows(odd, w.scale)), want)
+    assert torch.equal(hs.int8_matmul(hs.Int8Rows(ax, x8.scale), hs.Int8Rows(odd, w.scale)), want)
