@@ -169,6 +169,9 @@ __device__ __forceinline__ void put_pair8(const FfnGemm& P, int64_t r, int64_t c
   if (first) {
     row[2 * fq + c / 32] = (char)bg;
     row[2 * fq + fq / 32 + c / 32] = (char)bu;
+    // the last block's lane ends the row with zeros
+    if (c + 32 == fq)
+      for (int64_t at = 2 * fq + fq / 16; at < P.ldo1; at += 2) *reinterpret_cast<uint16_t*>(row + at) = 0;
   }
 }
 // Columns past f are zeros (absent weight rows read as zeros, but times an

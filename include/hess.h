@@ -586,7 +586,7 @@ enum { HESS_PREACT_F32 = 16 };
  * 32); h does not change, and the backward pass takes its derivatives at what the
  * codes stand for.  preact is then n rows of hess_gated_ffn_preact_i8_cols(f)
  * bytes: with fq = f rounded up to a multiple of 32, fq codes of g, fq of u (zeros
- * from f on), fq / 32 exponent bytes of g, fq / 32 of u.  Such a forward call
+ * from f on), fq / 32 exponent bytes of g, fq / 32 of u, zeros to the row's end.  Such a forward call
  * needs hess_gated_ffn_workspace with backward = 2, takes tiles whatever n is
  * (so that h of few tokens may differ from another call's in its last bit), and
  * has the tiles' rule on alignment. */

@@ -105,3 +105,34 @@ def test_tiles_of_unaligned_weights(n, d):
     want = hs.int8_linear_forward(x, w)
     assert torch.equal(hs.int8_linear_forward(x, hs.Int8Rows(odd, w.scale)), want)
     assert torch.equal(hs.int8_matmul(hs.Int8Rows(ax, x8.scale), hs.Int8Rows(odd, w.scale)), want)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("n,f,edge,whole,parts", [(5, 1, 0, 0, 1), (70, 32, 0, 0, 1), (70, 33, 0, 0, 1), (300, 200, 0, 0, 1),
+                                                  (300, 256, 256, 1 << 30, 1), (300, 330, 64, 0, 2), (300, 330, 128, 2, 2),
+                                                  (300, 96, 128, 1 << 30, 1), (300, 330, 256, 0, 2)])
+def test_saved_pair_is_written_whole(n, f, edge, whole, parts, dt):
+    """Every byte of the pair in 8 bits is the call's: those behind the exponents are zeros, and equal calls leave
+    equal tensors whatever the memory held."""
+    d = 520
+    say(f"pair written whole {dt} {n}x{d}x{f} edge {edge} whole {whole} parts {parts}")
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(n, d, generator=gen, device="cuda").to(TYPES[dt])
+    wg, wu = ((torch.randn(f, d, generator=gen, device="cuda") / 20).to(TYPES[dt]) for _ in range(2))
+    lib, code = hs._load(), hs._CODES[x.dtype]
+    cols, fq = lib.hess_gated_ffn_preact_i8_cols(f), -(-f // 32) * 32
+    made = []
+    try:
+        hs.set_ffn_schedule(edge, whole, parts)
+        for fill in (FILL, 0x25):
+            pre = torch.full((n + 1, cols), fill, dtype=torch.int8, device="cuda")
+            h = torch.empty(n, f, dtype=x.dtype, device="cuda")
+            work = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+            hs._check(lib.hess_gated_ffn_forward(x.data_ptr(), d, wg.data_ptr(), d, wu.data_ptr(), d, code, hs._PREACT_I8, n, d,
+                                                 f, h.data_ptr(), f, pre.data_ptr(), work.data_ptr(), work.numel(), stream()))
+            assert (pre[n] == fill).all(), "written behind the last row"
+            made.append(pre[:n])
+    finally:
+        hs.set_ffn_schedule()
+    assert not made[0][:, 2 * fq + fq // 16:].any(), "bytes behind the exponents are not zeros"
+    assert torch.equal(made[0], made[1])
