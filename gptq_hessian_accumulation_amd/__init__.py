@@ -144,6 +144,7 @@ def _load():
         "hess_distill_topk_backward": (c_int, [vp, vp, i64, c_int, i64, i64, vp, c_int, i64, vp, c_int, i64, c_int,
                                                vp, ctypes.c_float, vp, vp, i64, vp]),
         "hess_gated_ffn_preact_i8_cols": (i64, [i64]),
+        "hess_gated_ffn_i8_workspace": (i64, [i64, i64, i64, c_int]),
         "hess_gated_ffn_backward_x8": (c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, c_int, c_int, i64, i64, i64,
                                                vp, i64, vp, i64, vp, i64, vp, i64, vp]),
         "hess_int8_quantize": (c_int, [vp, i64, c_int, i64, i64, c_int, vp, i64, i64, vp, vp]),
@@ -724,7 +725,7 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
             mode |= _PREACT_F32
     if n > 0:
         ldh = h.stride(0) if out is not None and h.dim() == 2 and n > 1 else f
-        need = lib.hess_gated_ffn_workspace(n, d, f, code, 2 if in8 else 0)
+        need = lib.hess_gated_ffn_i8_workspace(n, d, f, code) if in8 else lib.hess_gated_ffn_workspace(n, d, f, code, 0)
         wp, wb, work = _workspace(workspace, need, x) if need else (None, 0, None)
         rc = lib.hess_gated_ffn_forward(*ins, code, mode, n, d, f, h.data_ptr(), ldh,
                                         pre.data_ptr() if save else None, wp, wb, _stream(None, x.get_device()))

@@ -216,7 +216,13 @@ int64_t hess_gated_ffn_preact_cols(int64_t f) {
 int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int backward) {
   if (check_ffn_sizes(n, d, f, dtype) != HESS_OK) return -1;
   if (n == 0) return 0;
-  return ffn_work(n, d, f, dtype, backward != 0 && backward != 2, backward == 2, backward == 3).total;
+  const int64_t need = ffn_work(n, d, f, dtype, backward != 0, false, backward == 3).total;
+  return backward == 2 ? std::max(need, ffn_work(n, d, f, dtype, false, true).total) : need;
+}
+
+int64_t hess_gated_ffn_i8_workspace(int64_t n, int64_t d, int64_t f, int dtype) {
+  if (check_ffn_sizes(n, d, f, dtype) != HESS_OK) return -1;
+  return n == 0 ? 0 : ffn_work(n, d, f, dtype, false, true).total;
 }
 
 int64_t hess_gated_ffn_preact_i8_cols(int64_t f) {

@@ -566,8 +566,9 @@ int hess_imatrix_destroy(hess_imx_t m);
  *
  * Workspace: hess_gated_ffn_workspace(n, d, f, dtype, backward) bytes of
  * device memory, 16-byte aligned, for the forward (backward = 0) or the
- * backward call (1; 2 and 3: see HESS_PREACT_I8 and hess_gated_ffn_backward_x8);
- * -1 for bad arguments.  No call allocates or synchronizes:
+ * backward call (any other value; 3: hess_gated_ffn_backward_x8 as well; 2: a
+ * forward call with HESS_PREACT_I8 as well, which alone needs no more than
+ * hess_gated_ffn_i8_workspace says); -1 for bad arguments.  No call allocates or synchronizes:
  * they may be captured into a HIP graph.  The workspace must not be shared by
  * calls that may overlap (two streams).
  */
@@ -587,11 +588,12 @@ enum { HESS_PREACT_F32 = 16 };
  * codes stand for.  preact is then n rows of hess_gated_ffn_preact_i8_cols(f)
  * bytes: with fq = f rounded up to a multiple of 32, fq codes of g, fq of u (zeros
  * from f on), fq / 32 exponent bytes of g, fq / 32 of u, zeros to the row's end.  Such a forward call
- * needs hess_gated_ffn_workspace with backward = 2, takes tiles whatever n is
+ * needs hess_gated_ffn_i8_workspace(n, d, f, dtype) bytes, takes tiles whatever n is
  * (so that h of few tokens may differ from another call's in its last bit), and
  * has the tiles' rule on alignment. */
 enum { HESS_PREACT_I8 = 64 };
 int64_t hess_gated_ffn_preact_i8_cols(int64_t f); /* -1 for bad f */
+int64_t hess_gated_ffn_i8_workspace(int64_t n, int64_t d, int64_t f, int dtype); /* -1 for bad arguments */
 
 int64_t hess_gated_ffn_workspace(int64_t n, int64_t d, int64_t f, int dtype, int backward);
 

@@ -36,3 +36,20 @@ def test_outputs_behind_the_last_row_of_weights(d, ld, where):
     assert lib.hess_int8_linear_forward(_ptr(0), d, 0, _ptr(2), ld, _ptr(3), n, d, f, _ptr(4), f, _ptr(6), 64, y, _ptr(5),
                                         GB, None) == EINVAL
     assert b"x_scale overlaps w" in _message()
+
+
+@pytest.mark.parametrize("n,d,f", [(1, 64, 64), (5, 25, 40), (70, 333, 1000), (300, 704, 1000), (8192, 4096, 11264)])
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_ffn_workspace_for_any_backward(n, d, f, dtype):
+    """Every value but 0 asks for the backward pass's room; what a forward call with the pair in 8 bits needs has a
+    function of its own, and 2 gives enough for either."""
+    lib = hs._load()
+    need = lib.hess_gated_ffn_workspace(n, d, f, dtype, 1)
+    assert need >= n * 2 * f * (4 if dtype == 1 else 2)
+    forward = lib.hess_gated_ffn_i8_workspace(n, d, f, dtype)
+    assert forward >= 0
+    for backward in (-1, 2, 3, 4, 64, 255):
+        assert lib.hess_gated_ffn_workspace(n, d, f, dtype, backward) >= need
+    assert lib.hess_gated_ffn_workspace(n, d, f, dtype, 2) >= forward
+    assert lib.hess_gated_ffn_i8_workspace(0, d, f, dtype) == 0
+    assert lib.hess_gated_ffn_i8_workspace(-1, d, f, dtype) == -1 and lib.hess_gated_ffn_i8_workspace(n, d, f, 7) == -1
