@@ -994,7 +994,16 @@ def distill_topk(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, 
 
 # -- 8-bit integers: rows as codes with scales, their product, a linear layer ---------------------
 
-_E8 = torch.float8_e8m0fnu  # powers of two by their exponent byte, as the library's block 32 has them
+# powers of two by their exponent byte, as the library's block 32 has them (None: a torch without the type, where
+# blocks of 32 are refused and all else runs)
+_E8 = getattr(torch, "float8_e8m0fnu", None)
+
+
+def _check_block(name: str, block: int) -> None:
+    if block != 0 and block != 32:
+        raise ValueError(f"{name} must be 0 or 32, not {block}")
+    if block != 0 and _E8 is None:
+        raise RuntimeError("blocks of 32 columns need a torch with float8_e8m0fnu")
 
 
 class Int8Rows(NamedTuple):
@@ -1019,8 +1028,8 @@ def _int8_args(name: str, rows: Int8Rows, block=None, tokens=0):
         raise ValueError(f"{name} is on {codes.device}, not on the current device")
     if codes.dtype != torch.int8:
         raise TypeError(f"codes of {name} must be int8, not {codes.dtype}")
-    if b != 0 and b != 32:
-        raise ValueError(f"block of {name} must be 0 or 32, not {b}")
+    if b != 0:
+        _check_block(f"block of {name}", b)
     if block is not None and b != block:
         raise ValueError(f"{name} must have " + ("a scale a row (block 0)" if block == 0 else "blocks of 32 columns"))
     shape = codes.shape
@@ -1068,9 +1077,9 @@ def quantize_int8(x: torch.Tensor, block: int = 0, stream=None) -> Int8Rows:
         with torch.cuda.stream(stream):
             return quantize_int8(x, block)
     lib = _load()
+    if block != 0:
+        _check_block("block", block)
     code = _float_code("x", x)
-    if block != 0 and block != 32:
-        raise ValueError(f"block must be 0 or 32, not {block}")
     shape = x.shape
     d = shape[-1] if len(shape) > 0 else 0
     if d < 1:

@@ -2,8 +2,11 @@
 
 import ctypes
 import os
+import subprocess
+import sys
 
 import pytest
+import torch
 
 import gptq_hessian_accumulation_amd as hs
 
@@ -53,3 +56,27 @@ def test_ffn_workspace_for_any_backward(n, d, f, dtype):
     assert lib.hess_gated_ffn_workspace(n, d, f, dtype, 2) >= forward
     assert lib.hess_gated_ffn_i8_workspace(0, d, f, dtype) == 0
     assert lib.hess_gated_ffn_i8_workspace(-1, d, f, dtype) == -1 and lib.hess_gated_ffn_i8_workspace(n, d, f, 7) == -1
+
+
+def test_import_without_the_type_of_exponents():
+    """A torch without float8_e8m0fnu: the package imports, and only blocks of 32 columns are refused."""
+    code = """
+import torch
+del torch.float8_e8m0fnu
+import gptq_hessian_accumulation_amd as hs
+x = torch.zeros(2, 32)
+for call, error, word in ((lambda: hs.quantize_int8(x, block=32), RuntimeError, "float8_e8m0fnu"),
+                          (lambda: hs.quantize_int8(x, block=16), ValueError, "0 or 32"),
+                          (lambda: hs.quantize_int8(x), ValueError, "on the GPU"),
+                          (lambda: hs.gated_ffn_forward(x, x, x), ValueError, "on the GPU")):
+    try:
+        call()
+    except error as e:
+        assert word in str(e), e
+    else:
+        raise AssertionError(word)
+print("imported")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(hs.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "imported" in r.stdout, r.stderr
