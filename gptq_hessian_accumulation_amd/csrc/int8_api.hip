@@ -53,7 +53,9 @@ Int8Gemm product(int64_t n, int64_t d, int64_t f) {
 
 // Workspace of a product: a, b with padded rows | partial tiles; before them for
 // a linear layer the codes and scales of x.  Room for copied rows is there
-// where d is no multiple of 16.
+// where d is no multiple of 16: of a only if it is copied (a linear layer's codes
+// of x have padded rows as they are), of b in any case, since sizes do not tell
+// whether its rows can be read where they are.
 struct ProductWork {
   int64_t a, b, slots, total;
 };
@@ -61,11 +63,11 @@ int64_t int8_slots(Int8Gemm g) {
   const int edge = int8_schedule(g);
   return (int64_t)(g.ntiles - g.full) * g.parts * edge * edge * 4;
 }
-ProductWork product_work(int64_t n, int64_t d, int64_t f) {
+ProductWork product_work(int64_t n, int64_t d, int64_t f, bool copy_a) {
   ProductWork w{};
   if (int8_few(n, d)) return w;
   const bool copy = d % 16 != 0;
-  w.b = copy ? up(n * code_stride(d), 256) : 0;
+  w.b = copy && copy_a ? up(n * code_stride(d), 256) : 0;
   w.slots = w.b + (copy ? up(f * code_stride(d), 256) : 0);
   w.total = w.slots + int8_slots(product(n, d, f));
   return w;
@@ -80,13 +82,12 @@ LinearWork linear_work(int64_t n, int64_t d, int64_t f, bool given) {
     w.scale = up(n * code_stride(d), 256);
     w.product = w.scale + up(4 * n, 256);
   }
-  w.total = w.product + product_work(n, d, f).total;
+  w.total = w.product + product_work(n, d, f, false).total;
   return w;
 }
 
 bool rows_of_16(const void* p, int64_t ld, int64_t rows) { return aligned(p, 16) && (rows <= 1 || ld % 16 == 0); }
 
-// One product; zeros: a's codes are zeros from d to the next multiple of 16.
 // Puts codes with padded rows in the workspace in place of m's.
 void copied(PackCodes& p, const int8_t*& m, int64_t& ld, int64_t rows, int64_t d, char* dst) {
   p.cols = d, p.pad = code_stride(d);
@@ -167,7 +168,7 @@ int hess_int8_dequantize(const int8_t* codes, int64_t ldc, const void* scale, in
 
 int64_t hess_int8_matmul_workspace(int64_t n, int64_t d, int64_t f) {
   if (check_product(n, d, f, HESS_BF16) != HESS_OK) return -1;
-  return n == 0 ? 0 : product_work(n, d, f).total;
+  return n == 0 ? 0 : product_work(n, d, f, true).total;
 }
 
 int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
@@ -187,7 +188,7 @@ int hess_int8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const i
   g.b = b, g.ldb = ldb, g.sb = b_scale;
   g.y = y, g.ldy = ldy;
   const Mat ins[4] = {{"a", a, lda, n, d, 1}, codes_read("b", g), {"a_scale", a_scale, n, 1, n, 4}, {"b_scale", b_scale, f, 1, f, 4}};
-  const ProductWork room = product_work(n, d, f);
+  const ProductWork room = product_work(n, d, f, true);
   if (int rc = check_work(work, work_bytes, room.total)) return rc;
   if (int rc = check_outputs(&out, 1, ins, 4, es, work, room.total)) return rc;
   char* base = static_cast<char*>(work);
@@ -253,7 +254,7 @@ int hess_int8_linear_forward(const void* x, int64_t ldx, int dtype, const int8_t
     ldc = code_stride(d);
     x_scale = reinterpret_cast<float*>(base + room.scale);
   }
-  const ProductWork rest = product_work(n, d, f);
+  const ProductWork rest = product_work(n, d, f, false);
   const Int8Rows r{x, ldx, x_codes, ldc, x_scale, n, d, code_stride(d)};
   PackCodes p{};
   if (untidy(g)) copied(p, g.b, g.ldb, f, d, base + room.product + rest.b);

@@ -80,3 +80,19 @@ print("imported")
     root = os.path.dirname(os.path.dirname(os.path.abspath(hs.__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "imported" in r.stdout, r.stderr
+
+
+@pytest.mark.parametrize("n,d,f", [(100, 33, 24), (777, 1001, 2731), (1999, 2561, 9728), (16384, 4097, 11264)])
+def test_linear_workspace_has_no_room_for_copies_never_made(n, d, f):
+    """Codes of x go to padded rows as they are: the layer's room is what the product of given codes needs less the
+    copy of its left operand, plus the codes and scales where the caller keeps none."""
+    lib = hs._load()
+    pad = -(-d // 16) * 16
+
+    def up(v):
+        return -(-v // 256) * 256
+
+    product = lib.hess_int8_matmul_workspace(n, d, f)
+    kept = lib.hess_int8_linear_workspace(n, d, f, 0, 4)
+    assert kept == product - up(n * pad) and kept >= f * pad
+    assert lib.hess_int8_linear_workspace(n, d, f, 0, 0) == kept + up(n * pad) + up(4 * n)
