@@ -52,7 +52,18 @@ __device__ __forceinline__ float normal_cdf(float g, float& e) {
   return g > 0.0f ? 1.0f - tail : tail;
 }
 
-template <bool Exact> __device__ __forceinline__ float act_value(float g, int act) {
+// v, but not as far as the compiler can tell: no expression of it is shared with one of v.
+__device__ __forceinline__ float apart(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
+// (The branches take a copy of g.  An expression that each of them forms and that a
+// caller forms of g again, |g| for one, is otherwise formed in the branches alone,
+// and on the way of gelu_tanh the compiler's code left its register unset: a largest
+// |g| after two calls is enough, and the optimized IR still has the value there.)
+template <bool Exact> __device__ __forceinline__ float act_value(float given, int act) {
+  const float g = apart(given);
   if (act == HESS_SILU) return g * sigmoidf<Exact>(g);
   if (act == HESS_GELU) {
     float e;
@@ -61,6 +72,7 @@ template <bool Exact> __device__ __forceinline__ float act_value(float g, int ac
   return g * sigmoidf<Exact>(1.5957691216057308f * (g + 0.044715f * g * g * g));
 }
 
+// (Its callers form nothing of g beside it, or they would need a copy as above.)
 template <bool Exact> __device__ __forceinline__ void act_both(float g, int act, float& a, float& da) {
   if (act == HESS_SILU) {
     const float s = sigmoidf<Exact>(g);
@@ -181,11 +193,7 @@ template <bool In, int N> __device__ __forceinline__ uint32_t top_inside(const F
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if constexpr (!In) v[j] = c + j < P.f ? v[j] : 0.0f;
-    // (a copy of its own: the compiler otherwise takes |v| from the activation's
-    // branches, one of which does not form it, and the largest value was missed)
-    float w = v[j];
-    asm("" : "+v"(w));
-    m = max(m, abs_bits(w));
+    m = max(m, abs_bits(v[j]));
   }
   return m;
 }
