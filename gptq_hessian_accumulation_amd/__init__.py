@@ -257,8 +257,8 @@ def set_tile_override(edge: int) -> None:
 
 
 def set_ffn_schedule(edge: int = 0, whole: int = 0, parts: int = 1) -> None:
-    """Force the feed-forward block's and the 8-bit product's tiles (edge 0 = automatic, 64, 128 or 256), the first ``whole`` done whole
-    and the others in ``parts`` ranges of the sum; process-wide."""
+    """Force the feed-forward block's and the 8-bit product's tiles (edge 0 = automatic, 64, 128 or 256), the first
+    ``whole`` done whole and the others in ``parts`` ranges of the sum; process-wide."""
     _check(_load().hess_set_ffn_schedule(int(edge), int(whole), int(parts)))
 
 
@@ -837,8 +837,8 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: st
 
     ``save``: in which type the pre-activations are kept for it, as for gated_ffn_forward; with torch.int8
     x is kept in 8 bits too (in blocks of 32 columns), and not at all where no weight needs a gradient:
-    the gradients are those at the values so held.  Reverse mode
-    only: dual tensors of forward mode raise NotImplementedError.
+    the gradients are those at the values so held.  Reverse mode only: dual tensors of forward mode raise
+    NotImplementedError.
     """
     _refuse_forward_mode("gated_ffn", x, w_gate, w_up)
     if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
@@ -1070,8 +1070,8 @@ def quantize_int8(x: torch.Tensor, block: int = 0, stream=None) -> Int8Rows:
     ``block=0``: a scale a row, max |x| / 127, and codes rint(127 x / max |x|): the operands of
     int8_matmul, tokens or a weight's output channels.  ``block=32``: a power of two for each 32
     columns, s with 64 <= max |x| / s < 128: checkpoints of activations (33 / 32 bytes a value; half a
-    step off, at most 1 / 128 of the block's largest magnitude, and less than a step past 127.5 of them).  A row (block) with an infinity or NaN
-    stands for NaN.
+    step off, at most 1 / 128 of the block's largest magnitude, and less than a step past 127.5 of them).
+    A row (block) with an infinity or NaN stands for NaN.
     """
     if stream is not None:  # the call, its temporaries and its outputs belong to it
         with torch.cuda.stream(stream):
@@ -1199,7 +1199,8 @@ def int8_linear_backward(dy: torch.Tensor, x: Int8Rows | None, w: Int8Rows | Non
 
     ``x``: the checkpoint that the forward call saved (None if dw is not needed); ``w``: its weights (None
     if dx is not needed).  For 16-bit types xq and wq are rounded to that type before the products, which
-    leaves the results about 1.4 times as far off as their own last rounding; sums are float32.
+    leaves the results about 1.4 times as far off as their own last rounding (without it the products
+    would double; float32 has none); sums are float32.
     """
     if stream is not None:
         with torch.cuda.stream(stream):

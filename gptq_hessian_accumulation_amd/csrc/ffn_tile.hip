@@ -28,8 +28,8 @@
 //
 //  * The pair kept in 8 bits: a block's 32 features lie in four lanes of one row
 //    (two waves' for edge 64), whose largest magnitudes are exchanged; 8192 tokens
-//    at 4096 x 11264, bf16: 1245 us, where no pair takes 1200 to 1250, one in bf16
-//    1230 and one in float32 1290.
+//    at 4096 x 11264, bf16: 1230 to 1260 us, where no pair takes 1200 to 1250, one
+//    in bf16 1230 and one in float32 1290.
 //
 // Measured (bf16 unless said; the card's clock, and with it every long product,
 // varies by a tenth from card to card and over the first passes): forward of

@@ -68,7 +68,10 @@ __global__ void __launch_bounds__(256) ffn_dgu(const typename Elem<DT>::type* dh
 
 // The same from the pair in 8 bits (rows of pair8_cols(f) bytes); workgroups behind
 // its rows restore x.  Bound by its bytes (bf16, 8192 x 11264: 130 us, 5.7 TB/s; with
-// x of 4096 columns 153 us, 5.5 TB/s, where a launch of its own for x took 24).
+// x of 4096 columns 153 to 157 us, 5.4 TB/s, where a launch of its own for x took 24).
+// dg and du are rounded to the operands' type, as from a pair in other types: with
+// the last rounding the gradients are 0.0024 (bf16) or 0.00033 (fp16) from the 64-bit
+// values instead of 0.0017 or 0.00024; without it the products would double.
 template <int DT>
 __global__ void __launch_bounds__(256) ffn_dgu8(const typename Elem<DT>::type* dh, int64_t lddh, const char* pre,
                                                 int64_t ldp, typename Elem<DT>::type* out, int64_t n, int64_t f,

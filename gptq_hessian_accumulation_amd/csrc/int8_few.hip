@@ -1,9 +1,10 @@
 // The product of few int8 rows, both operands straight from memory into
 // v_mfma_i32_16x16x64_i8 (any alignment, no LDS for them, no workspace): a decoding
 // step, bound by the weights' bytes.  A workgroup takes all of K, its waves a share
-// each, and their sums meet in LDS.  One row: 4096 x 11264 11.0 us with its
-// quantization (46 MB of weights: 4.2 TB/s), 10.9 without, where a launch that
-// quantizes the row first adds 3.2.  24 rows at 2560 x 9728: 9.6 us.
+// each, and their sums meet in LDS.  One row: 4096 x 11264 11.0 to 11.6 us with its
+// quantization where the weights come from memory (46 MB: 4.1 TB/s), 9.3 to 9.6 where
+// the last-level cache has them; 10.9 to 11.2 without it, where a launch that
+// quantizes the row first adds 3.2.  24 rows at 2560 x 9728: 8.5 to 9.6 us.
 //
 // Sums are int32 and exact: |a b| <= 2^14 and K < 2^17.  The output takes the
 // sum as a float32 (2^-24), times the two scales, rounded once to its type.

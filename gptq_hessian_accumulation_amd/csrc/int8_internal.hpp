@@ -71,7 +71,9 @@ hipError_t launch_int8_tile(const Int8Gemm& g, int edge, int dtype, hipStream_t 
 // and with tiles, us: 4096 x 2048 8.0 / 12.4, 6144 x 2560 13.7 / 13.8, 4096 x 8192
 // 16.7 / 14.3, 8192 x 1024 13.0 / 14.3, 8192 x 2560 17.2 / 15.0, 8192 x 8192 28.6 /
 // 24.0, 8192 x 16384 38.1 / 41.7, 16384 x 2048 23.8 / 17.3, 16384 x 8192 55.4 / 41.1;
-// 32 rows, 16384 x 8192 35.7 / 41.1.
+// 32 rows, 16384 x 8192 35.7 / 41.1.  (The first number of a product is d, the second
+// f.  The rule goes by d alone, and three of these take the slower way, by 9 to 17%:
+// 4096 x 8192, 8192 x 1024 and 8192 x 16384.)
 inline bool int8_few(int64_t n, int64_t d) { return n <= 32 || (n <= 64 && d < 8192); }
 
 // Copies up to two matrices of rows[m] x cols bytes (row stride ld[m]) to rows of

@@ -12,12 +12,13 @@
 // fp16.
 // A row or block with an infinity or NaN has a NaN scale and codes 0.
 //
-// All bound by their bytes (a large copy reaches 4.9 TB/s on the same card): 16384 x
-// 4096 bf16 to codes 38 us, 5.3 TB/s, a scale a row, and 39 us in blocks; back 36
-// and 40 us; float32 61 and 63 us, back 70 and 93 us.  A row is read once, into
-// registers: rows past 16,384 columns of a workgroup are read twice (512 x 65536 bf16
-// 28 us, 3.6 TB/s).  Calls of a few hundred rows take 2.3 to 4 us, most of it the
-// launch.
+// All bound by their bytes (a large copy reaches 4.9 TB/s on the same card).  16384 x
+// 4096, calls one after another on changing inputs: bf16 to codes 40 us, 5.0 TB/s, a
+// scale a row (46 to 47 us between long products, which leave the caches full and
+// the clock low), 36 us in blocks, back 34 and 39 us; float32 61 and 63 us, back 62
+// to 70 and 87 to 93 us.  A row is read once, into registers: rows past 16,384
+// columns of a workgroup are read twice (512 x 65536 bf16 27 us, 3.7 TB/s).  Calls of
+// a few hundred rows take 3.5 to 4.5 us, most of it the launch.
 
 #include <algorithm>
 
@@ -143,7 +144,12 @@ template <int DT, int Block> __global__ void __launch_bounds__(256) dequantize(I
 }
 
 // The operands of a linear layer's gradients: blockIdx.y 0 and 1 the sets of rows,
-// 2 the copy of dy.
+// 2 the copy of dy.  xq and wq are rounded to dtype, since the matrix instructions
+// take operands of one 16-bit type: gradients are then 0.0023 (bf16) or 0.00029
+// (fp16) from the 64-bit values, where the last rounding alone leaves 0.0017 or
+// 0.00021.  Their remainders as operands of their own would double the products,
+// which are all but 37 of 1,290 us of an 8,192-token backward pass at 4096 x 11264;
+// float32 has no such rounding.
 template <int DT> __global__ void __launch_bounds__(256) grad_operands(GradOperands G) {
   typedef typename Elem<DT>::type E;
   typedef E E8 __attribute__((ext_vector_type(8)));

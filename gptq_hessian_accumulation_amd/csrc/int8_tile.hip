@@ -27,8 +27,9 @@
 // 404 us, 2.7 POPS (library 477).  Matrix cores busy in 65% of the cycles at a
 // clock of 1.8 to 1.9 GHz, LDS in a quarter of them: the rest is the waves' meeting
 // and the reads behind it.  With stages of 64 bytes, a meeting each, and loads three
-// of them ahead: 643 us for the first, 55% busy; 1999 x 2560 x 9728 (edge 128) 68
-// us against 57 to 60.  Small products are bound by a launch's first loads and
+// of them ahead: 643 us against 603 for the first in one trace, 55% busy; 1999 x
+// 2560 x 9728 (edge 128), with the quantization of its rows, 68 us against 57 to 60
+// (53 to 54 without).  Small products are bound by a launch's first loads and
 // outputs: 300 x 704 x 1000 6 us.
 
 #include <algorithm>

@@ -587,10 +587,10 @@ enum { HESS_PREACT_F32 = 16 };
  * 32); h does not change, and the backward pass takes its derivatives at what the
  * codes stand for.  preact is then n rows of hess_gated_ffn_preact_i8_cols(f)
  * bytes: with fq = f rounded up to a multiple of 32, fq codes of g, fq of u (zeros
- * from f on), fq / 32 exponent bytes of g, fq / 32 of u, zeros to the row's end.  Such a forward call
- * needs hess_gated_ffn_i8_workspace(n, d, f, dtype) bytes, takes tiles whatever n is
- * (so that h of few tokens may differ from another call's in its last bit), and
- * has the tiles' rule on alignment. */
+ * from f on), fq / 32 exponent bytes of g, fq / 32 of u, zeros to the row's end.
+ * Such a forward call needs hess_gated_ffn_i8_workspace(n, d, f, dtype) bytes,
+ * takes tiles whatever n is (so that h of few tokens may differ from another
+ * call's in its last bit), and has the tiles' rule on alignment. */
 enum { HESS_PREACT_I8 = 64 };
 int64_t hess_gated_ffn_preact_i8_cols(int64_t f); /* -1 for bad f */
 int64_t hess_gated_ffn_i8_workspace(int64_t n, int64_t d, int64_t f, int dtype); /* -1 for bad arguments */
